@@ -183,6 +183,112 @@ sq_status sq_layernorm_quant(const float *H, const float *gamma, const float *be
                              int8_t *Xq, float *x_scale, void *Xop, int32_t *x_row_l1,
                              void *stream);
 
+/* ---- RMS norm with the residual's addition and the next linear's quantiser -- */
+
+/* A decoder's normalisation in front of an int8 linear, emitting that linear's
+ * smoothed int8 codes as sq_layernorm_quant does for the encoder:
+ *   r[m][j] = fl(H[m][j] + residual[m][j])       (H alone if residual is NULL)
+ *   y[m][j] = fl(fl(r[m][j] * rstd_m) * gamma[j]),
+ *   rstd_m  = RN(1 / sqrt(fl(fl(sum_j r^2 / K) + eps)))   (fp32 sums in a tree;
+ *             0 where that sum and eps are both 0),
+ * then the codes of y exactly as sq_quantize_act (static_scale == 0) or
+ * sq_quantize_act_static (static_scale > 0, finite) would write them for X = y.
+ * H and residual fp32 [M][K]; gamma fp32 [K]; eps >= 0.  R fp32 [M][K]
+ * (nullable): r, the residual stream that goes on; it may be exactly H or
+ * exactly residual.  Y fp32 [M][K] (nullable): y itself.  Arrays 16-byte
+ * aligned; other outputs as sq_quantize_act.  K <= 16384
+ * (SQ_ERR_UNSUPPORTED otherwise). */
+sq_status sq_rmsnorm_quant(const float *H, const float *residual, const float *gamma, float eps,
+                           const float *s, int64_t M, int64_t K, float static_scale, float *R,
+                           float *Y, int8_t *Xq, float *x_scale, void *Xop, int32_t *x_row_l1,
+                           void *stream);
+
+/* ---- Paged key/value cache -------------------------------------------------- */
+
+/* The cache of one layer: k_cache and v_cache, each
+ *   [num_pages][Hkv][page_size][D] of the 16-bit type `cache_type`,
+ * and for a batch of B sequences (device arrays, int32, 4-byte aligned):
+ *   q_start [B + 1]    sequence b's tokens are rows q_start[b] .. q_start[b+1]-1
+ *                      of this call's T rows (non-decreasing; rows outside every
+ *                      sequence are neither read nor written),
+ *   kv_len [B]         its cached tokens, this call's included, so that its
+ *                      i-th token stands at position kv_len[b] - q_len[b] + i,
+ *   block_table [B][max_pages]  the page of positions page_size n ..
+ *                      page_size n + page_size - 1 in column n.
+ * Hq query heads share Hkv key/value heads in groups of G = Hq / Hkv
+ * consecutive ones (Hq a multiple of Hkv, G <= 16, Hq <= 4096).  D is 64 or
+ * 128; page_size 16, 32, 64, 128 or 256.  T, B, max_pages * page_size and
+ * num_pages * Hkv * page_size at most 2^30 (SQ_ERR_UNSUPPORTED beyond).
+ * The contents of the device arrays are not checked on the host; whatever they
+ * hold, no access leaves the arrays (see each function). */
+typedef enum {
+    SQ_CACHE_BF16 = 0,
+    SQ_CACHE_F16 = 1
+} sq_cache_type;
+
+/* Rotation table: table[p][j] = (cos, sin) of p * inv_freq[j], the angle and
+ * its functions in double, rounded once.  inv_freq fp32 [rot / 2] (4-byte
+ * aligned), table fp32 [positions][rot / 2][2] (16-byte aligned); rot a
+ * multiple of 8, at most 1024. */
+sq_status sq_rope_table(const float *inv_freq, int64_t positions, int64_t rot, float *table,
+                        void *stream);
+
+/* Rotates the queries and keys of this call's tokens and appends their keys
+ * and values to the cache.  QKV fp32 [T][(Hq + 2 Hkv) D]: the Q, K and V blocks
+ * of the fused projection (sq_linear_i8's output), head h at columns h D of its
+ * block.  The first `rot` elements of every query and key head are rotated in
+ * pairs (x, y) -> (x cos - y sin, x sin + y cos): elements (j, j + rot/2), or
+ * (2j, 2j + 1) if `interleaved`, with rope[position][j] of sq_rope_table(...,
+ * rope_positions, rot); rot a multiple of 8, at most D, 0 for no rotation (rope
+ * may then be NULL).  Q fp32, rows of ldq floats (ldq >= Hq D, a multiple of 4):
+ * the rotated queries; it may be exactly QKV with ldq = (Hq + 2 Hkv) D (in
+ * place), and otherwise overlaps nothing.  Keys (rotated) and values go to row
+ * position % page_size of their page, rounded once to the cache's type; no
+ * other row of the cache is touched.  A token whose position is negative or has
+ * no row in `rope` gets a zero query row and is not stored; one whose page is
+ * outside the table or [0, num_pages) is not stored.  Two tokens of one call
+ * with the same page and row leave one of the two.
+ * Pointers 16-byte aligned but for the int32 arrays. */
+sq_status sq_kv_append(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                       const float *rope, int64_t rope_positions, int64_t rot, int interleaved,
+                       const int32_t *q_start, const int32_t *kv_len, int64_t B,
+                       const int32_t *block_table, int64_t max_pages, void *k_cache,
+                       void *v_cache, int cache_type, int64_t num_pages, int64_t page_size,
+                       float *Q, int64_t ldq, void *stream);
+
+/* Causal attention of this call's tokens over the cache.  With p the position
+ * of a token of sequence b and K[k], V[k] the cached rows of its key/value head,
+ *   O[t][h D + d] = sum_{k <= p} P[k] V[k][d],   P = softmax_k(scale Q[t][h] . K[k]).
+ * Positions k < prefix_len are read from page prefix_pages[k / page_size] for
+ * every sequence -- a prefix that the batch shares, read and multiplied once for
+ * all of it -- and the others from block_table; prefix_len need not be a
+ * multiple of page_size, 0 means none (prefix_pages may then be NULL).  Entries
+ * of block_table in front of page prefix_len / page_size are not used.
+ * A token with no key at or before its position (kv_len[b] = 0, or more tokens
+ * than kv_len[b]) gets zeros.  Keys whose page entry is outside [0, num_pages)
+ * are left out, as if masked; kv_len is taken as at most max_pages * page_size,
+ * and cache rows at or behind kv_len are not used, whatever they hold.
+ * Q fp32, rows of ldq floats (ldq >= Hq D, a multiple of 4); O fp32 [T][Hq D],
+ * overlapping nothing.  max_q: the most tokens of a sequence; it chooses the
+ * kernel only, results do not depend on it but for rounding.
+ * Queries and probabilities enter the tensor cores as pairs of 16-bit numbers
+ * of the cache's type and products are summed in fp32, as are the softmax's
+ * maxima and sums: O agrees with the exact attention over the stored rows to
+ * about 2^-18 of max |V| (bf16) or 2^-21 (fp16; |Q| at most 65504).
+ * workspace (16-byte aligned, zero-filled once before its first use): at least
+ * sq_paged_attention_workspace_bytes bytes; it serves one call at a time, on
+ * the rules of sq_linear_i8_ws (calls that share one must be ordered; after
+ * SQ_ERR_TIMEOUT zero-fill it again). */
+sq_status sq_paged_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                             int64_t prefix_len, size_t *bytes);
+sq_status sq_paged_attention(const float *Q, int64_t ldq, int64_t T, int64_t Hq, int64_t Hkv,
+                             int64_t D, const void *k_cache, const void *v_cache, int cache_type,
+                             int64_t num_pages, int64_t page_size, const int32_t *block_table,
+                             int64_t max_pages, const int32_t *q_start, const int32_t *kv_len,
+                             int64_t B, int64_t max_q, const int32_t *prefix_pages,
+                             int64_t prefix_len, float scale, float *O, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
 /* ---- INT8 GEMM + fused dequantising epilogue ------------------------------ */
 
 /* acc[m][n] = sum_k Xq[m][k] * Wq[n][k], exact in int32, then the epilogue

@@ -7,6 +7,7 @@ call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -30,6 +31,8 @@ EXPORTS = ("sq_status_string", "sq_version", "sq_operand_bytes", "sq_packed_weig
            "sq_linear_workspace_bytes", "sq_linear_i8_ws", "sq_linear_i8_requant_ws", "sq_linear_i8_static_ws", "sq_static_workspace_reset",
            "sq_static_workspace", "sq_linear_i8_mma_sync", "sq_linear_block_host_scratch_bytes",
            "sq_linear_block_host",
+           "sq_rmsnorm_quant", "sq_rope_table", "sq_kv_append",
+           "sq_paged_attention_workspace_bytes", "sq_paged_attention",
            "sq_check_division", "sq_device_status", "sq_get_device_status")
 
 class LinearLayerC(ctypes.Structure):
@@ -76,6 +79,16 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                 "sq_quantize_act_static": ([vp, vp, i64, i64, f32, vp, vp, vp, vp, vp], i32),
                 "sq_layernorm_quant": ([vp, vp, vp, f32, vp, i64, i64, f32, vp, vp, vp, vp, vp,
                                         vp], i32),
+                "sq_rmsnorm_quant": ([vp, vp, vp, f32, vp, i64, i64, f32, vp, vp, vp, vp, vp, vp,
+                                      vp], i32),
+                "sq_rope_table": ([vp, i64, i64, vp, vp], i32),
+                "sq_kv_append": ([vp, i64, i64, i64, i64, vp, i64, i64, i32, vp, vp, i64, vp, i64,
+                                  vp, vp, i32, i64, i64, vp, i64, vp], i32),
+                "sq_paged_attention_workspace_bytes": ([i64, i64, i64, i64, i64,
+                                                        ctypes.POINTER(ctypes.c_size_t)], i32),
+                "sq_paged_attention": ([vp, i64, i64, i64, i64, i64, vp, vp, i32, i64, i64, vp,
+                                        i64, vp, vp, i64, i64, vp, i64, f32, vp, vp,
+                                        ctypes.c_size_t, vp], i32),
                 "sq_linear_i8": ([vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, vp],
                                  i32),
                 "sq_linear_i8_requant": ([vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp,
@@ -144,6 +157,28 @@ def _need(t: torch.Tensor, dtype, name: str, shape=None):
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+@contextlib.contextmanager
+def _on(t: torch.Tensor, stream=None):
+    """Makes t's device and the given stream (t's device's current one if None)
+    current, so that what a call allocates belongs to the stream that uses it;
+    yields the stream's handle."""
+    if stream is None and t.device.index == torch.cuda.current_device():
+        yield _stream()
+        return
+    with torch.cuda.device(t.device):
+        s = stream if stream is not None else torch.cuda.current_stream()
+        if s.device != t.device:
+            raise ValueError(f"the stream is on {s.device}, the tensors on {t.device}")
+        with torch.cuda.stream(s):
+            yield _stream(s)
+
+
+def _same_device(ref: torch.Tensor, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} must be on {ref.device}, is on {t.device}")
 
 
 def operand_bytes(rows: int, K: int) -> int:
@@ -290,6 +325,204 @@ def layernorm_quant(H: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, ep
                                      float(static_scale), _p(Y), _p(Xq), _p(sx), _p(Xop),
                                      _p(l1), _stream(stream)), "sq_layernorm_quant")
     return Xq, sx, Xop, Y, l1
+
+
+def rmsnorm_quant(H: torch.Tensor, gamma: torch.Tensor, eps: float, s: torch.Tensor,
+                  residual: Optional[torch.Tensor] = None, static_scale: float = 0.0,
+                  want_sum: Optional[bool] = None, want_y: bool = False, want_q: bool = True,
+                  want_op: bool = True, want_l1: bool = False, out=None, stream=None):
+    """RMS norm of H (+ residual) with the next linear's quantiser fused in
+    (dynamic when static_scale is 0); returns (Xq or None, x_scale, Xop or None,
+    Y or None, l1 or None, R or None), R the sum (by default asked for when
+    there is a residual).  `out` may give those six (all but x_scale may be
+    None); its R may be H or the residual itself."""
+    _need(H, torch.float32, "H")
+    M, K = H.shape
+    for t, n in ((gamma, "gamma"), (s, "s")):
+        _need(t, torch.float32, n, (K,))
+    if residual is not None:
+        _need(residual, torch.float32, "residual", (M, K))
+    with _on(H, stream) as st:
+        if out is not None:
+            Xq, sx, Xop, Y, l1, R = out
+            for t, n, dt, shape in ((Xq, "Xq", torch.int8, (M, K)),
+                                    (sx, "x_scale", torch.float32, (M,)),
+                                    (Xop, "Xop", torch.bfloat16, (M, K)),
+                                    (Y, "Y", torch.float32, (M, K)),
+                                    (l1, "l1", torch.int32, (M,)),
+                                    (R, "R", torch.float32, (M, K))):
+                if t is not None:
+                    _need(t, dt, n, shape)
+        else:
+            new = lambda want, dt, *shape: (  # noqa: E731
+                torch.empty(shape, dtype=dt, device=H.device) if want else None)
+            Xq = new(want_q, torch.int8, M, K)
+            sx = new(True, torch.float32, M)
+            Xop = new(want_op, torch.bfloat16, M, K)
+            Y = new(want_y, torch.float32, M, K)
+            l1 = new(want_l1, torch.int32, M)
+            R = new(residual is not None if want_sum is None else want_sum, torch.float32, M, K)
+        _same_device(H, gamma=gamma, s=s, residual=residual, Xq=Xq, x_scale=sx, Xop=Xop, Y=Y,
+                     l1=l1, R=R)
+        _check(load().sq_rmsnorm_quant(_p(H), _p(residual), _p(gamma), float(eps), _p(s), M, K,
+                                       float(static_scale), _p(R), _p(Y), _p(Xq), _p(sx), _p(Xop),
+                                       _p(l1), st), "sq_rmsnorm_quant")
+    return Xq, sx, Xop, Y, l1, R
+
+
+def rope_table(inv_freq: torch.Tensor, positions: int, out=None, stream=None) -> torch.Tensor:
+    """(cos, sin) of p * inv_freq[j] for p < positions: fp32 [positions, n, 2]
+    for n inverse frequencies (n a multiple of 4), for kv_append."""
+    _need(inv_freq, torch.float32, "inv_freq")
+    n = inv_freq.numel()
+    with _on(inv_freq, stream) as st:
+        if out is None:
+            out = torch.empty(int(positions), n, 2, dtype=torch.float32, device=inv_freq.device)
+        _need(out, torch.float32, "table", (int(positions), n, 2))
+        _same_device(inv_freq, table=out)
+        _check(load().sq_rope_table(_p(inv_freq), int(positions), 2 * n, _p(out), st),
+               "sq_rope_table")
+    return out
+
+
+CACHE_BF16, CACHE_F16 = 0, 1
+_CACHE_TYPES = {torch.bfloat16: CACHE_BF16, torch.float16: CACHE_F16}
+
+
+def empty_kv_cache(num_pages: int, kv_heads: int, page_size: int, D: int,
+                   dtype=torch.bfloat16, device="cuda"):
+    """(k_cache, v_cache) of one layer, [num_pages, kv_heads, page_size, D]."""
+    return tuple(torch.empty(num_pages, kv_heads, page_size, D, dtype=dtype, device=device)
+                 for _ in range(2))
+
+
+def _rows_of(t: torch.Tensor, cols: int, name: str, rows: Optional[int] = None) -> int:
+    """A 2-D fp32 view of `cols` columns whose rows may lie apart (a block of
+    columns of a wider matrix); returns the row stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.float32:
+        raise ValueError(f"{name} must be {torch.float32}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must have shape ({'T' if rows is None else rows}, {cols}), "
+                         f"got {tuple(t.shape)}")
+    if t.shape[0] <= 1:  # a single row's stride says nothing
+        if t.shape[0] == 1 and cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}'s columns must be contiguous")
+        return max(cols, 4)
+    if (cols > 1 and t.stride(1) != 1) or t.stride(0) < cols:
+        raise ValueError(f"{name}'s columns must be contiguous and its rows apart")
+    return t.stride(0)
+
+
+def _need_paged(k_cache, v_cache, block_table, q_start, kv_len):
+    """Checks the cache and the batch's tables; returns (type, pages, Hkv, page size, D, B,
+    table width)."""
+    if k_cache.dtype not in _CACHE_TYPES:
+        raise ValueError(f"k_cache must be bfloat16 or float16, got {k_cache.dtype}")
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must have shape (num_pages, kv_heads, page_size, D)")
+    _need(k_cache, k_cache.dtype, "k_cache")
+    _need(v_cache, k_cache.dtype, "v_cache", k_cache.shape)
+    if kv_len.dim() != 1:
+        raise ValueError("kv_len must have one dimension")
+    B = kv_len.shape[0]
+    _need(kv_len, torch.int32, "kv_len")
+    _need(q_start, torch.int32, "q_start", (B + 1,))
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must have shape ({B}, max_pages)")
+    _need(block_table, torch.int32, "block_table")
+    _same_device(k_cache, v_cache=v_cache, block_table=block_table, q_start=q_start,
+                 kv_len=kv_len)
+    pages, Hkv, page_size, D = k_cache.shape
+    return _CACHE_TYPES[k_cache.dtype], pages, Hkv, page_size, D, B, block_table.shape[1]
+
+
+def kv_append(QKV: torch.Tensor, Hq: int, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              block_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+              rope: Optional[torch.Tensor] = None, interleaved: bool = False,
+              q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rotates the queries and keys of the fused projection's output QKV
+    [T, (Hq + 2 Hkv) * D] and appends keys and values to the paged cache;
+    returns the rotated queries [T, Hq * D].  rope: rope_table's [positions, n,
+    2], None for no rotation.  q_out may be the view QKV[:, :Hq * D] (in place)."""
+    ctype, pages, Hkv, page_size, D, B, width = _need_paged(k_cache, v_cache, block_table,
+                                                            q_start, kv_len)
+    _need(QKV, torch.float32, "QKV")
+    if QKV.dim() != 2 or QKV.shape[1] != (Hq + 2 * Hkv) * D:
+        raise ValueError(f"QKV must have shape (T, {(Hq + 2 * Hkv) * D}), got {tuple(QKV.shape)}")
+    T = QKV.shape[0]
+    rot = positions = 0
+    if rope is not None:
+        if rope.dim() != 3 or rope.shape[2] != 2:
+            raise ValueError("rope must have shape (positions, n, 2)")
+        _need(rope, torch.float32, "rope")
+        positions, rot = rope.shape[0], 2 * rope.shape[1]
+    with _on(QKV, stream) as st:
+        if q_out is None:
+            q_out = torch.empty(T, Hq * D, dtype=torch.float32, device=QKV.device)
+        ldq = _rows_of(q_out, Hq * D, "q_out", T)
+        _same_device(QKV, k_cache=k_cache, rope=rope, q_out=q_out)
+        _check(load().sq_kv_append(_p(QKV), T, Hq, Hkv, D, _p(rope), positions, rot,
+                                   int(bool(interleaved)), _p(q_start), _p(kv_len), B,
+                                   _p(block_table), width, _p(k_cache), _p(v_cache), ctype, pages,
+                                   page_size, _p(q_out), ldq, st), "sq_kv_append")
+    return q_out
+
+
+def paged_attention_workspace_bytes(T: int, Hq: int, Hkv: int, D: int,
+                                    prefix_len: int = 0) -> int:
+    """Bytes of paged_attention's workspace for T rows (see empty_workspace) on
+    the current device."""
+    n = ctypes.c_size_t(0)
+    _check(load().sq_paged_attention_workspace_bytes(T, Hq, Hkv, D, prefix_len, ctypes.byref(n)),
+           "sq_paged_attention_workspace_bytes")
+    return int(n.value)
+
+
+def paged_attention(Q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+                    max_q: Optional[int] = None, prefix_pages: Optional[torch.Tensor] = None,
+                    prefix_len: int = 0, scale: Optional[float] = None,
+                    workspace: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal attention of the rows Q [T, Hq * D] (kv_append's queries; rows may
+    lie apart) over the paged cache -> [T, Hq * D].  Positions below prefix_len
+    come from prefix_pages for every sequence.  max_q: the most tokens of a
+    sequence (T if not given).  workspace: a zero-filled uint8 tensor that one
+    call at a time uses (empty_workspace(paged_attention_workspace_bytes(...)));
+    a fresh one is made if None.  With `out`, rows of no sequence are left as
+    they are; without it they are zeros."""
+    ctype, pages, Hkv, page_size, D, B, width = _need_paged(k_cache, v_cache, block_table,
+                                                            q_start, kv_len)
+    if Q.dim() != 2 or Q.shape[1] % D != 0 or Q.shape[1] == 0:
+        raise ValueError(f"Q must have shape (T, heads * {D}), got {tuple(Q.shape)}")
+    T, Hq = Q.shape[0], Q.shape[1] // D
+    ldq = _rows_of(Q, Hq * D, "Q")
+    if prefix_len and prefix_pages is None:
+        raise ValueError("prefix_len without prefix_pages")
+    if prefix_pages is not None:
+        _need(prefix_pages, torch.int32, "prefix_pages")
+        if prefix_pages.dim() != 1 or prefix_pages.shape[0] * page_size < prefix_len:
+            raise ValueError(f"prefix_pages must name every page of {prefix_len} positions")
+    if scale is None:
+        scale = 1.0 / float(D) ** 0.5
+    with _on(Q, stream) as st:
+        if out is None:
+            out = torch.zeros(T, Hq * D, dtype=torch.float32, device=Q.device)
+        _need(out, torch.float32, "out", (T, Hq * D))
+        if workspace is None:
+            workspace = empty_workspace(
+                paged_attention_workspace_bytes(T, Hq, Hkv, D, prefix_len), Q.device)
+        wp, wn = _workspace(workspace)
+        _same_device(Q, k_cache=k_cache, prefix_pages=prefix_pages, workspace=workspace, out=out)
+        _check(load().sq_paged_attention(_p(Q), ldq, T, Hq, Hkv, D, _p(k_cache), _p(v_cache),
+                                         ctype, pages, page_size, _p(block_table), width,
+                                         _p(q_start), _p(kv_len), B,
+                                         T if max_q is None else int(max_q), _p(prefix_pages),
+                                         int(prefix_len), float(scale), _p(out), wp, wn, st),
+               "sq_paged_attention")
+    return out
 
 
 def _out(Xa, Wa, mode, out):

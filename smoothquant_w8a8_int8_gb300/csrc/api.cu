@@ -82,6 +82,28 @@ sq_status check_quant_args(const float *A, const float *s, int64_t rows, int64_t
     return SQ_OK;
 }
 
+// Sizes of the paged cache and of the rows that go with it.
+sq_status check_paged_shape(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int cache_type,
+                            int64_t num_pages, int64_t page_size, int64_t B, int64_t max_pages,
+                            int64_t ldq) {
+    if (T < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || num_pages < 0 || B < 0 || max_pages < 0)
+        return SQ_ERR_INVALID_ARG;
+    if (cache_type != SQ_CACHE_BF16 && cache_type != SQ_CACHE_F16) return SQ_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return SQ_ERR_UNSUPPORTED;
+    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 &&
+        page_size != 256)
+        return SQ_ERR_UNSUPPORTED;
+    if (Hq % Hkv != 0) return SQ_ERR_INVALID_ARG;
+    if (Hq > 4096 || Hq / Hkv > 16) return SQ_ERR_UNSUPPORTED;
+    if (ldq < Hq * D) return SQ_ERR_INVALID_ARG;
+    if (ldq % 4 != 0) return SQ_ERR_ALIGNMENT;
+    // token, sequence, key and cache-row numbers are 32-bit; element offsets are not
+    const int64_t lim = (int64_t)1 << 30;
+    if (T > lim || B > lim || max_pages > lim / page_size || num_pages > lim / (Hkv * page_size))
+        return SQ_ERR_UNSUPPORTED;
+    return SQ_OK;
+}
+
 }  // namespace
 
 namespace sq {
@@ -348,6 +370,107 @@ sq_status sq_layernorm_quant(const float *H, const float *gamma, const float *be
                                   static_cast<__nv_bfloat16 *>(Xop), x_row_l1, as_stream(stream));
 }
 
+sq_status sq_rmsnorm_quant(const float *H, const float *residual, const float *gamma, float eps,
+                           const float *s, int64_t M, int64_t K, float static_scale, float *R,
+                           float *Y, int8_t *Xq, float *x_scale, void *Xop, int32_t *x_row_l1,
+                           void *stream) {
+    if (!(eps >= 0.0f) || !(eps <= 3.4028234663852886e38f)) return SQ_ERR_INVALID_ARG;
+    if (!(static_scale >= 0.0f) || !(static_scale <= 3.4028234663852886e38f))
+        return SQ_ERR_INVALID_ARG;
+    sq_status rc = check_quant_args(H, s, M, K, Xq, x_scale, Xop);
+    if (rc != SQ_OK) return rc;
+    if (M == 0) return SQ_OK;
+    if (!gamma) return SQ_ERR_INVALID_ARG;
+    if (!aligned16(gamma) || (residual && !aligned16(residual)) || (R && !aligned16(R)) ||
+        (Y && !aligned16(Y)) || (x_row_l1 && !aligned4(x_row_l1)))
+        return SQ_ERR_ALIGNMENT;
+    if (K > 16384) return SQ_ERR_UNSUPPORTED;
+    if ((rc = require_sm103()) != SQ_OK) return rc;
+    return launch_rmsnorm_quant(H, residual, gamma, eps, s, M, K, static_scale, R, Y, Xq, x_scale,
+                                static_cast<__nv_bfloat16 *>(Xop), x_row_l1, as_stream(stream));
+}
+
+sq_status sq_rope_table(const float *inv_freq, int64_t positions, int64_t rot, float *table,
+                        void *stream) {
+    if (positions < 0 || rot < 0) return SQ_ERR_INVALID_ARG;
+    if (rot % 8 != 0) return SQ_ERR_ALIGNMENT;
+    if (positions > (int64_t)1 << 31 || rot > 1024) return SQ_ERR_UNSUPPORTED;
+    if (positions == 0 || rot == 0) return SQ_OK;
+    if (!inv_freq || !table) return SQ_ERR_INVALID_ARG;
+    if (!aligned4(inv_freq) || !aligned16(table)) return SQ_ERR_ALIGNMENT;
+    sq_status rc = require_sm103();
+    if (rc != SQ_OK) return rc;
+    return launch_rope_table(inv_freq, positions, rot, table, as_stream(stream));
+}
+
+sq_status sq_kv_append(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                       const float *rope, int64_t rope_positions, int64_t rot, int interleaved,
+                       const int32_t *q_start, const int32_t *kv_len, int64_t B,
+                       const int32_t *block_table, int64_t max_pages, void *k_cache,
+                       void *v_cache, int cache_type, int64_t num_pages, int64_t page_size,
+                       float *Q, int64_t ldq, void *stream) {
+    sq_status rc = check_paged_shape(T, Hq, Hkv, D, cache_type, num_pages, page_size, B,
+                                     max_pages, ldq);
+    if (rc != SQ_OK) return rc;
+    if (rot < 0 || rot > D || rope_positions < 0) return SQ_ERR_INVALID_ARG;
+    if (rot % 8 != 0) return SQ_ERR_ALIGNMENT;
+    if (T == 0 || B == 0) return SQ_OK;
+    if (num_pages == 0 || !QKV || !q_start || !kv_len || !block_table || !k_cache || !v_cache || !Q ||
+        (rot > 0 && !rope))
+        return SQ_ERR_INVALID_ARG;
+    if (!aligned16(QKV) || !aligned16(Q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        (rot > 0 && !aligned16(rope)) || !aligned4(q_start) || !aligned4(kv_len) ||
+        !aligned4(block_table))
+        return SQ_ERR_ALIGNMENT;
+    if ((rc = require_sm103()) != SQ_OK) return rc;
+    return launch_kv_append(QKV, T, Hq, Hkv, D, rope, rope_positions, rot, interleaved ? 1 : 0,
+                            q_start, kv_len, B, block_table, max_pages, k_cache, v_cache,
+                            cache_type, num_pages, page_size, Q, ldq, as_stream(stream));
+}
+
+sq_status sq_paged_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                             int64_t prefix_len, size_t *bytes) {
+    if (!bytes) return SQ_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (prefix_len < 0) return SQ_ERR_INVALID_ARG;
+    sq_status rc = check_paged_shape(T, Hq, Hkv, D, SQ_CACHE_BF16, 1, 16, 0, 0, Hq * D);
+    if (rc != SQ_OK) return rc;
+    if (T == 0) return SQ_OK;
+    return paged_workspace_bytes(T, Hq, D, prefix_len, bytes);
+}
+
+sq_status sq_paged_attention(const float *Q, int64_t ldq, int64_t T, int64_t Hq, int64_t Hkv,
+                             int64_t D, const void *k_cache, const void *v_cache, int cache_type,
+                             int64_t num_pages, int64_t page_size, const int32_t *block_table,
+                             int64_t max_pages, const int32_t *q_start, const int32_t *kv_len,
+                             int64_t B, int64_t max_q, const int32_t *prefix_pages,
+                             int64_t prefix_len, float scale, float *O, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+    sq_status rc = check_paged_shape(T, Hq, Hkv, D, cache_type, num_pages, page_size, B,
+                                     max_pages, ldq);
+    if (rc != SQ_OK) return rc;
+    if (!(scale == scale) || !(fabsf(scale) <= 3.4028234663852886e38f)) return SQ_ERR_INVALID_ARG;
+    if (max_q < 0 || prefix_len < 0) return SQ_ERR_INVALID_ARG;
+    if (prefix_len > (int64_t)1 << 30) return SQ_ERR_UNSUPPORTED;
+    if (T == 0 || B == 0) return SQ_OK;
+    if (num_pages == 0 || !Q || !q_start || !kv_len || !block_table || !k_cache || !v_cache || !O || !workspace ||
+        (prefix_len > 0 && !prefix_pages))
+        return SQ_ERR_INVALID_ARG;
+    if (!aligned16(Q) || !aligned16(O) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !aligned16(workspace) || !aligned4(q_start) || !aligned4(kv_len) ||
+        !aligned4(block_table) || (prefix_len > 0 && !aligned4(prefix_pages)))
+        return SQ_ERR_ALIGNMENT;
+    if ((rc = require_sm103()) != SQ_OK) return rc;
+    size_t need = 0;
+    if ((rc = paged_workspace_bytes(T, Hq, D, prefix_len, &need)) != SQ_OK) return rc;
+    if (workspace_bytes < need) return SQ_ERR_INVALID_ARG;
+    const PagedCall c = {Q,         ldq,         T,         Hq,      Hkv,          D,
+                         k_cache,   v_cache,     cache_type, num_pages, page_size,  block_table,
+                         max_pages, q_start,     kv_len,    B,       max_q,        prefix_pages,
+                         prefix_len, scale,      O,         workspace, workspace_bytes};
+    return launch_paged_attention(c, as_stream(stream));
+}
+
 sq_status sq_linear_i8(const void *Xop, const float *x_scale, const int32_t *x_row_l1,
                        const void *Wop, const float *w_scale, const int32_t *w_row_l1,
                        const float *bias, const float *residual, int64_t M, int64_t N, int64_t K,
@@ -463,7 +586,10 @@ sq_status sq_device_status(void *stream) {
     if (rq == SQ_ERR_CUDA) return rq;
     const sq_status ra = attention_take_error(as_stream(stream));
     if (ra == SQ_ERR_CUDA) return ra;
+    const sq_status rp = paged_take_error(as_stream(stream));
+    if (rp == SQ_ERR_CUDA) return rp;
     sq_status rc = gemm_tc_take_error(as_stream(stream));
+    if (rc == SQ_OK) rc = rp;
     if (rc == SQ_OK) rc = rq;
     if (rc == SQ_OK) rc = ra;
     if (rc == SQ_ERR_TIMEOUT) {

@@ -1,0 +1,128 @@
+// Host side of the attention over the paged cache: which kernel takes a call,
+// and its workspace.
+#include "paged.cuh"
+
+#include <algorithm>
+#include <mutex>
+
+namespace sq {
+namespace {
+
+__device__ unsigned int g_paged_error;
+
+constexpr int64_t kCounterBytes = 16384;
+constexpr int64_t kPieceRows = 256;  // rows of a partial result, the largest kernel's
+
+// Device address of the error word, looked up on a device's first call.
+sq_status error_word(int device, unsigned **out) {
+    static std::mutex mu;
+    static unsigned *known[64] = {};
+    std::lock_guard<std::mutex> lock(mu);
+    unsigned *&p = known[device & 63];
+    if (!p) {
+        void *v = nullptr;
+        if (cudaGetSymbolAddress(&v, g_paged_error) != cudaSuccess || !v) {
+            (void)cudaGetLastError();
+            return SQ_ERR_CUDA;
+        }
+        p = static_cast<unsigned *>(v);
+    }
+    *out = p;
+    return SQ_OK;
+}
+
+int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+// counters | partial maxima and sums | partial outputs | the prefix's maxima
+// and sums | the prefix's outputs
+sq_status paged_workspace_bytes(int64_t T, int64_t Hq, int64_t D, int64_t prefix_len,
+                                size_t *bytes) {
+    DeviceInfo di;
+    sq_status rc = device_info(&di);
+    if (rc != SQ_OK) return rc;
+    const int64_t rows = 2 * (int64_t)di.sms * kPieceRows;
+    int64_t n = kCounterBytes + up256(rows * 8) + up256(rows * D * 4);
+    if (prefix_len > 0) n += up256(T * Hq * 8) + up256(T * Hq * D * 4);
+    *bytes = (size_t)n;
+    return SQ_OK;
+}
+
+sq_status launch_paged_attention(const PagedCall &c, cudaStream_t st) {
+    DeviceInfo di;
+    sq_status rc = device_info(&di);
+    if (rc != SQ_OK) return rc;
+    if (di.sms * 2 * 4 > kCounterBytes) return SQ_ERR_UNSUPPORTED;
+    PagedArgs a = {};
+    if ((rc = error_word(di.device, &a.error)) != SQ_OK) return rc;
+    a.Q = c.Q;
+    a.O = c.O;
+    a.ldq = c.ldq;
+    a.block_table = c.block_table;
+    a.q_start = c.q_start;
+    a.kv_len = c.kv_len;
+    a.prefix_pages = c.prefix_pages;
+    a.max_pages = c.max_pages;
+    char *w = static_cast<char *>(c.workspace);
+    const int64_t rows = 2 * (int64_t)di.sms * kPieceRows;
+    a.counters = reinterpret_cast<unsigned *>(w);
+    w += kCounterBytes;
+    a.part_ml = reinterpret_cast<float2 *>(w);
+    w += up256(rows * 8);
+    a.part_o = reinterpret_cast<float *>(w);
+    w += up256(rows * c.D * 4);
+    if (c.prefix_len > 0) {
+        a.prefix_ml = reinterpret_cast<float2 *>(w);
+        w += up256(c.T * c.Hq * 8);
+        a.prefix_o = reinterpret_cast<float *>(w);
+    }
+    a.T = (int)c.T;
+    a.B = (int)c.B;
+    a.Hq = (int)c.Hq;
+    a.Hkv = (int)c.Hkv;
+    a.G = (int)(c.Hq / c.Hkv);
+    a.num_pages = (int)c.num_pages;
+    a.page_shift = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6
+                   : c.page_size == 128 ? 7 : 8;
+    a.prefix_len = (int)c.prefix_len;
+    a.cap = (int)(c.max_pages * c.page_size);
+    a.scale = fabsf(c.scale) * 1.4426950408889634f;
+    a.sign = c.scale < 0.0f ? -1.0f : 1.0f;
+    const bool bf16 = c.cache_type == SQ_CACHE_BF16;
+    const int64_t cache_rows = c.num_pages * c.Hkv * c.page_size;
+    const int bx = (int)std::min<int64_t>(c.page_size, 64);
+    CUtensorMap mk, mv;
+    if ((rc = make_map_16(&mk, bf16, c.k_cache, cache_rows, c.D, bx, 64)) != SQ_OK ||
+        (rc = make_map_16(&mv, bf16, c.v_cache, cache_rows, c.D, bx, 64)) != SQ_OK)
+        return rc;
+    for (int phase = c.prefix_len > 0 ? 1 : 0; phase >= 0; --phase) {
+        a.prefix_phase = phase;
+        const int64_t most = (phase ? c.T : c.max_q) * a.G;
+        const int rg = most <= 8 ? 1 : 2;
+        a.tpt = std::max(1, rg * 8 / a.G);
+        a.kstart = phase ? 0 : a.prefix_len / 64 * 64;
+        if ((rc = launch_paged_rows(a, mk, mv, (int)c.D, bf16, rg, bx, di.sms, st)) != SQ_OK)
+            return rc;
+    }
+    return SQ_OK;
+}
+
+sq_status paged_take_error(cudaStream_t st) {
+    unsigned int word = 0;
+    if (cudaMemcpyFromSymbolAsync(&word, g_paged_error, sizeof(word), 0, cudaMemcpyDeviceToHost,
+                                  st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return SQ_ERR_CUDA;
+    if (word != 0) {
+        const unsigned int zero = 0;
+        if (cudaMemcpyToSymbolAsync(g_paged_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice,
+                                    st) != cudaSuccess ||
+            cudaStreamSynchronize(st) != cudaSuccess)
+            return SQ_ERR_CUDA;
+        return SQ_ERR_TIMEOUT;
+    }
+    return SQ_OK;
+}
+
+}  // namespace sq

@@ -1,0 +1,222 @@
+// The line of work of the attention kernels over the paged cache, and its
+// division over the CTAs.  Host and device, so that it can be checked without
+// a GPU.
+//
+// An item is a tile of query rows (tokens x heads of one key/value
+// head's group) of one sequence and one key/value head; its keys are cut into
+// tiles of KT.  All (item, key tile) pairs stand in one line -- sequences,
+// then row tiles, then key/value heads, then key tiles -- and CTA c of n takes
+// pairs [c W / n, (c + 1) W / n): every CTA has the same share whatever the
+// lengths, known only on the device, are.  An item that lies in several CTAs'
+// shares leaves one partial result (row maximum, sum, unnormalised output) per
+// CTA in the workspace; the CTA that arrives last (a counter) joins them in
+// the order of the line, so that the result does not depend on who is last.
+#pragma once
+#include <cuda_runtime.h>
+#include <cstdint>
+
+namespace sq {
+
+struct PagedArgs {
+    const float *Q;      // [T] rows of ldq floats, head h at column h D
+    float *O;            // [T][Hq D]
+    int64_t ldq;
+    const int *block_table, *q_start, *kv_len, *prefix_pages;
+    int64_t max_pages;
+    float *prefix_o;     // [T Hq][D] unnormalised output over the prefix
+    float2 *prefix_ml;   // [T Hq] its row maximum (log2 units) and sum
+    unsigned *counters;  // zero between launches
+    float *part_o;       // [2 CTAs][rows][D] partial outputs, two slots per CTA
+    float2 *part_ml;     // [2 CTAs][rows]
+    unsigned *error;     // the library's error word
+    int T, B, Hq, Hkv, G;
+    int tpt;             // tokens per row tile
+    int num_pages, page_shift;
+    int prefix_len;
+    int kstart;          // first key of the suffix's first key tile
+    int cap;             // keys a row of the page table can name
+    float scale;         // |scale| log2 e; the sign is folded into the queries
+    float sign;
+    int prefix_phase;    // 1: every token over the prefix, into prefix_o / prefix_ml
+};
+
+namespace {
+
+#define SQ_HD __host__ __device__ __forceinline__
+
+SQ_HD int load_int(const int *p) {
+#ifdef __CUDA_ARCH__
+    return __ldg(p);
+#else
+    return *p;
+#endif
+}
+SQ_HD int at_most(int a, int b) { return a < b ? a : b; }
+SQ_HD int at_least(int a, int b) { return a > b ? a : b; }
+
+struct Seq {
+    int q0, qlen, kv;  // first token, tokens, keys after the append
+};
+// The device arrays are taken as they come: offsets clamped into [0, T] and
+// made non-decreasing, lengths into [0, cap].
+SQ_HD Seq load_seq(const PagedArgs &a, int b) {
+    Seq s;
+    const int e = a.prefix_phase ? a.B : b + 1;
+    s.q0 = at_most(at_least(load_int(a.q_start + (a.prefix_phase ? 0 : b)), 0), a.T);
+    s.qlen = at_most(at_least(load_int(a.q_start + e), s.q0), a.T) - s.q0;
+    s.kv = a.prefix_phase ? a.prefix_len : at_most(at_least(load_int(a.kv_len + b), 0), a.cap);
+    return s;
+}
+SQ_HD int row_tiles(const PagedArgs &a, const Seq &s) {
+    return (s.qlen + a.tpt - 1) / a.tpt;
+}
+// One past the last key that any row of row tile j attends to (suffix: causal;
+// a tile none of whose rows has a key gets one at or below zero).
+SQ_HD int tile_keys(const PagedArgs &a, const Seq &s, int j) {
+    return a.prefix_phase ? s.kv : s.kv - s.qlen + at_most(s.qlen, (j + 1) * a.tpt);
+}
+template <int KT>
+SQ_HD int key_tiles(const PagedArgs &a, const Seq &s, int j) {
+    const int n = tile_keys(a, s, j) - a.kstart;
+    return n <= KT ? 1 : (n + KT - 1) / KT;  // at least one: its rows are written
+}
+// sum of floor((p i + q) / m) over i < n; p, q >= 0, m > 0.  The sum counts
+// lattice points below a line: whole parts of p / m and q / m are summed in
+// closed form, and what is left is the same sum with the axes exchanged.
+SQ_HD int64_t floor_sum(int64_t n, int64_t m, int64_t p, int64_t q) {
+    int64_t total = 0;
+    while (n > 0) {
+        total += (n - 1) * n / 2 * (p / m) + n * (q / m);
+        p %= m;
+        q %= m;
+        const int64_t top = p * n + q;
+        if (top < m) break;
+        n = top / m;
+        q = top % m;
+        const int64_t was = m;
+        m = p;
+        p = was;
+    }
+    return total;
+}
+// key tiles of the first J row tiles
+template <int KT>
+SQ_HD int64_t key_tiles_before(const PagedArgs &a, const Seq &s, int J) {
+    if (a.prefix_phase) return (int64_t)J * key_tiles<KT>(a, s, 0);
+    const int tiles = row_tiles(a, s);
+    const int whole = at_most(J, tiles - 1);  // the last row tile may hold fewer tokens
+    if (whole <= 0) return J > 0 ? key_tiles<KT>(a, s, J - 1) : 0;
+    const int64_t base = s.kv - s.qlen - a.kstart;
+    // row tiles whose keys fit one key tile: base + (j + 1) tpt <= KT
+    int64_t ones = KT - base < 0 ? 0 : (KT - base) / a.tpt;
+    ones = ones < whole ? ones : whole;
+    int64_t sum = ones + floor_sum(whole - ones, KT, a.tpt, base + (ones + 1) * a.tpt + KT - 1);
+    if (J > whole) sum += key_tiles<KT>(a, s, J - 1);
+    return sum;
+}
+
+// Where a CTA's share starts.
+struct Share {
+    int64_t total;       // W
+    int64_t begin, end;  // this CTA's pairs
+    int64_t seq_begin;   // the line's position of sequence `seq`
+    int seq;
+    int ctas;            // CTAs that take a share
+};
+SQ_HD int64_t share_begin(int64_t total, int ctas, int c) {
+    return total * c / ctas;
+}
+// the CTA whose share holds position x
+SQ_HD int share_of(int64_t total, int ctas, int64_t x) {
+    return (int)(((x + 1) * ctas - 1) / total);
+}
+
+// A CTA's piece of an item, as its producer hands it to the other warps.
+struct Piece {
+    int tok0, ntok;     // tokens of the row tile
+    int head;           // key/value head
+    int pos0;           // position of token tok0 (suffix)
+    int key0, ntiles;   // first key and key tiles of the piece
+    int keys;           // one past the last key any row attends to
+    int seq;
+    int first_cta, npieces;  // npieces = 1: the whole item
+    int slot;           // this CTA's partial slot
+    int stop;           // no further piece
+};
+
+// Walks the pieces of a CTA's share.
+template <int KT>
+struct Walk {
+    int64_t at, end;  // position, end of the share
+    int b, j, h, k;
+    Seq s;
+    int tiles, nk;
+    int64_t before;  // key tiles of the sequence's row tiles before j
+
+    SQ_HD void enter(const PagedArgs &a) {
+        s = load_seq(a, b);
+        tiles = row_tiles(a, s);
+    }
+    SQ_HD void start(const PagedArgs &a, const Share &sh) {
+        at = sh.begin;
+        end = sh.end;
+        if (at >= end) return;
+        b = sh.seq;
+        enter(a);
+        const int64_t rem = at - sh.seq_begin;
+        int lo = 0, hi = tiles - 1;  // the last row tile that starts at or before rem
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (a.Hkv * key_tiles_before<KT>(a, s, mid) <= rem) lo = mid;
+            else hi = mid - 1;
+        }
+        j = lo;
+        before = key_tiles_before<KT>(a, s, j);
+        nk = key_tiles<KT>(a, s, j);
+        const int64_t r = rem - a.Hkv * before;
+        h = (int)(r / nk);
+        k = (int)(r % nk);
+    }
+    // the next piece, or false at the end of the share
+    SQ_HD bool next(const PagedArgs &a, const Share &sh, Piece &p) {
+        if (at >= end) return false;
+        const int64_t left = end - at;
+        const int take = left < nk - k ? (int)left : nk - k;
+        const int64_t s0 = at - k;
+        p.tok0 = s.q0 + j * a.tpt;
+        p.ntok = at_most(a.tpt, s.qlen - j * a.tpt);
+        p.head = h;
+        p.pos0 = s.kv - s.qlen + j * a.tpt;
+        p.key0 = a.kstart + k * KT;
+        p.ntiles = take;
+        p.keys = tile_keys(a, s, j);
+        p.seq = b;
+        p.first_cta = share_of(sh.total, sh.ctas, s0);
+        p.npieces = share_of(sh.total, sh.ctas, s0 + nk - 1) - p.first_cta + 1;
+        p.slot = k == 0 ? 1 : 0;  // begun here: slot 1; begun before: slot 0
+        p.stop = 0;
+        at += take;
+        k += take;
+        if (k == nk) {
+            k = 0;
+            if (++h == a.Hkv) {
+                h = 0;
+                before += nk;
+                ++j;
+                if (j == tiles && at < end) {
+                    do {  // the next sequence with a row
+                        ++b;
+                        enter(a);
+                    } while (tiles == 0 && b < a.B - 1);
+                    j = 0;
+                    before = 0;
+                }
+                if (j < tiles) nk = key_tiles<KT>(a, s, j);
+            }
+        }
+        return true;
+    }
+};
+
+}  // namespace
+}  // namespace sq

@@ -1,0 +1,260 @@
+// Root-mean-square norm of a residual stream with the residual's addition and
+// the next linear's activation quantiser fused in: the decoder's counterpart
+// of the encoder's LayerNorm + quantiser.
+//
+// Per row m of H fp32 [M][K] (and residual R0, if given):
+//   r_j = fl(H_j + R0_j)                  (stored to R when asked for)
+//   ms  = fl(sum_j r_j^2 / K)             (fp32 sums in a tree)
+//   y_j = fl(fl(r_j * rstd) * gamma_j),   rstd = RN(1 / sqrt(fl(ms + eps)))
+// and the codes of y as the activation quantiser states them: v = fl(y / s),
+// scale = fl(max|v| / 127) or the given one, code = round-half-even(fl(v / scale)).
+// The row stays in registers from the one read of H and the residual to the
+// codes: 8 bytes read and 4 + 2 written per element with the sum and the
+// operand asked for, which is what bounds the kernel.
+#include "row_codes.cuh"
+
+#include <algorithm>
+#include <mutex>
+
+namespace sq {
+namespace {
+
+// rows of up to 4096 elements: 256 threads of 4 float4; up to 8192: 8 float4;
+// up to 16384: 512 threads of 8 float4
+constexpr int kMaxRow = 16384;
+
+// A group of tpr threads owns a row.  STATIC: the given scale; otherwise the
+// row's own.  The smoothing factors, negated, and their reciprocals stand in
+// shared-memory tables, and the codes come from p = RN(RN(y RN(1/s)) RN(1/scale))
+// with the elements within 2^-14 of a half-integer on IEEE divisions: the same
+// codes as the division's (p is within 4.2e-5 of fl(fl(y/s)/scale) for
+// |quotient| <= 127.0001).  A row whose maximum is NaN or outside
+// [2^-60, 2^100], and every row when a static scale lies outside [2^-60, 2^60]
+// (fast == 0), takes IEEE divisions throughout.
+template <bool STATIC, int VPT, int NT>
+__global__ void __launch_bounds__(NT, VPT == 4 ? 4 : 512 / NT) rmsnorm_quant_kernel(
+    const float *H, const float *residual, const float *__restrict__ gamma, float eps,
+    const float *__restrict__ s, int64_t rows, int K4, int tpr, float *R, float *Y,
+    int8_t *__restrict__ q, float *__restrict__ scale, __nv_bfloat16 *__restrict__ op,
+    int32_t *__restrict__ l1, float fixed_scale, int fast) {
+    extern __shared__ float4 qtab[];
+    float4 *nstab = qtab;      // -s
+    float4 *ytab = qtab + K4;  // RN(1/s) or NaN
+    __shared__ float red2[2][NT / 32];
+    pdl_launch_dependents();
+    pdl_wait();
+    int rb = 0;  // the slot array of the group's next reduction (see row_group_reduce)
+    const int rpb = NT / tpr;
+    const int g = threadIdx.x / tpr;
+    const int t = threadIdx.x % tpr;
+    const float4 *s4 = reinterpret_cast<const float4 *>(s);
+    const float4 *g4 = reinterpret_cast<const float4 *>(gamma);
+    for (int j = threadIdx.x; j < K4; j += NT) {
+        const float4 v = __ldg(s4 + j);
+        nstab[j] = make_float4(-v.x, -v.y, -v.z, -v.w);
+        ytab[j] = make_float4(smooth_recip(v.x), smooth_recip(v.y), smooth_recip(v.z),
+                              smooth_recip(v.w));
+    }
+    __syncthreads();
+    const unsigned long long magic2 = pk(kRoundMagic, kRoundMagic);
+    const float Kf = (float)(4 * K4);
+    const int64_t tiles = (rows + rpb - 1) / rpb;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int64_t row = tile * rpb + g;
+        const bool valid = row < rows;
+        const int64_t off = (valid ? row : 0) * K4;
+        const float4 *h4 = reinterpret_cast<const float4 *>(H) + off;
+        float4 v[VPT];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int j = t + i * tpr;
+            v[i] = (valid && j < K4) ? __ldcs(h4 + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (residual) {
+            const float4 *r4 = reinterpret_cast<const float4 *>(residual) + off;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int j = t + i * tpr;
+                if (valid && j < K4) {
+                    const float4 r = __ldcs(r4 + j);
+                    v[i] = make_float4(v[i].x + r.x, v[i].y + r.y, v[i].z + r.z, v[i].w + r.w);
+                }
+            }
+        }
+        float sq = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int j = t + i * tpr;
+            if (R && valid && j < K4) reinterpret_cast<float4 *>(R)[off + j] = v[i];
+            sq += (v[i].x * v[i].x + v[i].y * v[i].y) + (v[i].z * v[i].z + v[i].w * v[i].w);
+        }
+        const float ms = __fdiv_rn(row_group_reduce<2>(sq, tpr, g, red2[rb]), Kf);
+        rb ^= 1;
+        // a row of zeros with eps = 0 is its own norm: zeros
+        const float var = __fadd_rn(ms, eps);
+        const float rstd = var == 0.0f ? 0.0f : __frsqrt_rn(var);
+        // y (kept in v), and the row maximum of |fl(y / s)| by the corrected
+        // reciprocal division on f32x2 pairs
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int j = t + i * tpr;
+            if (j >= K4) continue;
+            const float4 gv = __ldg(g4 + j);
+            float4 y;
+            y.x = __fmul_rn(__fmul_rn(v[i].x, rstd), gv.x);
+            y.y = __fmul_rn(__fmul_rn(v[i].y, rstd), gv.y);
+            y.z = __fmul_rn(__fmul_rn(v[i].z, rstd), gv.z);
+            y.w = __fmul_rn(__fmul_rn(v[i].w, rstd), gv.w);
+            if (Y && valid) reinterpret_cast<float4 *>(Y)[off + j] = y;
+            v[i] = y;
+            if (!STATIC) {
+                const float4 ys = ytab[j], ns = nstab[j];
+                const unsigned long long x01 = pk(y.x, y.y), x23 = pk(y.z, y.w);
+                const unsigned long long y01 = pk(ys.x, ys.y), y23 = pk(ys.z, ys.w);
+                const unsigned long long q01 = mul2(x01, y01), q23 = mul2(x23, y23);
+                float d0, d1, d2, d3;
+                upk(fma2(fma2(q01, pk(ns.x, ns.y), x01), y01, q01), d0, d1);
+                upk(fma2(fma2(q23, pk(ns.z, ns.w), x23), y23, q23), d2, d3);
+                m = max3_nan(m, max2_nan(fabsf(d0), fabsf(d1)), max2_nan(fabsf(d2), fabsf(d3)));
+            }
+        }
+        bool exact = !fast;
+        if (!STATIC) {
+            m = row_group_reduce<0>(m, tpr, g, red2[rb]);
+            rb ^= 1;
+            exact = !(m >= 0x1p-60f && m <= 0x1p100f);
+        }
+        float sc = fixed_scale;
+        if (!STATIC) {
+            if (exact) {
+                float me = 0.0f;
+                for (int i = 0; i < VPT; ++i) {
+                    const int j = t + i * tpr;
+                    if (j >= K4) continue;
+                    const float4 ns = nstab[j];
+                    me = fmaxf(me, fmaxf(abs_quotient(v[i].x, -ns.x), abs_quotient(v[i].y, -ns.y)));
+                    me = fmaxf(me, fmaxf(abs_quotient(v[i].z, -ns.z), abs_quotient(v[i].w, -ns.w)));
+                }
+                m = row_group_reduce<1>(me, tpr, g, red2[rb]);
+                rb ^= 1;
+            }
+            sc = m == 0.0f ? 1.0f : __fdiv_rn(m, 127.0f);
+        }
+        float a1 = 0.0f;
+        if (valid) {
+            if (t == 0) scale[row] = sc;
+            if (exact) {
+                for (int i = 0; i < VPT; ++i) {
+                    const int j = t + i * tpr;
+                    if (j >= K4) continue;
+                    const float4 ns = nstab[j];
+                    const float c0 = exact_code(v[i].x, -ns.x, sc);
+                    const float c1 = exact_code(v[i].y, -ns.y, sc);
+                    const float c2 = exact_code(v[i].z, -ns.z, sc);
+                    const float c3 = exact_code(v[i].w, -ns.w, sc);
+                    store4_codes(c0, c1, c2, c3, (off + j) * 4, q, op);
+                    a1 += (fabsf(c0) + fabsf(c1)) + (fabsf(c2) + fabsf(c3));
+                }
+            } else {
+                const float rsc = __frcp_rn(sc);
+                const unsigned long long r2 = pk(rsc, rsc);
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    const int j = t + i * tpr;
+                    if (j >= K4) continue;
+                    const float4 ys = ytab[j];
+                    const unsigned long long p01 =
+                        mul2(mul2(pk(v[i].x, v[i].y), pk(ys.x, ys.y)), r2);
+                    const unsigned long long p23 =
+                        mul2(mul2(pk(v[i].z, v[i].w), pk(ys.z, ys.w)), r2);
+                    const unsigned long long t01 = sub2(add2(p01, magic2), magic2);
+                    const unsigned long long t23 = sub2(add2(p23, magic2), magic2);
+                    float c[4], d[4];
+                    upk(t01, c[0], c[1]);
+                    upk(t23, c[2], c[3]);
+                    upk(sub2(p01, t01), d[0], d[1]);
+                    upk(sub2(p23, t23), d[2], d[3]);
+                    // NaN kept: a column whose s has no reciprocal
+                    const float dm = max3_nan(fabsf(d[0]), fabsf(d[1]),
+                                              max2_nan(fabsf(d[2]), fabsf(d[3])));
+                    if (!(dm <= kTieLimit)) {
+                        const float4 ns = nstab[j];
+                        if (!(fabsf(d[0]) <= kTieLimit)) c[0] = exact_code(v[i].x, -ns.x, sc);
+                        if (!(fabsf(d[1]) <= kTieLimit)) c[1] = exact_code(v[i].y, -ns.y, sc);
+                        if (!(fabsf(d[2]) <= kTieLimit)) c[2] = exact_code(v[i].z, -ns.z, sc);
+                        if (!(fabsf(d[3]) <= kTieLimit)) c[3] = exact_code(v[i].w, -ns.w, sc);
+                    }
+                    if (STATIC) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) c[e] = fminf(127.0f, fmaxf(-127.0f, c[e]));
+                    }
+                    store4_codes(c[0], c[1], c[2], c[3], (off + j) * 4, q, op);
+                    a1 += (fabsf(c[0]) + fabsf(c[1])) + (fabsf(c[2]) + fabsf(c[3]));
+                }
+            }
+        }
+        if (l1) {
+            a1 = row_group_reduce<2>(a1, tpr, g, red2[rb]);  // exact: <= 127 * 16384 < 2^24
+            rb ^= 1;
+            if (valid && t == 0) l1[row] = (int32_t)a1;
+        }
+    }
+}
+
+using RmsKern = void (*)(const float *, const float *, const float *, float, const float *,
+                         int64_t, int, int, float *, float *, int8_t *, float *,
+                         __nv_bfloat16 *, int32_t *, float, int);
+
+}  // namespace
+
+sq_status launch_rmsnorm_quant(const float *H, const float *residual, const float *gamma,
+                               float eps, const float *s, int64_t rows, int64_t K,
+                               float static_scale, float *R, float *Y, int8_t *q, float *scale,
+                               __nv_bfloat16 *op, int32_t *l1, cudaStream_t st) {
+    DeviceInfo di;
+    sq_status rc = device_info(&di);
+    if (rc != SQ_OK) return rc;
+    if (K > kMaxRow) return SQ_ERR_UNSUPPORTED;
+    const int K4 = (int)(K / 4);
+    const int vi = K <= 4096 ? 0 : K <= 8192 ? 1 : 2;
+    const int ki = static_scale > 0.0f ? 1 : 0;
+    static const RmsKern kerns[2][3] = {
+        {rmsnorm_quant_kernel<false, 4, 256>, rmsnorm_quant_kernel<false, 8, 256>,
+         rmsnorm_quant_kernel<false, 8, 512>},
+        {rmsnorm_quant_kernel<true, 4, 256>, rmsnorm_quant_kernel<true, 8, 256>,
+         rmsnorm_quant_kernel<true, 8, 512>}};
+    const RmsKern kern = kerns[ki][vi];
+    const int vpt = vi == 0 ? 4 : 8, nt = vi == 2 ? 512 : 256;
+    int tpr = 32;
+    while (tpr * vpt < K4) tpr <<= 1;
+    const int64_t tiles = (rows + nt / tpr - 1) / (nt / tpr);
+    // the range of scales for which the product decides the code (see the kernel)
+    const int fast = static_scale >= 0x1p-60f && static_scale <= 0x1p60f;
+    const int smem = K4 * 32;
+    static std::mutex mu;
+    static int occ[64][2][3] = {};  // resident blocks at the widest row of each variant
+    int resident = 0;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        int &o = occ[di.device & 63][ki][vi];
+        const int widest = (vi == 0 ? 4096 : vi == 1 ? 8192 : kMaxRow) * 8;
+        if (!o) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, widest) !=
+                    cudaSuccess ||
+                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, kern, nt, widest) !=
+                    cudaSuccess ||
+                o < 1) {
+                o = 0;
+                return SQ_ERR_CUDA;
+            }
+        }
+        resident = o;
+    }
+    const int64_t grid = std::min<int64_t>(tiles, 2 * (int64_t)di.sms * resident);
+    return launch_pdl(kern, dim3((unsigned)grid), dim3((unsigned)nt), (size_t)smem, st, 1, H,
+                      residual, gamma, eps, s, rows, K4, tpr, R, Y, q, scale, op, l1,
+                      static_scale, fast);
+}
+
+}  // namespace sq

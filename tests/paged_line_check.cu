@@ -1,0 +1,158 @@
+// Host-only check of the paged attention's division of work (paged_line.cuh),
+// run on the CPU by tests/test_paged_line.py: for random batches, head counts,
+// tile sizes and CTA counts, the pieces that all CTAs walk cover every (row
+// tile, key/value head, key tile) exactly once, in order; the pieces of a split
+// item name the CTAs that hold them, two partial slots per CTA are enough, and
+// the counter of a split item is nobody else's.  Prints a summary line; exit
+// status 1 on any failure.
+#include "paged_line.cuh"
+
+#include <cstdio>
+#include <map>
+#include <random>
+#include <tuple>
+#include <vector>
+
+using namespace sq;
+
+static long long g_checked = 0, g_fail = 0;
+#define CHECK(cond)                                              \
+    do {                                                         \
+        ++g_checked;                                             \
+        if (!(cond) && g_fail++ < 20)                            \
+            std::printf("FAIL line %d: %s\n", __LINE__, #cond);  \
+    } while (0)
+
+template <int KT>
+static void check(PagedArgs a, int grid, int min_pairs) {
+    // the line, pair by pair, as the header's comment states it
+    const int nb = a.prefix_phase ? 1 : a.B;
+    std::vector<std::tuple<int, int, int, int>> line;  // (sequence, row tile, head, key tile)
+    std::vector<int64_t> seq_begin;
+    for (int b = 0; b < nb; ++b) {
+        const Seq s = load_seq(a, b);
+        CHECK(s.q0 >= 0 && s.qlen >= 0 && s.q0 + s.qlen <= a.T && s.kv >= 0);
+        seq_begin.push_back((int64_t)line.size());
+        for (int j = 0; j < row_tiles(a, s); ++j) {
+            int last = 0;  // keys of the tile's last token, one past
+            for (int i = j * a.tpt; i < std::min(s.qlen, (j + 1) * a.tpt); ++i)
+                last = a.prefix_phase ? a.prefix_len : s.kv - s.qlen + i + 1;
+            int n = 1;
+            while (a.kstart + n * KT < last) ++n;
+            CHECK(n == key_tiles<KT>(a, s, j));
+            for (int h = 0; h < a.Hkv; ++h)
+                for (int k = 0; k < n; ++k) line.emplace_back(b, j, h, k);
+        }
+        CHECK(a.Hkv * key_tiles_before<KT>(a, s, row_tiles(a, s)) ==
+              (int64_t)line.size() - seq_begin[b]);
+    }
+    const int64_t total = (int64_t)line.size();
+    if (total == 0) return;
+    const int64_t fit = (total + min_pairs - 1) / min_pairs;
+    const int ctas = fit < grid ? (int)fit : grid;
+    int64_t at = 0;
+    std::map<int, std::tuple<int, int, int>> counter;          // first CTA -> split item
+    std::map<std::tuple<int, int, int>, std::vector<int>> parts;  // split item -> CTAs
+    std::map<std::tuple<int, int, int>, int> want;
+    for (int c = 0; c < ctas; ++c) {
+        Share sh;
+        sh.total = total;
+        sh.ctas = ctas;
+        sh.begin = share_begin(total, ctas, c);
+        sh.end = share_begin(total, ctas, c + 1);
+        CHECK(sh.begin == at && sh.end > sh.begin);
+        sh.seq = 0;
+        for (int b = 0; b < nb; ++b)
+            if (seq_begin[b] <= sh.begin &&
+                (b + 1 == nb ? total : seq_begin[b + 1]) > seq_begin[b])
+                sh.seq = b;
+        sh.seq_begin = seq_begin[sh.seq];
+        Walk<KT> w;
+        w.start(a, sh);
+        Piece p;
+        bool slots[2] = {false, false};
+        while (w.next(a, sh, p)) {
+            const auto [b, j, h, k] = line[at];
+            const Seq s = load_seq(a, b);
+            CHECK(p.seq == b && p.head == h && p.ntiles >= 1);
+            CHECK(p.tok0 == s.q0 + j * a.tpt && p.ntok == std::min(a.tpt, s.qlen - j * a.tpt));
+            CHECK(p.key0 == a.kstart + k * KT && p.keys == tile_keys(a, s, j));
+            if (!a.prefix_phase) CHECK(p.pos0 == s.kv - s.qlen + j * a.tpt);
+            for (int i = 0; i < p.ntiles; ++i)
+                CHECK(at + i < total && line[at + i] == std::make_tuple(b, j, h, k + i));
+            const auto item = std::make_tuple(b, j, h);
+            const bool whole = k == 0 && p.ntiles == key_tiles<KT>(a, s, j);
+            CHECK(whole == (p.npieces == 1));
+            if (!whole) {
+                CHECK(p.slot >= 0 && p.slot < 2 && !slots[p.slot]);
+                slots[p.slot] = true;
+                // the joiner reads slot 1 of the first CTA and slot 0 of the others
+                CHECK((c == p.first_cta) == (p.slot == 1));
+                CHECK(!counter.count(p.first_cta) || counter[p.first_cta] == item);
+                counter[p.first_cta] = item;
+                parts[item].push_back(c);
+                want[item] = p.npieces;
+                CHECK(parts[item].size() ==
+                      (size_t)(c - p.first_cta + 1));  // every CTA between holds a piece
+            }
+            at += p.ntiles;
+        }
+        CHECK(at == sh.end);
+    }
+    CHECK(at == total);
+    for (auto &e : parts) CHECK((int)e.second.size() == want[e.first]);
+    for (int64_t x = 0; x < total; x += 1 + total / 97) {
+        const int c = share_of(total, ctas, x);
+        CHECK(c >= 0 && c < ctas && share_begin(total, ctas, c) <= x &&
+              x < share_begin(total, ctas, c + 1));
+    }
+}
+
+int main() {
+    std::mt19937 rng(7);
+    auto pick = [&](int lo, int hi) { return lo + (int)(rng() % (unsigned)(hi - lo + 1)); };
+    for (int trial = 0; trial < 4000; ++trial) {
+        PagedArgs a = {};
+        a.B = pick(1, trial % 3 ? 6 : 40);
+        a.Hkv = pick(1, 4);
+        a.G = pick(1, 8);
+        const int rows = trial % 2 ? 256 : (trial % 4 ? 8 : 16);
+        a.tpt = std::max(1, rows / a.G);
+        const int KT = trial % 2 ? 128 : 64;
+        const int page = 16 << pick(0, 4);
+        a.max_pages = pick(0, 3000 / page);
+        a.cap = (int)(a.max_pages * page);
+        std::vector<int> q(a.B + 1), kv(a.B);
+        q[0] = pick(0, 3);
+        const int longest = pick(0, 2) ? pick(0, 5) : pick(0, 700);
+        for (int b = 0; b < a.B; ++b) {
+            q[b + 1] = q[b] + pick(0, longest);
+            kv[b] = pick(0, 4) ? pick(0, 2500) : 0;
+        }
+        a.T = q[a.B] + pick(0, 5);
+        if (trial % 11 == 0)  // arrays that hold anything
+            for (int b = 0; b < a.B; ++b) {
+                q[pick(0, a.B)] = (int)rng();
+                kv[b] = (int)rng();
+            }
+        a.q_start = q.data();
+        a.kv_len = kv.data();
+        a.prefix_len = pick(0, 1) ? pick(1, 1500) : 0;
+        for (int phase = a.prefix_len ? 1 : 0; phase >= 0; --phase) {
+            a.prefix_phase = phase;
+            a.kstart = phase ? 0 : a.prefix_len / KT * KT;
+            const int grid = pick(1, 152), least = pick(1, 4);
+            if (KT == 64) check<64>(a, grid, least);
+            else check<128>(a, grid, least);
+        }
+    }
+    // the closed-form sum against a loop
+    for (int trial = 0; trial < 20000; ++trial) {
+        const int64_t n = pick(0, 60), m = pick(1, 130), p = pick(0, 300), q = pick(0, 3000);
+        int64_t want = 0;
+        for (int64_t i = 0; i < n; ++i) want += (p * i + q) / m;
+        CHECK(floor_sum(n, m, p, q) == want);
+    }
+    std::printf("%lld checks, %lld failures\n", g_checked, g_fail);
+    return g_fail != 0;
+}
