@@ -1,93 +1,15 @@
-// Shared parts of the attention kernels over the paged cache: bounded waits,
-// the CTA's share of the work, and the rows' last step.
+// Shared parts of the attention kernels over the paged cache: the workers'
+// shares, the split of fp32 numbers over 16-bit ones, and the rows' last step.
 #pragma once
 #include "common.cuh"
 #include "paged_line.cuh"
 
-#include <cuda.h>
 #include <cuda_fp16.h>
 
 namespace sq {
 
 namespace {
 
-constexpr unsigned long long kPagedTimeoutNs = 4000000000ull;
-
-__device__ __forceinline__ uint32_t su32(const void *p) {
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-__device__ __forceinline__ uint64_t gtime() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-__device__ __forceinline__ void bar_init(uint64_t *bar, unsigned count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(bar)), "r"(count));
-}
-__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort,
-                                       unsigned *error) {
-    const uint64_t t0 = gtime();
-    for (uint32_t it = 1;; ++it) {
-        if (try_wait(bar, parity)) return true;
-        if ((it & 63u) == 0) {
-            if (*abort) return false;
-            if (gtime() - t0 > kPagedTimeoutNs) {
-                *abort = 1;
-                atomicOr(error, 1u);
-                return false;
-            }
-        }
-    }
-}
-// Bounded wait for the phase of parity `parity`; false when the CTA aborted.
-__device__ __forceinline__ bool wait_bar(const uint64_t *bar, uint32_t parity,
-                                         volatile int *abort, unsigned *error) {
-    const uint32_t a = su32(bar);
-    if (try_wait(a, parity)) return true;
-    return wait_slow(a, parity, abort, error);
-}
-// Every lane waits (so that every lane sees what the barrier publishes); the
-// outcome is the warp's.
-__device__ __forceinline__ bool warp_wait(const uint64_t *bar, uint32_t parity,
-                                          volatile int *abort, unsigned *error) {
-    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, error)) != 0;
-}
-__device__ __forceinline__ void drain_bar(const uint64_t *bar, uint32_t parity,
-                                          unsigned *error) {
-    const uint32_t a = su32(bar);
-    const uint64_t t0 = gtime();
-    while (!try_wait(a, parity))
-        if (gtime() - t0 > kPagedTimeoutNs) {
-            atomicOr(error, 2u);
-            return;
-        }
-}
-__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(bar)) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(bar)),
-                 "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, uint64_t *bar,
-                                        int x, int y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(su32(bar)), "r"(x), "r"(y)
-        : "memory");
-}
 // 2^x, relative error below 2^-22, results below 2^-126 flushed to zero
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -99,29 +21,34 @@ __device__ __forceinline__ float max_factor(float a, float b) {
     return a == -INFINITY ? 0.0f : ex2(a - b);
 }
 
-// (a, b) as a pair of the cache's 16-bit type, a in the low half, and what the
-// rounding left of each, rounded the same way: hi + lo is within 2^-18 (bf16)
-// or 2^-22 (fp16) of the value, relative.
-template <bool BF>
-__device__ __forceinline__ void split16(float a, float b, uint32_t &hi, uint32_t &lo) {
-    if (BF) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        const __nv_bfloat162 l =
-            __floats2bfloat162_rn(a - __low2float(h), b - __high2float(h));
-        hi = *reinterpret_cast<const uint32_t *>(&h);
-        lo = *reinterpret_cast<const uint32_t *>(&l);
-    } else {
-        const __half2 h = __floats2half2_rn(a, b);
-        const __half2 l = __floats2half2_rn(a - __low2float(h), b - __high2float(h));
-        hi = *reinterpret_cast<const uint32_t *>(&h);
-        lo = *reinterpret_cast<const uint32_t *>(&l);
+// N pairs of 16-bit numbers of the cache's type that sum to (a, b), a in the
+// low half: each is the rounding of what the ones before it left.  Two bf16
+// numbers are within 2^-18 of the value (relative), three within 2^-27, two
+// fp16 numbers within 2^-22.
+template <bool BF, int N>
+__device__ __forceinline__ void split16(float a, float b, uint32_t (&w)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (BF) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            a -= __low2float(h);
+            b -= __high2float(h);
+        } else {
+            const __half2 h = __floats2half2_rn(a, b);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            a -= __low2float(h);
+            b -= __high2float(h);
+        }
     }
 }
 
-// The line's length and this CTA's share of it, by all NT threads of the
-// block: each sums a run of sequences, a scan over the threads places them.
-template <int KT, int NT>
-__device__ __forceinline__ void find_share(const PagedArgs &a, int min_pairs, Share *out) {
+// The line's length and the shares of this block's W workers (worker w of block
+// c is number w gridDim.x + c, so that neighbours on the line are on different
+// SMs), by all NT threads: each sums a run of sequences, a scan over the
+// threads places them.
+template <int KT, int NT, int W>
+__device__ __forceinline__ void find_shares(const PagedArgs &a, int min_pairs, Share *out) {
     __shared__ int64_t warp_sum[NT / 32];
     const int nb = a.prefix_phase ? 1 : a.B;
     const int run = (nb + NT - 1) / NT;
@@ -146,26 +73,30 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int min_pairs, Sh
     }
     before += incl - mine;  // pairs of the runs before this thread's
     const int64_t fit = (total + min_pairs - 1) / min_pairs;
-    const int ctas = fit < (int64_t)gridDim.x ? (int)fit : (int)gridDim.x;
-    const bool some = (int)blockIdx.x < ctas;
-    const int64_t begin = some ? share_begin(total, ctas, blockIdx.x) : total;
-    if (some && begin >= before && begin < before + mine) {
-        int64_t at = before;
-        int b = b0;
-        for (; b < b1 - 1; ++b) {
-            const Seq s = load_seq(a, b);
-            const int64_t n = a.Hkv * key_tiles_before<KT>(a, s, row_tiles(a, s));
-            if (begin < at + n) break;
-            at += n;
+    const int most = W * (int)gridDim.x;
+    const int workers = fit < most ? (int)fit : most;
+#pragma unroll 1
+    for (int w = 0; w < W; ++w) {
+        const int c = w * (int)gridDim.x + (int)blockIdx.x;
+        const int64_t begin = c < workers ? share_begin(total, workers, c) : total;
+        if (begin < total && begin >= before && begin < before + mine) {
+            int64_t at = before;
+            int b = b0;
+            for (; b < b1 - 1; ++b) {
+                const Seq s = load_seq(a, b);
+                const int64_t n = a.Hkv * key_tiles_before<KT>(a, s, row_tiles(a, s));
+                if (begin < at + n) break;
+                at += n;
+            }
+            out[w].seq = b;
+            out[w].seq_begin = at;
         }
-        out->seq = b;
-        out->seq_begin = at;
-    }
-    if (threadIdx.x == 0) {
-        out->total = total;
-        out->ctas = ctas;
-        out->begin = begin;
-        out->end = some ? share_begin(total, ctas, blockIdx.x + 1) : total;
+        if (threadIdx.x == w) {
+            out[w].total = total;
+            out[w].workers = workers;
+            out[w].begin = begin;
+            out[w].end = c < workers ? share_begin(total, workers, c + 1) : total;
+        }
     }
     __syncthreads();
 }
@@ -186,50 +117,54 @@ __device__ __forceinline__ int row_limit(const PagedArgs &a, const Piece &p, int
     return min(a.prefix_len, kv - end + tok + 1);
 }
 
-// N consecutive output columns of one row, from its maximum m (log2 units),
-// sum l and unnormalised output o: the prefix's buffer, or the output joined
-// with it.  row = token * Hq + query head.
-template <int D, int N>
-__device__ __forceinline__ void write_row(const PagedArgs &a, int64_t row, int col, float m,
-                                          float l, float (&o)[N]) {
+// A row's last step, from its maximum m (log2 units) and sum l: the factors of
+// its own unnormalised output and of the prefix's, or the prefix's buffer.
+// row = token * Hq + query head; `first`: the caller that stores m and l.
+struct RowEnd {
+    float own, front;
+    int64_t at;
+};
+template <int D>
+__device__ __forceinline__ RowEnd row_end(const PagedArgs &a, int64_t row, float m, float l,
+                                          bool first) {
+    RowEnd e;
+    e.at = row * D;
+    e.own = 1.0f;
+    e.front = 0.0f;
     if (a.prefix_phase) {
-        if (col == 0) a.prefix_ml[row] = make_float2(m, l);
-        float4 *d = reinterpret_cast<float4 *>(a.prefix_o + row * D + col);
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i)
-            d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        return;
+        if (first) a.prefix_ml[row] = make_float2(m, l);
+        return e;
     }
-    float own = 1.0f;
     if (a.prefix_len > 0) {
         const float2 f = a.prefix_ml[row];
         const float top = fmaxf(m, f.x);
-        own = max_factor(m, top);
-        const float front = max_factor(f.x, top);
-        l = l * own + f.y * front;
-        const float4 *d = reinterpret_cast<const float4 *>(a.prefix_o + row * D + col);
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-            const float4 v = d[i];
-            o[4 * i] = o[4 * i] * own + v.x * front;
-            o[4 * i + 1] = o[4 * i + 1] * own + v.y * front;
-            o[4 * i + 2] = o[4 * i + 2] * own + v.z * front;
-            o[4 * i + 3] = o[4 * i + 3] * own + v.w * front;
-        }
+        e.own = max_factor(m, top);
+        e.front = max_factor(f.x, top);
+        l = l * e.own + f.y * e.front;
     }
     const float inv = l > 0.0f ? __frcp_rn(l) : 0.0f;  // no key: zeros
-    float4 *d = reinterpret_cast<float4 *>(a.O + row * D + col);
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i)
-        d[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv,
-                           o[4 * i + 3] * inv);
+    e.own *= inv;
+    e.front *= inv;
+    return e;
+}
+__device__ __forceinline__ void row_store(const PagedArgs &a, const RowEnd &e, int col, float2 o) {
+    if (a.prefix_phase) {
+        *reinterpret_cast<float2 *>(a.prefix_o + e.at + col) = o;
+        return;
+    }
+    float2 r = make_float2(o.x * e.own, o.y * e.own);
+    if (a.prefix_len > 0) {
+        const float2 f = *reinterpret_cast<const float2 *>(a.prefix_o + e.at + col);
+        r.x += f.x * e.front;
+        r.y += f.y * e.front;
+    }
+    *reinterpret_cast<float2 *>(a.O + e.at + col) = r;
 }
 
 }  // namespace
 
-// Launchers of the two kernels (see the files): the map of K and of V, one box
-// of `bx` cache rows x 64 elements.
-sq_status launch_paged_rows(const PagedArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
-                            int D, bool bf16, int row_groups, int bx, int sms, cudaStream_t st);
+// The kernel for at most 16 rows per item (paged_rows.cu): rows = 8 or 16.
+sq_status launch_paged_rows(const PagedArgs &a, const void *k_cache, const void *v_cache, int D,
+                            bool bf16, int rows, int sms, cudaStream_t st);
 
 }  // namespace sq

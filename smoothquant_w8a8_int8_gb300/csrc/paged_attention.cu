@@ -53,7 +53,7 @@ sq_status launch_paged_attention(const PagedCall &c, cudaStream_t st) {
     DeviceInfo di;
     sq_status rc = device_info(&di);
     if (rc != SQ_OK) return rc;
-    if (di.sms * 2 * 4 > kCounterBytes) return SQ_ERR_UNSUPPORTED;
+    if (di.sms * 8 * 4 > kCounterBytes) return SQ_ERR_UNSUPPORTED;
     PagedArgs a = {};
     if ((rc = error_word(di.device, &a.error)) != SQ_OK) return rc;
     a.Q = c.Q;
@@ -90,19 +90,14 @@ sq_status launch_paged_attention(const PagedCall &c, cudaStream_t st) {
     a.scale = fabsf(c.scale) * 1.4426950408889634f;
     a.sign = c.scale < 0.0f ? -1.0f : 1.0f;
     const bool bf16 = c.cache_type == SQ_CACHE_BF16;
-    const int64_t cache_rows = c.num_pages * c.Hkv * c.page_size;
-    const int bx = (int)std::min<int64_t>(c.page_size, 64);
-    CUtensorMap mk, mv;
-    if ((rc = make_map_16(&mk, bf16, c.k_cache, cache_rows, c.D, bx, 64)) != SQ_OK ||
-        (rc = make_map_16(&mv, bf16, c.v_cache, cache_rows, c.D, bx, 64)) != SQ_OK)
-        return rc;
     for (int phase = c.prefix_len > 0 ? 1 : 0; phase >= 0; --phase) {
         a.prefix_phase = phase;
         const int64_t most = (phase ? c.T : c.max_q) * a.G;
-        const int rg = most <= 8 ? 1 : 2;
-        a.tpt = std::max(1, rg * 8 / a.G);
-        a.kstart = phase ? 0 : a.prefix_len / 64 * 64;
-        if ((rc = launch_paged_rows(a, mk, mv, (int)c.D, bf16, rg, bx, di.sms, st)) != SQ_OK)
+        const int r = most <= 8 ? 8 : 16;
+        a.tpt = std::max(1, r / a.G);
+        a.kstart = phase ? 0 : a.prefix_len / 16 * 16;
+        if ((rc = launch_paged_rows(a, c.k_cache, c.v_cache, (int)c.D, bf16, r, di.sms, st)) !=
+            SQ_OK)
             return rc;
     }
     return SQ_OK;

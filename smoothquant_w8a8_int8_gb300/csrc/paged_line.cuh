@@ -5,12 +5,13 @@
 // An item is a tile of query rows (tokens x heads of one key/value
 // head's group) of one sequence and one key/value head; its keys are cut into
 // tiles of KT.  All (item, key tile) pairs stand in one line -- sequences,
-// then row tiles, then key/value heads, then key tiles -- and CTA c of n takes
-// pairs [c W / n, (c + 1) W / n): every CTA has the same share whatever the
-// lengths, known only on the device, are.  An item that lies in several CTAs'
-// shares leaves one partial result (row maximum, sum, unnormalised output) per
-// CTA in the workspace; the CTA that arrives last (a counter) joins them in
-// the order of the line, so that the result does not depend on who is last.
+// then row tiles, then key/value heads, then key tiles -- and worker c of n (a
+// CTA, or a warp) takes pairs [c W / n, (c + 1) W / n): every worker has the
+// same share whatever the lengths, known only on the device, are.  An item that
+// lies in several workers' shares leaves one partial result (row maximum, sum,
+// unnormalised output) per worker in the workspace; the one that arrives last
+// (a counter) joins them in the order of the line, so that the result does not
+// depend on who is last.
 #pragma once
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -26,8 +27,8 @@ struct PagedArgs {
     float *prefix_o;     // [T Hq][D] unnormalised output over the prefix
     float2 *prefix_ml;   // [T Hq] its row maximum (log2 units) and sum
     unsigned *counters;  // zero between launches
-    float *part_o;       // [2 CTAs][rows][D] partial outputs, two slots per CTA
-    float2 *part_ml;     // [2 CTAs][rows]
+    float *part_o;       // [2 workers][rows][D] partial outputs, two slots each
+    float2 *part_ml;     // [2 workers][rows]
     unsigned *error;     // the library's error word
     int T, B, Hq, Hkv, G;
     int tpt;             // tokens per row tile
@@ -115,23 +116,23 @@ SQ_HD int64_t key_tiles_before(const PagedArgs &a, const Seq &s, int J) {
     return sum;
 }
 
-// Where a CTA's share starts.
+// Where a worker's share starts.
 struct Share {
     int64_t total;       // W
-    int64_t begin, end;  // this CTA's pairs
+    int64_t begin, end;  // this worker's pairs
     int64_t seq_begin;   // the line's position of sequence `seq`
     int seq;
-    int ctas;            // CTAs that take a share
+    int workers;         // workers that take a share
 };
-SQ_HD int64_t share_begin(int64_t total, int ctas, int c) {
-    return total * c / ctas;
+SQ_HD int64_t share_begin(int64_t total, int workers, int c) {
+    return total * c / workers;
 }
-// the CTA whose share holds position x
-SQ_HD int share_of(int64_t total, int ctas, int64_t x) {
-    return (int)(((x + 1) * ctas - 1) / total);
+// the worker whose share holds position x
+SQ_HD int share_of(int64_t total, int workers, int64_t x) {
+    return (int)(((x + 1) * workers - 1) / total);
 }
 
-// A CTA's piece of an item, as its producer hands it to the other warps.
+// A worker's piece of an item.
 struct Piece {
     int tok0, ntok;     // tokens of the row tile
     int head;           // key/value head
@@ -139,12 +140,11 @@ struct Piece {
     int key0, ntiles;   // first key and key tiles of the piece
     int keys;           // one past the last key any row attends to
     int seq;
-    int first_cta, npieces;  // npieces = 1: the whole item
-    int slot;           // this CTA's partial slot
-    int stop;           // no further piece
+    int first, npieces;  // first worker of the item; npieces = 1: the whole item
+    int slot;           // the worker's partial slot
 };
 
-// Walks the pieces of a CTA's share.
+// Walks the pieces of a worker's share.
 template <int KT>
 struct Walk {
     int64_t at, end;  // position, end of the share
@@ -191,10 +191,9 @@ struct Walk {
         p.ntiles = take;
         p.keys = tile_keys(a, s, j);
         p.seq = b;
-        p.first_cta = share_of(sh.total, sh.ctas, s0);
-        p.npieces = share_of(sh.total, sh.ctas, s0 + nk - 1) - p.first_cta + 1;
+        p.first = share_of(sh.total, sh.workers, s0);
+        p.npieces = share_of(sh.total, sh.workers, s0 + nk - 1) - p.first + 1;
         p.slot = k == 0 ? 1 : 0;  // begun here: slot 1; begun before: slot 0
-        p.stop = 0;
         at += take;
         k += take;
         if (k == nk) {

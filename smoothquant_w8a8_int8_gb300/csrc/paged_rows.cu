@@ -4,22 +4,27 @@
 // With m the running row maximum and l the running sum (both fp32), a tile of
 // keys contributes s = q K^T, m' = max(m, max s), p = 2^(s - m'), and
 // l = l 2^(m - m') + sum p, O = O 2^(m - m') + p V: one pass over the cache.
-// The cache is read once and every byte of it serves at most 16 rows, so the
-// kernel is bound by memory; all it has to do is keep enough copies in flight
-// and the arithmetic out of their way.
+// Every byte of the cache serves at most 16 rows, so the kernel is bound by
+// memory; all it has to do is keep enough copies in flight and the arithmetic
+// out of their way.
 //
-// A CTA holds a ring of tiles of 64 keys and values that one warp fills with
-// TMA (128-byte swizzle, one box per page and 64 columns).  RG groups of four
-// warps own 8 query rows each; a group's warps take 16 keys of every tile
-// each, with their own m, l and O, and join them through shared memory at the
-// end of an item.  The products run on the warp-level tensor instructions
-// (m16n8k16): 16 rows are too few for tensor memory's 128.
+// A worker is a warp: it takes its share of the line in steps of 16 keys, with
+// a ring of its own in shared memory that it fills with cp.async, two or more
+// steps ahead and across the borders of items.  Warps meet nobody, so that no
+// warp's item end stalls the others' copies; 8 warps hold 128 KB in flight per
+// SM.  A step lies in one page whatever the page's size (TMA boxes of one
+// 16-row page each measured 104 ns of its unit's time a box, 3.0 TB/s in all;
+// 16-byte copies by the lanes stream random 16-row pages at 7.0 TB/s).  Rows
+// behind the last key and rows of missing pages are filled with zeros.
 //
-// Precision: keys and values enter as stored.  Each fp32 query is split in two
-// 16-bit numbers (split16) and the two parts of 8 rows make up the
-// instruction's 16 rows -- rows 0-7 the rounded queries, rows 8-15 what the
-// rounding left -- so that the split costs nothing; the sums of both halves
-// are added in fp32.  The probabilities are split the same way.
+// The products run on the warp-level tensor instructions (m16n8k16, 8 cycles
+// each per SM quarter): 16 rows are too few for tensor memory's 128.
+//
+// Precision: keys and values enter as stored.  The fp32 queries and
+// probabilities are split over several 16-bit numbers (split16): two for fp16,
+// three for bf16, so that what is lost (2^-22) is no more than fp32 sums lose.
+// Up to 8 rows, two of the parts share an instruction's 16 rows (the first in
+// rows 0-7, the second in rows 8-15) and the two halves are added in fp32.
 #include "paged.cuh"
 
 #include <algorithm>
@@ -28,17 +33,17 @@
 namespace sq {
 namespace {
 
-constexpr int kKT = 64;      // keys per tile
-constexpr int kItems = 4;    // pieces the producer may be ahead
-constexpr int kMinPairs = 2; // key tiles of a CTA's share at least
+constexpr int kKT = 16;       // keys per step
+constexpr int kWarps = 8;
+constexpr int kMinSteps = 4;  // steps of a worker's share at least
+constexpr int kPieces = 8;    // more than the steps that the copies are ahead
 
-template <int D, int RG>
+template <int D>
 struct RowsCfg {
-    static constexpr int kThreads = RG * 128 + 32;
-    static constexpr int kTileBytes = kKT * D * 2;  // keys, or values, of a tile
-    static constexpr int kStages = (RG == 1 ? 196608 : 163840) / (2 * kTileBytes);
-    static constexpr int kJoin = RG * 4 * 8 * D * 4;  // [group][warp][row][D] outputs
-    static constexpr int kSmem = kStages * 2 * kTileBytes + kJoin + 1024;
+    static constexpr int kStepBytes = 2 * kKT * D * 2;  // keys, then values
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kSmem = kWarps * kStages * kStepBytes;
+    static_assert(kStages < kPieces, "a piece per step in flight and the one being worked on");
 };
 
 template <bool BF>
@@ -69,342 +74,350 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                  : "r"(addr)
                  : "memory");
 }
-
-template <int D, bool BF, int RG>
-__global__ void __launch_bounds__(RowsCfg<D, RG>::kThreads, 1)
-    paged_rows_kernel(const __grid_constant__ CUtensorMap mapK,
-                      const __grid_constant__ CUtensorMap mapV, const __grid_constant__ PagedArgs a,
-                      int bx) {
-    using C = RowsCfg<D, RG>;
-    constexpr int ST = C::kStages;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    float *join = reinterpret_cast<float *>(smem + ST * 2 * C::kTileBytes);
-    __shared__ uint64_t full[ST], empty[ST], item_full[kItems], item_empty[kItems], grp[RG];
-    __shared__ unsigned char holes[ST];  // bit i: the i-th box of the tile's keys is missing
-    __shared__ Piece items[kItems];
-    __shared__ Share share;
-    __shared__ float2 join_ml[RG][4][8];
-    __shared__ int last_flag[RG];
-    __shared__ int abort_flag;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    volatile int *abort = &abort_flag;
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < ST; ++i) {
-            bar_init(&full[i], 1);
-            bar_init(&empty[i], RG * 4);
-        }
-        for (int i = 0; i < kItems; ++i) {
-            bar_init(&item_full[i], 1);
-            bar_init(&item_empty[i], RG * 4);
-        }
-        for (int i = 0; i < RG; ++i) bar_init(&grp[i], 4);
-        abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    __syncthreads();
-    pdl_launch_dependents();
-    pdl_wait();  // every global-memory access below follows the previous kernel
-    find_share<kKT, C::kThreads>(a, kMinPairs, &share);
-
-    if (warp == RG * 4) {
-        // ------------------------------------------------------------ copies
-        const uint32_t sbase = su32(smem);
-        const int nsub = kKT / bx;  // boxes along the tile's keys
-        const int page_rows = 1 << a.page_shift;
-        const int rows_total = a.num_pages * a.Hkv << a.page_shift;
-        Walk<kKT> walk;
-        walk.start(a, share);
-        uint32_t tile = 0;  // tiles copied so far
-        bool ok = true;
-        for (uint32_t n = 0; ok; ++n) {
-            Piece p;
-            const bool more = walk.next(a, share, p);
-            const int slot = n % kItems;
-            if (n >= kItems &&
-                !warp_wait(&item_empty[slot], (n / kItems - 1) & 1u, abort, a.error))
-                break;
-            if (lane == 0) {
-                if (more) items[slot] = p;
-                else items[slot].stop = 1;
-                bar_arrive(&item_full[slot]);
-            }
-            if (!more) break;
-            const int *pages = a.prefix_phase ? a.prefix_pages
-                                              : a.block_table + (int64_t)p.seq * a.max_pages;
-            const int first_key = a.prefix_phase ? 0 : a.prefix_len;
-            int held = -1, entry = -1;  // lane i holds the page-table entry 32 held + i
-            for (int i = 0; i < p.ntiles; ++i, ++tile) {
-                const int st = tile % ST;
-                const int key0 = p.key0 + i * kKT;
-                // the tile's pages: the entries lane by lane, 32 at a time
-                int row = rows_total;  // past the end: the copy brings zeros
-                unsigned miss = 0;
-                for (int sub = 0; sub < nsub; ++sub) {
-                    const int key = key0 + sub * bx;
-                    const int idx = key >> a.page_shift;
-                    const bool in = key < p.keys && key + bx > first_key;
-                    int e = -1;
-                    if (in) {
-                        if (idx >> 5 != held) {
-                            held = idx >> 5;
-                            const int at = (held << 5) + lane;
-                            entry = (int64_t)at << a.page_shift < p.keys ? __ldg(pages + at) : -1;
-                        }
-                        e = __shfl_sync(0xffffffffu, entry, idx & 31);
-                    }
-                    const bool there = e >= 0 && e < a.num_pages;
-                    if (!there) miss |= 1u << sub;
-                    // lane: sub-box, 64-column slab, keys or values
-                    if (there && lane % nsub == sub)
-                        row = ((e * a.Hkv + p.head) << a.page_shift) + (key & (page_rows - 1));
-                }
-                if (tile >= ST && !warp_wait(&empty[st], (tile / ST - 1) & 1u, abort, a.error)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    holes[st] = (unsigned char)miss;
-                    bar_expect(&full[st], 2 * C::kTileBytes);
-                }
-                __syncwarp();
-                if (lane < nsub * (D / 64) * 2) {
-                    const int sub = lane % nsub, rest = lane / nsub;
-                    const int slab = rest % (D / 64), kv = rest / (D / 64);
-                    tma_box(sbase + (2 * st + kv) * C::kTileBytes + slab * kKT * 128 +
-                                sub * bx * 128,
-                            kv ? &mapV : &mapK, &full[st], slab * 64, row);
-                }
-            }
-        }
-        // every copy issued has landed before the shared memory can go away
-        if (lane == 0)
-            for (uint32_t i = tile > ST ? tile - ST : 0; i < tile; ++i)
-                drain_bar(&full[i % ST], (i / ST) & 1u, a.error);
-    } else {
-        // ------------------------------------------------- products and softmax
-        const int rg = warp >> 2, w = warp & 3;
-        const int g = lane >> 2, t = lane & 3;  // fragment row and column pair
-        const int gt = threadIdx.x & 127;       // thread of the group
-        uint32_t gphase = 0;
-        // the group's four warps meet (bounded, so that an abort leaves nobody behind)
-        auto group_sync = [&]() -> bool {
-            __syncwarp();
-            if (lane == 0) bar_arrive(&grp[rg]);
-            const bool ok = warp_wait(&grp[rg], gphase & 1u, abort, a.error);
-            ++gphase;
-            return ok;
-        };
-        uint32_t tile = 0;
-        for (uint32_t n = 0;; ++n) {
-            const int slot = n % kItems;
-            if (!warp_wait(&item_full[slot], (n / kItems) & 1u, abort, a.error)) break;
-            const Piece p = items[slot];
-            __syncwarp();
-            if (lane == 0) bar_arrive(&item_empty[slot]);
-            if (p.stop) break;
-            const int row = rg * 8 + g;  // this thread's row of the item
-            const int tok = row / a.G;
-            const bool live = tok < p.ntok;
-            const int limit = live ? row_limit(a, p, tok) : p.keys;
-            const int first_key = a.prefix_phase ? 0 : a.prefix_len;
-            // the queries, split: a0, a2 rounded (rows 0-7), a1, a3 the rest (rows 8-15)
-            uint32_t qf[D / 16][4];
-            const float *qrow = a.Q + (int64_t)(p.tok0 + tok) * a.ldq +
-                                (p.head * a.G + row % a.G) * D;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                float2 x = make_float2(0.f, 0.f), y = x;
-                if (live) {
-                    x = *reinterpret_cast<const float2 *>(qrow + 16 * i + 2 * t);
-                    y = *reinterpret_cast<const float2 *>(qrow + 16 * i + 2 * t + 8);
-                }
-                split16<BF>(x.x * a.sign, x.y * a.sign, qf[i][0], qf[i][1]);
-                split16<BF>(y.x * a.sign, y.y * a.sign, qf[i][2], qf[i][3]);
-            }
-            float o[D / 8][4];
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-            float m = -INFINITY, l = 0.0f;
-            bool ok = true;
-            for (int it = 0; it < p.ntiles; ++it, ++tile) {
-                const int st = tile % ST;
-                if (!warp_wait(&full[st], (tile / ST) & 1u, abort, a.error)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t ks = su32(smem) + 2 * st * C::kTileBytes;
-                const uint32_t vs = ks + C::kTileBytes;
-                const int key0 = p.key0 + it * kKT + 16 * w;  // this warp's keys
-                // logits of 8 rows x 16 keys, both halves of the split
-                float s[2][4];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
-                {
-                    const int kr = 16 * w + (lane >> 4) * 8 + (lane & 7);
-                    const uint32_t base = ks + kr * 128;
-                    const int half = (lane >> 3) & 1;
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        uint32_t b[4];
-                        ldsm4(b, base + (i / 4) * kKT * 128 +
-                                     ((((2 * i + half) & 7) ^ (kr & 7)) << 4));
-                        mma16816<BF>(s[0], qf[i], b[0], b[1]);
-                        mma16816<BF>(s[1], qf[i], b[2], b[3]);
-                    }
-                }
-                float x[4] = {s[0][0] + s[0][2], s[0][1] + s[0][3], s[1][0] + s[1][2],
-                              s[1][1] + s[1][3]};
-                const bool missing = (holes[st] >> (16 * w / bx)) & 1;
-                // does the mask cut this warp's keys?
-                const bool cut = key0 + 16 > p.keys || key0 < first_key || missing;
-                uint32_t vmask0 = 0xffffffffu, vmask1 = 0xffffffffu;
-                if (__any_sync(0xffffffffu, cut || key0 + 16 > limit)) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = key0 + 8 * (i >> 1) + 2 * t + (i & 1);
-                        if (missing || key >= limit || key < first_key) x[i] = -INFINITY;
-                    }
-                    // rows of the tile that hold no key of the sequence may hold
-                    // anything: their values are taken as zeros
-                    auto there = [&](int key) {
-                        return key < p.keys && key >= first_key ? 0xffffu : 0u;
-                    };
-                    vmask0 = there(key0 + 2 * t) | there(key0 + 2 * t + 1) << 16;
-                    vmask1 = there(key0 + 2 * t + 8) | there(key0 + 2 * t + 9) << 16;
-                }
-                float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = mx == -INFINITY ? m : fmaxf(m, mx * a.scale);
-                if (__any_sync(0xffffffffu, mn > m)) {
-                    const float f = max_factor(m, mn);
-                    l *= f;
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        o[i][0] *= f;
-                        o[i][1] *= f;
-                        o[i][2] *= f;
-                        o[i][3] *= f;
-                    }
-                    m = mn;
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[i] = x[i] == -INFINITY ? 0.0f : ex2(fmaf(x[i], a.scale, -m));
-                    l += x[i];
-                }
-                uint32_t pf[4];  // a0 / a1: keys 2t, 2t+1 rounded / rest; a2 / a3: keys + 8
-                split16<BF>(x[0], x[1], pf[0], pf[1]);
-                split16<BF>(x[2], x[3], pf[2], pf[3]);
-                {
-                    const int kr = 16 * w + ((lane >> 3) & 1) * 8 + (lane & 7);
-                    const uint32_t base = vs + kr * 128;
-                    const int half = lane >> 4;
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        uint32_t b[4];
-                        ldsm4t(b, base + (i / 4) * kKT * 128 +
-                                      ((((2 * i + half) & 7) ^ (kr & 7)) << 4));
-                        mma16816<BF>(o[2 * i], pf, b[0] & vmask0, b[1] & vmask1);
-                        mma16816<BF>(o[2 * i + 1], pf, b[2] & vmask0, b[3] & vmask1);
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) bar_arrive(&empty[st]);
-            }
-            if (!ok) break;
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
-            // the four warps' results
-            float *mine = join + ((rg * 4 + w) * 8 + g) * D;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                *reinterpret_cast<float2 *>(mine + 8 * i + 2 * t) =
-                    make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3]);
-            if (t == 0) join_ml[rg][w][g] = make_float2(m, l);
-            if (!group_sync()) break;
-            // thread: row gt / 16, D / 16 columns
-            constexpr int N = D / 16;
-            const int jr = gt >> 4, jc = (gt & 15) * N;
-            const int irow = rg * 8 + jr;
-            const bool jlive = irow / a.G < p.ntok;
-            float jm = -INFINITY, jl = 0.0f, jo[N];
-#pragma unroll
-            for (int i = 0; i < N; ++i) jo[i] = 0.0f;
-            for (int v = 0; v < 4; ++v) jm = fmaxf(jm, join_ml[rg][v][jr].x);
-            for (int v = 0; v < 4; ++v) {
-                const float2 e = join_ml[rg][v][jr];
-                const float f = max_factor(e.x, jm);
-                jl += e.y * f;
-                const float *src = join + ((rg * 4 + v) * 8 + jr) * D + jc;
-#pragma unroll
-                for (int i = 0; i < N; ++i) jo[i] += src[i] * f;
-            }
-            bool write = true;
-            if (p.npieces > 1) {
-                // this CTA's part of the item, then whoever is last joins them all
-                const int64_t base = ((int64_t)(2 * blockIdx.x + p.slot) * RG * 8 + irow);
-                float4 *d = reinterpret_cast<float4 *>(a.part_o + base * D + jc);
-#pragma unroll
-                for (int i = 0; i < N / 4; ++i)
-                    __stcg(d + i, make_float4(jo[4 * i], jo[4 * i + 1], jo[4 * i + 2],
-                                              jo[4 * i + 3]));
-                if (jc == 0) __stcg(a.part_ml + base, make_float2(jm, jl));
-                __threadfence();
-                if (!group_sync()) break;
-                unsigned *count = a.counters + p.first_cta * RG + rg;
-                if (gt == 0) {
-                    const bool last = atomicAdd(count, 1u) == (unsigned)p.npieces - 1;
-                    if (last) *count = 0;  // as the next launch wants it
-                    last_flag[rg] = last;
-                }
-                if (!group_sync()) break;
-                write = last_flag[rg] != 0;
-                if (write) {
-                    __threadfence();
-                    jm = -INFINITY;
-                    jl = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < N; ++i) jo[i] = 0.0f;
-                    for (int c = 0; c < p.npieces; ++c) {
-                        const int64_t from =
-                            (int64_t)(2 * (p.first_cta + c) + (c == 0)) * RG * 8 + irow;
-                        const float2 e = __ldcg(a.part_ml + from);
-                        const float top = fmaxf(jm, e.x);
-                        const float f = max_factor(jm, top), fe = max_factor(e.x, top);
-                        jm = top;
-                        jl = jl * f + e.y * fe;
-                        const float4 *src =
-                            reinterpret_cast<const float4 *>(a.part_o + from * D + jc);
-#pragma unroll
-                        for (int i = 0; i < N / 4; ++i) {
-                            const float4 v = __ldcg(src + i);
-                            jo[4 * i] = jo[4 * i] * f + v.x * fe;
-                            jo[4 * i + 1] = jo[4 * i + 1] * f + v.y * fe;
-                            jo[4 * i + 2] = jo[4 * i + 2] * f + v.z * fe;
-                            jo[4 * i + 3] = jo[4 * i + 3] * f + v.w * fe;
-                        }
-                    }
-                }
-            }
-            if (write && jlive)
-                write_row<D, N>(a,
-                                (int64_t)(p.tok0 + irow / a.G) * a.Hq + p.head * a.G + irow % a.G,
-                                jc, jm, jl, jo);
-            // the buffers are free for the next item
-            if (!group_sync()) break;
-        }
-    }
-    __syncthreads();
+// 16 bytes of global memory, or zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
 }
 
-template <int D, bool BF, int RG>
-sq_status launch_rows(const PagedArgs &a, const CUtensorMap &mk, const CUtensorMap &mv, int bx,
-                      int sms, cudaStream_t st) {
-    using C = RowsCfg<D, RG>;
+// The instruction's operand sets for rows of which each thread holds RPT (ROWS
+// / 8) pairs of elements: N parts of ROWS = 8 rows in (N + 1) / 2 sets, of 16
+// rows in N sets.
+template <bool BF, int ROWS>
+struct Parts {
+    static constexpr int kParts = BF ? 3 : 2;
+    static constexpr int kSets = ROWS == 8 ? (kParts + 1) / 2 : kParts;
+    static constexpr int kRows = ROWS / 8;
+    // registers r and r + 1 of every set (rows 0-7 and 8-15) from this thread's
+    // pairs (x[row][0], x[row][1])
+    static __device__ __forceinline__ void fill(const float (&x)[kRows][2], int r,
+                                                uint32_t (&f)[kSets][4]) {
+        uint32_t w[kRows][kParts];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) split16<BF, kParts>(x[i][0], x[i][1], w[i]);
+        if (ROWS == 8) {
+            f[0][r] = w[0][0];
+            f[0][r + 1] = w[0][1];
+            if (kSets > 1) {
+                f[kSets - 1][r] = w[0][kParts - 1];
+                f[kSets - 1][r + 1] = 0;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kSets; ++j) {
+                f[j][r] = w[0][j];
+                f[j][r + 1] = w[kRows - 1][j];
+            }
+        }
+    }
+};
+
+template <int D, bool BF, int ROWS>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    paged_rows_kernel(const __grid_constant__ PagedArgs a, const uint16_t *__restrict__ k_cache,
+                      const uint16_t *__restrict__ v_cache) {
+    using C = RowsCfg<D>;
+    using F = Parts<BF, ROWS>;
+    constexpr int ST = C::kStages, R = F::kRows, S = F::kSets;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Share shares[kWarps];
+    __shared__ Piece pieces[kWarps][kPieces];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    pdl_wait();  // every global-memory access below follows the previous kernel
+    find_shares<kKT, kWarps * 32, kWarps>(a, kMinSteps, shares);
+    const Share &share = shares[warp];
+    const int worker = warp * gridDim.x + blockIdx.x;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * ST * C::kStepBytes;
+    const int first_key = a.prefix_phase ? 0 : a.prefix_len;
+
+    // ---- the copies: one step of the share per call, or nothing at its end
+    Walk<kKT> walk;
+    walk.start(a, share);
+    int npieces = 0, left = 0, key = 0, held = -1, entry = -1, filled = 0;
+    int64_t head_row = 0;  // the piece's head, in cache rows of a page
+    int keys = 0;
+    unsigned holes = 0;    // bit i: the page of the step in buffer i is missing
+    const int *pages = nullptr;
+    auto copy_step = [&]() {
+        if (left == 0) {
+            Piece p;
+            if (walk.next(a, share, p)) {
+                if (lane == 0) pieces[warp][npieces % kPieces] = p;
+                ++npieces;
+                left = p.ntiles;
+                key = p.key0;
+                keys = p.keys;
+                head_row = (int64_t)p.head << a.page_shift;
+                pages = a.prefix_phase ? a.prefix_pages
+                                       : a.block_table + (int64_t)p.seq * a.max_pages;
+                held = -1;
+            }
+        }
+        if (left > 0) {
+            // lane i holds the page-table entry 32 held + i
+            const int idx = key >> a.page_shift;
+            if (idx >> 5 != held) {
+                held = idx >> 5;
+                const int at = (held << 5) + lane;
+                entry = (int64_t)at << a.page_shift < keys ? __ldg(pages + at) : -1;
+            }
+            const int e = __shfl_sync(0xffffffffu, entry, idx & 31);
+            const bool there = e >= 0 && e < a.num_pages;
+            holes = (holes & ~(1u << (filled % ST))) | (there ? 0u : 1u << (filled % ST));
+            const int64_t row0 = (there ? (((int64_t)e * a.Hkv) << a.page_shift) + head_row : 0) +
+                                 (key & ((1 << a.page_shift) - 1));
+            const uint32_t dst = ring + (filled % ST) * C::kStepBytes;
+#pragma unroll
+            for (int j = 0; j < kKT * D / 8 / 32; ++j) {
+                const int c = j * 32 + lane;
+                const int r = c / (D / 8), ch = c % (D / 8);
+                const bool in = there && key + r < keys && key + r >= first_key;
+                const int64_t off = (row0 + r) * D + ch * 8;
+                const uint32_t d = dst + r * D * 2 + ((ch ^ (r & 7)) << 4);
+                copy16(d, k_cache + (in ? off : 0), in);
+                copy16(d + kKT * D * 2, v_cache + (in ? off : 0), in);
+            }
+            key += kKT;
+            --left;
+        }
+        ++filled;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < ST - 1; ++i) copy_step();
+    __syncwarp();
+
+    const int g = lane >> 2, t = lane & 3;  // fragment row and column pair
+    int step = 0;
+    for (int n = 0; n < npieces; ++n) {
+        const Piece p = pieces[warp][n % kPieces];
+        // this thread's rows of the item: g and, of 16, g + 8
+        int tok[R], limit[R];
+        bool live[R];
+        const float *qrow[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int row = g + 8 * i;
+            tok[i] = row / a.G;
+            live[i] = tok[i] < p.ntok;
+            limit[i] = live[i] ? row_limit(a, p, tok[i]) : p.keys;
+            qrow[i] = a.Q + (int64_t)(p.tok0 + tok[i]) * a.ldq +
+                      (p.head * a.G + row % a.G) * D + 2 * t;
+        }
+        uint32_t qf[D / 16][S][4];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x[R][2];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float2 q =
+                        live[r] ? *reinterpret_cast<const float2 *>(qrow[r] + 16 * i + 8 * h)
+                                : make_float2(0.f, 0.f);
+                    x[r][0] = q.x * a.sign;
+                    x[r][1] = q.y * a.sign;
+                }
+                F::fill(x, 2 * h, qf[i]);
+            }
+        float o[D / 8][2 * R], m[R], l[R];
+#pragma unroll
+        for (int i = 0; i < D / 8 * 2 * R; ++i) o[i / (2 * R)][i % (2 * R)] = 0.0f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.0f;
+        }
+        int key0 = p.key0;
+        for (int it = 0; it < p.ntiles; ++it, ++step, key0 += kKT) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
+            __syncwarp();
+            const uint32_t ks = ring + (step % ST) * C::kStepBytes;
+            const uint32_t vs = ks + kKT * D * 2;
+            // logits of the rows x 16 keys
+            float s[2][2][4];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i >> 3][i >> 2 & 1][i & 3] = 0.0f;
+            {
+                const int kr = (lane >> 4) * 8 + (lane & 7), half = (lane >> 3) & 1;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    uint32_t b[4];
+                    ldsm4(b, ks + kr * D * 2 + (((2 * i + half) ^ (kr & 7)) << 4));
+#pragma unroll
+                    for (int j = 0; j < S; ++j) {
+                        mma16816<BF>(s[i & 1][0], qf[i][j], b[0], b[1]);
+                        mma16816<BF>(s[i & 1][1], qf[i][j], b[2], b[3]);
+                    }
+                }
+            }
+            // x[row][key]: keys 2t, 2t + 1, 2t + 8, 2t + 9 of the step
+            float x[R][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float c0 = s[0][e >> 1][e & 1] + s[1][e >> 1][e & 1];
+                const float c1 = s[0][e >> 1][2 + (e & 1)] + s[1][e >> 1][2 + (e & 1)];
+                if (R == 1) x[0][e] = c0 + c1;
+                else x[0][e] = c0, x[R - 1][e] = c1;
+            }
+            // keys that are masked: behind the row's own, in front of the
+            // suffix, or of a page that is missing
+            bool cut = key0 < first_key;
+#pragma unroll
+            for (int r = 0; r < R; ++r) cut = cut || key0 + kKT > limit[r];
+            const bool missing = holes >> (step % ST) & 1;
+            if (__any_sync(0xffffffffu, cut || missing)) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = key0 + 8 * (i >> 1) + 2 * t + (i & 1);
+                        if (missing || k >= limit[r] || k < first_key) x[r][i] = -INFINITY;
+                    }
+            }
+            float grow[R];
+            bool any = false;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float mx = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float mn = mx == -INFINITY ? m[r] : fmaxf(m[r], mx * a.scale);
+                any = any || mn > m[r];
+                grow[r] = mn > m[r] ? max_factor(m[r], mn) : 1.0f;
+                m[r] = mn;
+            }
+            if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) l[r] *= grow[r];
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        o[i][2 * r] *= grow[r];
+                        o[i][2 * r + 1] *= grow[r];
+                    }
+            }
+            uint32_t pf[S][4];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[r][i] = x[r][i] == -INFINITY ? 0.0f : ex2(fmaf(x[r][i], a.scale, -m[r]));
+                    l[r] += x[r][i];
+                }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float y[R][2];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    y[r][0] = x[r][2 * h];
+                    y[r][1] = x[r][2 * h + 1];
+                }
+                F::fill(y, 2 * h, pf);
+            }
+            {
+                const int kr = ((lane >> 3) & 1) * 8 + (lane & 7), half = lane >> 4;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    uint32_t b[4];
+                    ldsm4t(b, vs + kr * D * 2 + (((2 * i + half) ^ (kr & 7)) << 4));
+                    // the step's products alone go through the instruction's
+                    // accumulator, which truncates: over 512 steps that would
+                    // cost 6e-6 of the output
+                    float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+                    for (int j = 0; j < S; ++j) {
+                        mma16816<BF>(c[0], pf[j], b[0], b[1]);
+                        mma16816<BF>(c[1], pf[j], b[2], b[3]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            if (R == 1) {
+                                o[2 * i + j][q] += c[j][q] + c[j][2 + q];
+                            } else {
+                                o[2 * i + j][q] += c[j][q];
+                                o[2 * i + j][2 * R - 2 + q] += c[j][2 + q];
+                            }
+                        }
+                }
+            }
+            __syncwarp();  // the step's buffer is free
+            copy_step();
+        }
+        __syncwarp();  // the copies' next piece is in shared memory
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        }
+        if (p.npieces > 1) {
+            // this worker's part of the item, then whoever is last joins them all
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int64_t base = (int64_t)(2 * worker + p.slot) * ROWS + g + 8 * r;
+                float *d = a.part_o + base * D + 2 * t;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    __stcg(reinterpret_cast<float2 *>(d + 8 * i),
+                           make_float2(o[i][2 * r], o[i][2 * r + 1]));
+                if (t == 0) __stcg(a.part_ml + base, make_float2(m[r], l[r]));
+            }
+            __threadfence();
+            __syncwarp();
+            unsigned last = 0;
+            if (lane == 0) {
+                unsigned *count = a.counters + p.first;
+                last = atomicAdd(count, 1u) == (unsigned)p.npieces - 1;
+                if (last) *count = 0;  // as the next launch wants it
+            }
+            if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+            __threadfence();
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                m[r] = -INFINITY;
+                l[r] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) o[i][2 * r] = o[i][2 * r + 1] = 0.0f;
+                for (int c = 0; c < p.npieces; ++c) {
+                    const int64_t base =
+                        (int64_t)(2 * (p.first + c) + (c == 0)) * ROWS + g + 8 * r;
+                    const float2 f = __ldcg(a.part_ml + base);
+                    const float top = fmaxf(m[r], f.x);
+                    const float fo = max_factor(m[r], top), fp = max_factor(f.x, top);
+                    m[r] = top;
+                    l[r] = l[r] * fo + f.y * fp;
+                    const float *src = a.part_o + base * D + 2 * t;
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(src + 8 * i));
+                        o[i][2 * r] = o[i][2 * r] * fo + v.x * fp;
+                        o[i][2 * r + 1] = o[i][2 * r + 1] * fo + v.y * fp;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (!live[r]) continue;
+            const int64_t out = (int64_t)(p.tok0 + tok[r]) * a.Hq + p.head * a.G + (g + 8 * r) % a.G;
+            const RowEnd e = row_end<D>(a, out, m[r], l[r], t == 0);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                row_store(a, e, 8 * i + 2 * t, make_float2(o[i][2 * r], o[i][2 * r + 1]));
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <int D, bool BF, int ROWS>
+sq_status launch_rows(const PagedArgs &a, const void *k_cache, const void *v_cache, int sms,
+                      cudaStream_t st) {
+    using C = RowsCfg<D>;
     static std::mutex mu;
     static bool done[64] = {};
     DeviceInfo di;
@@ -413,31 +426,32 @@ sq_status launch_rows(const PagedArgs &a, const CUtensorMap &mk, const CUtensorM
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!done[di.device & 63]) {
-            if (cudaFuncSetAttribute(paged_rows_kernel<D, BF, RG>,
+            if (cudaFuncSetAttribute(paged_rows_kernel<D, BF, ROWS>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      C::kSmem) != cudaSuccess)
                 return SQ_ERR_CUDA;
             done[di.device & 63] = true;
         }
     }
-    return launch_pdl(paged_rows_kernel<D, BF, RG>, dim3((unsigned)sms), dim3(C::kThreads),
-                      C::kSmem, st, 1, mk, mv, a, bx);
+    return launch_pdl(paged_rows_kernel<D, BF, ROWS>, dim3((unsigned)sms), dim3(kWarps * 32),
+                      C::kSmem, st, 1, a, static_cast<const uint16_t *>(k_cache),
+                      static_cast<const uint16_t *>(v_cache));
 }
 
 }  // namespace
 
-sq_status launch_paged_rows(const PagedArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
-                            int D, bool bf16, int row_groups, int bx, int sms, cudaStream_t st) {
-    const int v = (D == 128 ? 4 : 0) + (bf16 ? 2 : 0) + (row_groups == 2 ? 1 : 0);
+sq_status launch_paged_rows(const PagedArgs &a, const void *k_cache, const void *v_cache, int D,
+                            bool bf16, int rows, int sms, cudaStream_t st) {
+    const int v = (D == 128 ? 4 : 0) + (bf16 ? 2 : 0) + (rows == 16 ? 1 : 0);
     switch (v) {
-    case 0: return launch_rows<64, false, 1>(a, mk, mv, bx, sms, st);
-    case 1: return launch_rows<64, false, 2>(a, mk, mv, bx, sms, st);
-    case 2: return launch_rows<64, true, 1>(a, mk, mv, bx, sms, st);
-    case 3: return launch_rows<64, true, 2>(a, mk, mv, bx, sms, st);
-    case 4: return launch_rows<128, false, 1>(a, mk, mv, bx, sms, st);
-    case 5: return launch_rows<128, false, 2>(a, mk, mv, bx, sms, st);
-    case 6: return launch_rows<128, true, 1>(a, mk, mv, bx, sms, st);
-    default: return launch_rows<128, true, 2>(a, mk, mv, bx, sms, st);
+    case 0: return launch_rows<64, false, 8>(a, k_cache, v_cache, sms, st);
+    case 1: return launch_rows<64, false, 16>(a, k_cache, v_cache, sms, st);
+    case 2: return launch_rows<64, true, 8>(a, k_cache, v_cache, sms, st);
+    case 3: return launch_rows<64, true, 16>(a, k_cache, v_cache, sms, st);
+    case 4: return launch_rows<128, false, 8>(a, k_cache, v_cache, sms, st);
+    case 5: return launch_rows<128, false, 16>(a, k_cache, v_cache, sms, st);
+    case 6: return launch_rows<128, true, 8>(a, k_cache, v_cache, sms, st);
+    default: return launch_rows<128, true, 16>(a, k_cache, v_cache, sms, st);
     }
 }
 

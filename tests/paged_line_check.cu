@@ -1,8 +1,8 @@
 // Host-only check of the paged attention's division of work (paged_line.cuh),
 // run on the CPU by tests/test_paged_line.py: for random batches, head counts,
-// tile sizes and CTA counts, the pieces that all CTAs walk cover every (row
+// tile sizes and worker counts, the pieces that all workers walk cover every (row
 // tile, key/value head, key tile) exactly once, in order; the pieces of a split
-// item name the CTAs that hold them, two partial slots per CTA are enough, and
+// item name the workers that hold them, two partial slots per worker are enough, and
 // the counter of a split item is nobody else's.  Prints a summary line; exit
 // status 1 on any failure.
 #include "paged_line.cuh"
@@ -49,17 +49,17 @@ static void check(PagedArgs a, int grid, int min_pairs) {
     const int64_t total = (int64_t)line.size();
     if (total == 0) return;
     const int64_t fit = (total + min_pairs - 1) / min_pairs;
-    const int ctas = fit < grid ? (int)fit : grid;
+    const int workers = fit < grid ? (int)fit : grid;
     int64_t at = 0;
-    std::map<int, std::tuple<int, int, int>> counter;          // first CTA -> split item
-    std::map<std::tuple<int, int, int>, std::vector<int>> parts;  // split item -> CTAs
+    std::map<int, std::tuple<int, int, int>> counter;          // first worker -> split item
+    std::map<std::tuple<int, int, int>, std::vector<int>> parts;  // split item -> workers
     std::map<std::tuple<int, int, int>, int> want;
-    for (int c = 0; c < ctas; ++c) {
+    for (int c = 0; c < workers; ++c) {
         Share sh;
         sh.total = total;
-        sh.ctas = ctas;
-        sh.begin = share_begin(total, ctas, c);
-        sh.end = share_begin(total, ctas, c + 1);
+        sh.workers = workers;
+        sh.begin = share_begin(total, workers, c);
+        sh.end = share_begin(total, workers, c + 1);
         CHECK(sh.begin == at && sh.end > sh.begin);
         sh.seq = 0;
         for (int b = 0; b < nb; ++b)
@@ -86,14 +86,14 @@ static void check(PagedArgs a, int grid, int min_pairs) {
             if (!whole) {
                 CHECK(p.slot >= 0 && p.slot < 2 && !slots[p.slot]);
                 slots[p.slot] = true;
-                // the joiner reads slot 1 of the first CTA and slot 0 of the others
-                CHECK((c == p.first_cta) == (p.slot == 1));
-                CHECK(!counter.count(p.first_cta) || counter[p.first_cta] == item);
-                counter[p.first_cta] = item;
+                // the joiner reads slot 1 of the first worker and slot 0 of the others
+                CHECK((c == p.first) == (p.slot == 1));
+                CHECK(!counter.count(p.first) || counter[p.first] == item);
+                counter[p.first] = item;
                 parts[item].push_back(c);
                 want[item] = p.npieces;
                 CHECK(parts[item].size() ==
-                      (size_t)(c - p.first_cta + 1));  // every CTA between holds a piece
+                      (size_t)(c - p.first + 1));  // every worker between holds a piece
             }
             at += p.ntiles;
         }
@@ -102,9 +102,9 @@ static void check(PagedArgs a, int grid, int min_pairs) {
     CHECK(at == total);
     for (auto &e : parts) CHECK((int)e.second.size() == want[e.first]);
     for (int64_t x = 0; x < total; x += 1 + total / 97) {
-        const int c = share_of(total, ctas, x);
-        CHECK(c >= 0 && c < ctas && share_begin(total, ctas, c) <= x &&
-              x < share_begin(total, ctas, c + 1));
+        const int c = share_of(total, workers, x);
+        CHECK(c >= 0 && c < workers && share_begin(total, workers, c) <= x &&
+              x < share_begin(total, workers, c + 1));
     }
 }
 
@@ -118,7 +118,7 @@ int main() {
         a.G = pick(1, 8);
         const int rows = trial % 2 ? 256 : (trial % 4 ? 8 : 16);
         a.tpt = std::max(1, rows / a.G);
-        const int KT = trial % 2 ? 128 : 64;
+        const int KT = trial % 2 ? 128 : 16;
         const int page = 16 << pick(0, 4);
         a.max_pages = pick(0, 3000 / page);
         a.cap = (int)(a.max_pages * page);
@@ -142,7 +142,7 @@ int main() {
             a.prefix_phase = phase;
             a.kstart = phase ? 0 : a.prefix_len / KT * KT;
             const int grid = pick(1, 152), least = pick(1, 4);
-            if (KT == 64) check<64>(a, grid, least);
+            if (KT == 16) check<16>(a, grid, least);
             else check<128>(a, grid, least);
         }
     }
