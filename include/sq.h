@@ -216,7 +216,7 @@ sq_status sq_rmsnorm_quant(const float *H, const float *residual, const float *g
  *   block_table [B][max_pages]  the page of positions page_size n ..
  *                      page_size n + page_size - 1 in column n.
  * Hq query heads share Hkv key/value heads in groups of G = Hq / Hkv
- * consecutive ones (Hq a multiple of Hkv, G <= 16, Hq <= 4096).  D is 64 or
+ * consecutive ones (Hq a multiple of Hkv, G <= 128, Hq <= 4096).  D is 64 or
  * 128; page_size 16, 32, 64, 128 or 256.  T, B, max_pages * page_size and
  * num_pages * Hkv * page_size at most 2^30 (SQ_ERR_UNSUPPORTED beyond).
  * The contents of the device arrays are not checked on the host; whatever they

@@ -94,7 +94,7 @@ sq_status check_paged_shape(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int c
         page_size != 256)
         return SQ_ERR_UNSUPPORTED;
     if (Hq % Hkv != 0) return SQ_ERR_INVALID_ARG;
-    if (Hq > 4096 || Hq / Hkv > 16) return SQ_ERR_UNSUPPORTED;
+    if (Hq > 4096 || Hq / Hkv > 128) return SQ_ERR_UNSUPPORTED;
     if (ldq < Hq * D) return SQ_ERR_INVALID_ARG;
     if (ldq % 4 != 0) return SQ_ERR_ALIGNMENT;
     // token, sequence, key and cache-row numbers are 32-bit; element offsets are not

@@ -22,18 +22,22 @@ __device__ __forceinline__ float max_factor(float a, float b) {
 }
 
 // N pairs of 16-bit numbers of the cache's type that sum to (a, b), a in the
-// low half: each is the rounding of what the ones before it left.  Two bf16
-// numbers are within 2^-18 of the value (relative), three within 2^-27, two
-// fp16 numbers within 2^-22.
+// low half.  Three bf16 numbers hold an fp32 number exactly: each takes the
+// next 8 bits of its significand, by masking (the conversion instructions run
+// at a quarter of the rate).  Two fp16 numbers are within 2^-22 of it, each the
+// rounding of what is left.
 template <bool BF, int N>
 __device__ __forceinline__ void split16(float a, float b, uint32_t (&w)[N]) {
+    static_assert(N == (BF ? 3 : 2), "parts of an fp32 number");
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         if (BF) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-            w[i] = *reinterpret_cast<const uint32_t *>(&h);
-            a -= __low2float(h);
-            b -= __high2float(h);
+            const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+            w[i] = __byte_perm(ua, ub, 0x7632);  // the two high halves
+            if (i + 1 < N) {
+                a -= __uint_as_float(ua & 0xffff0000u);
+                b -= __uint_as_float(ub & 0xffff0000u);
+            }
         } else {
             const __half2 h = __floats2half2_rn(a, b);
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
@@ -47,7 +51,7 @@ __device__ __forceinline__ void split16(float a, float b, uint32_t (&w)[N]) {
 // c is number w gridDim.x + c, so that neighbours on the line are on different
 // SMs), by all NT threads: each sums a run of sequences, a scan over the
 // threads places them.
-template <int KT, int NT, int W>
+template <int KT, int PAD, int NT, int W>
 __device__ __forceinline__ void find_shares(const PagedArgs &a, int min_pairs, Share *out) {
     __shared__ int64_t warp_sum[NT / 32];
     const int nb = a.prefix_phase ? 1 : a.B;
@@ -56,7 +60,7 @@ __device__ __forceinline__ void find_shares(const PagedArgs &a, int min_pairs, S
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) {
         const Seq s = load_seq(a, b);
-        mine += a.Hkv * key_tiles_before<KT>(a, s, row_tiles(a, s));
+        mine += a.Hkv * pairs_before<KT, PAD>(a, s, row_tiles(a, s));
     }
     int64_t incl = mine;
 #pragma unroll
@@ -84,7 +88,7 @@ __device__ __forceinline__ void find_shares(const PagedArgs &a, int min_pairs, S
             int b = b0;
             for (; b < b1 - 1; ++b) {
                 const Seq s = load_seq(a, b);
-                const int64_t n = a.Hkv * key_tiles_before<KT>(a, s, row_tiles(a, s));
+                const int64_t n = a.Hkv * pairs_before<KT, PAD>(a, s, row_tiles(a, s));
                 if (begin < at + n) break;
                 at += n;
             }
@@ -161,10 +165,30 @@ __device__ __forceinline__ void row_store(const PagedArgs &a, const RowEnd &e, i
     *reinterpret_cast<float2 *>(a.O + e.at + col) = r;
 }
 
+// four columns of a row (o scaled by RowEnd::own) to the prefix's buffer or,
+// joined with it, to the output
+__device__ __forceinline__ void finish4(const PagedArgs &a, int64_t at, float front, float4 o) {
+    if (a.prefix_phase) {
+        *reinterpret_cast<float4 *>(a.prefix_o + at) = o;
+        return;
+    }
+    if (a.prefix_len > 0) {
+        const float4 f = *reinterpret_cast<const float4 *>(a.prefix_o + at);
+        o.x += f.x * front;
+        o.y += f.y * front;
+        o.z += f.z * front;
+        o.w += f.w * front;
+    }
+    *reinterpret_cast<float4 *>(a.O + at) = o;
+}
+
 }  // namespace
 
 // The kernel for at most 16 rows per item (paged_rows.cu): rows = 8 or 16.
 sq_status launch_paged_rows(const PagedArgs &a, const void *k_cache, const void *v_cache, int D,
                             bool bf16, int rows, int sms, cudaStream_t st);
+// The kernel for up to 256 rows per item (paged_tiles.cu).
+sq_status launch_paged_tiles(const PagedArgs &a, const void *k_cache, const void *v_cache, int D,
+                             bool bf16, int sms, cudaStream_t st);
 
 }  // namespace sq

@@ -11,7 +11,7 @@ namespace {
 __device__ unsigned int g_paged_error;
 
 constexpr int64_t kCounterBytes = 16384;
-constexpr int64_t kPieceRows = 256;  // rows of a partial result, the largest kernel's
+constexpr int64_t kPieceRows = 128;  // rows of a partial result, the largest kernel's
 
 // Device address of the error word, looked up on a device's first call.
 sq_status error_word(int device, unsigned **out) {
@@ -82,23 +82,28 @@ sq_status launch_paged_attention(const PagedCall &c, cudaStream_t st) {
     a.Hq = (int)c.Hq;
     a.Hkv = (int)c.Hkv;
     a.G = (int)(c.Hq / c.Hkv);
+    a.g_inv = (65536 + a.G - 1) / a.G;  // n e < 2^16 for the excess e < G of g_inv G over 2^16
     a.num_pages = (int)c.num_pages;
     a.page_shift = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6
                    : c.page_size == 128 ? 7 : 8;
     a.prefix_len = (int)c.prefix_len;
     a.cap = (int)(c.max_pages * c.page_size);
-    a.scale = fabsf(c.scale) * 1.4426950408889634f;
+    // (not zero: a masked logit's -inf stays -inf under it)
+    a.scale = std::max(fabsf(c.scale) * 1.4426950408889634f, 1e-30f);
     a.sign = c.scale < 0.0f ? -1.0f : 1.0f;
     const bool bf16 = c.cache_type == SQ_CACHE_BF16;
     for (int phase = c.prefix_len > 0 ? 1 : 0; phase >= 0; --phase) {
         a.prefix_phase = phase;
-        const int64_t most = (phase ? c.T : c.max_q) * a.G;
-        const int r = most <= 8 ? 8 : 16;
-        a.tpt = std::max(1, r / a.G);
-        a.kstart = phase ? 0 : a.prefix_len / 16 * 16;
-        if ((rc = launch_paged_rows(a, c.k_cache, c.v_cache, (int)c.D, bf16, r, di.sms, st)) !=
-            SQ_OK)
-            return rc;
+        const int64_t most = std::max<int64_t>(1, phase ? c.T : std::min(c.max_q, c.T)) * a.G;
+        // up to 16 rows per key/value head: the warp-level products; more: tensor
+        // memory's
+        const bool few = most <= 16;
+        const int r = few ? (most <= 8 ? 8 : 16) : 128, kt = few ? 16 : 128;
+        a.tpt = r / a.G;
+        a.kstart = phase ? 0 : a.prefix_len / kt * kt;
+        rc = few ? launch_paged_rows(a, c.k_cache, c.v_cache, (int)c.D, bf16, r, di.sms, st)
+                 : launch_paged_tiles(a, c.k_cache, c.v_cache, (int)c.D, bf16, di.sms, st);
+        if (rc != SQ_OK) return rc;
     }
     return SQ_OK;
 }

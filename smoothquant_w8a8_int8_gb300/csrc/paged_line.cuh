@@ -5,9 +5,10 @@
 // An item is a tile of query rows (tokens x heads of one key/value
 // head's group) of one sequence and one key/value head; its keys are cut into
 // tiles of KT.  All (item, key tile) pairs stand in one line -- sequences,
-// then row tiles, then key/value heads, then key tiles -- and worker c of n (a
-// CTA, or a warp) takes pairs [c W / n, (c + 1) W / n): every worker has the
-// same share whatever the lengths, known only on the device, are.  An item that
+// then row tiles, then key/value heads, then key tiles -- each item's followed
+// by PAD pairs without work that stand for the time of its start and end, and
+// worker c of n (a CTA, or a warp) takes pairs [c W / n, (c + 1) W / n): every
+// worker has the same share whatever the lengths, known only on the device, are.  An item that
 // lies in several workers' shares leaves one partial result (row maximum, sum,
 // unnormalised output) per worker in the workspace; the one that arrives last
 // (a counter) joins them in the order of the line, so that the result does not
@@ -32,6 +33,7 @@ struct PagedArgs {
     unsigned *error;     // the library's error word
     int T, B, Hq, Hkv, G;
     int tpt;             // tokens per row tile
+    int g_inv;           // ceil(2^16 / G): n / G = n g_inv >> 16 for n < 256
     int num_pages, page_shift;
     int prefix_len;
     int kstart;          // first key of the suffix's first key tile
@@ -100,19 +102,21 @@ SQ_HD int64_t floor_sum(int64_t n, int64_t m, int64_t p, int64_t q) {
     }
     return total;
 }
-// key tiles of the first J row tiles
-template <int KT>
-SQ_HD int64_t key_tiles_before(const PagedArgs &a, const Seq &s, int J) {
-    if (a.prefix_phase) return (int64_t)J * key_tiles<KT>(a, s, 0);
+// pairs of one key/value head's items over the first J row tiles
+template <int KT, int PAD>
+SQ_HD int64_t pairs_before(const PagedArgs &a, const Seq &s, int J) {
+    if (a.prefix_phase) return (int64_t)J * (key_tiles<KT>(a, s, 0) + PAD);
     const int tiles = row_tiles(a, s);
     const int whole = at_most(J, tiles - 1);  // the last row tile may hold fewer tokens
-    if (whole <= 0) return J > 0 ? key_tiles<KT>(a, s, J - 1) : 0;
-    const int64_t base = s.kv - s.qlen - a.kstart;
-    // row tiles whose keys fit one key tile: base + (j + 1) tpt <= KT
-    int64_t ones = KT - base < 0 ? 0 : (KT - base) / a.tpt;
-    ones = ones < whole ? ones : whole;
-    int64_t sum = ones + floor_sum(whole - ones, KT, a.tpt, base + (ones + 1) * a.tpt + KT - 1);
-    if (J > whole) sum += key_tiles<KT>(a, s, J - 1);
+    int64_t sum = (int64_t)J * PAD;
+    if (whole > 0) {
+        const int64_t base = s.kv - s.qlen - a.kstart;
+        // row tiles whose keys fit one key tile: base + (j + 1) tpt <= KT
+        int64_t ones = KT - base < 0 ? 0 : (KT - base) / a.tpt;
+        ones = ones < whole ? ones : whole;
+        sum += ones + floor_sum(whole - ones, KT, a.tpt, base + (ones + 1) * a.tpt + KT - 1);
+    }
+    if (J > whole && J > 0) sum += key_tiles<KT>(a, s, J - 1);
     return sum;
 }
 
@@ -145,13 +149,13 @@ struct Piece {
 };
 
 // Walks the pieces of a worker's share.
-template <int KT>
+template <int KT, int PAD>
 struct Walk {
     int64_t at, end;  // position, end of the share
     int b, j, h, k;
     Seq s;
     int tiles, nk;
-    int64_t before;  // key tiles of the sequence's row tiles before j
+    int64_t before;  // pairs_before of row tile j
 
     SQ_HD void enter(const PagedArgs &a) {
         s = load_seq(a, b);
@@ -167,18 +171,38 @@ struct Walk {
         int lo = 0, hi = tiles - 1;  // the last row tile that starts at or before rem
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
-            if (a.Hkv * key_tiles_before<KT>(a, s, mid) <= rem) lo = mid;
+            if (a.Hkv * pairs_before<KT, PAD>(a, s, mid) <= rem) lo = mid;
             else hi = mid - 1;
         }
         j = lo;
-        before = key_tiles_before<KT>(a, s, j);
+        before = pairs_before<KT, PAD>(a, s, j);
         nk = key_tiles<KT>(a, s, j);
         const int64_t r = rem - a.Hkv * before;
-        h = (int)(r / nk);
-        k = (int)(r % nk);
+        h = (int)(r / (nk + PAD));
+        k = (int)(r % (nk + PAD));
+    }
+    // on to the next item
+    SQ_HD void advance(const PagedArgs &a) {
+        k = 0;
+        if (++h < a.Hkv) return;
+        h = 0;
+        before += nk + PAD;
+        if (++j == tiles && at < end) {
+            do {  // the next sequence with a row
+                ++b;
+                enter(a);
+            } while (tiles == 0 && b < a.B - 1);
+            j = 0;
+            before = 0;
+        }
+        if (j < tiles) nk = key_tiles<KT>(a, s, j);
     }
     // the next piece, or false at the end of the share
     SQ_HD bool next(const PagedArgs &a, const Share &sh, Piece &p) {
+        if (at < end && k >= nk) {  // among an item's pairs without work
+            at += nk + PAD - k;
+            advance(a);
+        }
         if (at >= end) return false;
         const int64_t left = end - at;
         const int take = left < nk - k ? (int)left : nk - k;
@@ -197,21 +221,8 @@ struct Walk {
         at += take;
         k += take;
         if (k == nk) {
-            k = 0;
-            if (++h == a.Hkv) {
-                h = 0;
-                before += nk;
-                ++j;
-                if (j == tiles && at < end) {
-                    do {  // the next sequence with a row
-                        ++b;
-                        enter(a);
-                    } while (tiles == 0 && b < a.B - 1);
-                    j = 0;
-                    before = 0;
-                }
-                if (j < tiles) nk = key_tiles<KT>(a, s, j);
-            }
+            at += PAD;
+            advance(a);
         }
         return true;
     }

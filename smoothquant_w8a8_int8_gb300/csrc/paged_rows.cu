@@ -21,8 +21,8 @@
 // each per SM quarter): 16 rows are too few for tensor memory's 128.
 //
 // Precision: keys and values enter as stored.  The fp32 queries and
-// probabilities are split over several 16-bit numbers (split16): two for fp16,
-// three for bf16, so that what is lost (2^-22) is no more than fp32 sums lose.
+// probabilities are split over several 16-bit numbers (split16): two for fp16
+// (within 2^-22), three for bf16 (exact).
 // Up to 8 rows, two of the parts share an instruction's 16 rows (the first in
 // rows 0-7, the second in rows 8-15) and the two halves are added in fp32.
 #include "paged.cuh"
@@ -35,6 +35,7 @@ namespace {
 
 constexpr int kKT = 16;       // keys per step
 constexpr int kWarps = 8;
+constexpr int kPad = 2;       // an item's start and end, in steps
 constexpr int kMinSteps = 4;  // steps of a worker's share at least
 constexpr int kPieces = 8;    // more than the steps that the copies are ahead
 
@@ -126,14 +127,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_launch_dependents();
     pdl_wait();  // every global-memory access below follows the previous kernel
-    find_shares<kKT, kWarps * 32, kWarps>(a, kMinSteps, shares);
+    find_shares<kKT, kPad, kWarps * 32, kWarps>(a, kMinSteps, shares);
     const Share &share = shares[warp];
     const int worker = warp * gridDim.x + blockIdx.x;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * ST * C::kStepBytes;
     const int first_key = a.prefix_phase ? 0 : a.prefix_len;
 
     // ---- the copies: one step of the share per call, or nothing at its end
-    Walk<kKT> walk;
+    Walk<kKT, kPad> walk;
     walk.start(a, share);
     int npieces = 0, left = 0, key = 0, held = -1, entry = -1, filled = 0;
     int64_t head_row = 0;  // the piece's head, in cache rows of a page

@@ -1,0 +1,876 @@
+// Attention over the paged cache for many query rows per key/value head, on the
+// 5th-generation tensor cores (tcgen05): prompts, chunks of prompts, drafts of
+// many heads, and the prefix that a batch shares.
+//
+// An item is up to 128 query rows (tokens x heads of a group, the instruction's
+// M) of one sequence and key/value head; its keys come in tiles of 128.  Per
+// tile: S = Q K^T into tensor memory; the softmax of the tile alone, two threads
+// per row, whose probabilities take S's place; P V into a second area of tensor
+// memory; and from there into the output in registers,
+//   O = O 2^(M - M') + (P V) 2^(m - M'),   M' = max(M, m),
+// m the tile's row maximum, M the output's.  Since a tile's softmax knows
+// nothing of the tiles before it, all four steps run at once on different
+// tiles: the products of tile t + 1 and t - 1, the softmax of tile t, the sum of
+// tile t - 2, and across items too.  The sum is formed outside the tensor cores,
+// whose accumulator truncates: kept there over the 64 tiles of 8192 keys it
+// would be off by 6e-6.
+//
+// Precision.  Keys and values enter as stored; fp32 queries and probabilities
+// are split in 16-bit numbers of their type, one instruction per part: two for
+// fp16 (within 2^-22), three for bf16 (exact; two would leave 2^-17).
+// The probabilities of a tile carry a factor 2^12, and fp16 queries are scaled
+// row by row by a power of two, so that no part falls below fp16's range.
+//
+// Bound: the products, at twice (fp16) or three times (bf16) the instructions
+// of the plain operands' attention.
+//
+// Roles (640 threads, one persistent CTA per SM):
+//   warps 0-3, 4-7   queries and softmax, 64 keys of a tile each;
+//   warps 8-11       the output: sum over the tiles, partial results, rows;
+//   warps 12-15      copies: keys and values with cp.async into a ring of
+//                    128-row slots in the operands' layout (128-byte swizzle;
+//                    rows of no key are zeros);
+//   warp 16          tensor memory, and lane 0 issues the products;
+//   warp 17          walks the CTA's share and hands its pieces to the others.
+// Tensor memory, 512 columns: two areas of 64 columns per part for S and then P,
+// and two areas (bf16: one) of 128 for P V.
+// Every wait is bounded (4 s); on expiry the CTA records an error for
+// sq_device_status, lets its copies and products land and exits.
+#include "paged.cuh"
+
+#include <algorithm>
+#include <mutex>
+
+namespace sq {
+namespace {
+
+constexpr unsigned long long kPagedTimeoutNs = 4000000000ull;
+
+__device__ __forceinline__ uint32_t su32(const void *p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ uint64_t gtime() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+__device__ __forceinline__ void bar_init(uint64_t *bar, unsigned count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(bar)), "r"(count));
+}
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort,
+                                       unsigned *error) {
+    const uint64_t t0 = gtime();
+    for (uint32_t it = 1;; ++it) {
+        if (try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*abort) return false;
+            if (gtime() - t0 > kPagedTimeoutNs) {
+                *abort = 1;
+                atomicOr(error, 1u);
+                return false;
+            }
+        }
+    }
+}
+// Bounded wait for the phase of parity `parity`; false when the CTA aborted.
+__device__ __forceinline__ bool wait_bar(const uint64_t *bar, uint32_t parity,
+                                         volatile int *abort, unsigned *error) {
+    const uint32_t a = su32(bar);
+    if (try_wait(a, parity)) return true;
+    return wait_slow(a, parity, abort, error);
+}
+// Every lane waits (so that every lane sees what the barrier publishes); the
+// outcome is the warp's.
+__device__ __forceinline__ bool warp_wait(const uint64_t *bar, uint32_t parity,
+                                          volatile int *abort, unsigned *error) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, error)) != 0;
+}
+__device__ __forceinline__ void drain_bar(const uint64_t *bar, uint32_t parity,
+                                          unsigned *error) {
+    const uint32_t a = su32(bar);
+    const uint64_t t0 = gtime();
+    while (!try_wait(a, parity))
+        if (gtime() - t0 > kPagedTimeoutNs) {
+            atomicOr(error, 2u);
+            return;
+        }
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(bar)) : "memory");
+}
+
+constexpr int kKT = 128;     // keys per tile
+constexpr int kRows = 128;   // query rows per item
+constexpr int kThreads = 640;
+constexpr int kItems = 4;    // pieces the walk may be ahead
+constexpr int kStats = 4;    // tiles whose maxima and sums are kept
+constexpr int kMiss = 8;     // more than the tiles between a copy and its softmax
+constexpr int kPad = 2;      // an item's start and end, in key tiles
+constexpr int kMinTiles = 1; // key tiles of a CTA's share at least
+constexpr float kBias = 12.0f;  // log2 of the probabilities' factor
+
+template <int D, bool BF>
+struct TilesCfg {
+    static constexpr int kParts = BF ? 3 : 2;
+    static constexpr int kSlab = kKT * 128;            // 128 rows x 64 elements
+    static constexpr int kSlot = kSlab * (D / 64);     // keys or values of a tile
+    static constexpr int kSlots = D == 64 ? 6 : BF ? 3 : 4;
+    static constexpr int kQPart = kRows * D * 2;       // one part of the queries
+    static constexpr int kSmem = kParts * kQPart + kSlots * kSlot + 1024;
+    // tensor memory: S and P of a tile, S's first column in it, P V
+    static constexpr int kArea = 64 * kParts;
+    static constexpr int kS0 = kArea - 128;
+    static constexpr int kPVs = BF ? 1 : 2;
+    static constexpr int kPV0 = 2 * kArea;
+};
+
+struct TileBars {
+    uint64_t full[6], empty[6];
+    uint64_t item_full[kItems], item_empty[kItems];
+    uint64_t q_full, q_empty, s_full[2], p_full[2], pv_full[2], pv_empty[2], group, pair[4], mma_done;
+    uint32_t tmem;
+    int abort_flag;
+    int last;
+    unsigned miss[kMiss];  // bit i: keys 16 i .. 16 i + 15 of the tile are of a missing page
+    Piece items[kItems];
+    int stop[kItems];
+    Share share;
+    float2 stat[kStats][2][kRows];  // a tile's row maxima (log2 units) and half sums
+    float half_max[2][2][kRows];    // a tile's row maxima over its halves
+    float qmul[2][kRows];        // what the rows' queries were divided by
+};
+
+__device__ __forceinline__ void fence_async_smem() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void tc_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// shared-memory operand, 128-byte swizzle: 8-row atoms of 1024 bytes; `lead` is
+// the distance of 64-element groups of an operand that is not K-major
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lead) {
+    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(lead >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+// kind::f16: fp32 sums of bf16 or fp16 operands, M = 128
+__host__ __device__ constexpr uint32_t idesc_f16(int n, bool bf16, bool b_by_rows) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_by_rows ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// A from tensor memory: 8 columns hold K = 16
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+            su32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+// 2^e, e in [-126, 127]
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+// The multiple of 8 that scales numbers whose largest has the exponent e into
+// fp16's range, the largest into [2^8, 2^16); tiny and zero rows as if e = -32.
+__device__ __forceinline__ int shift_of(int e) { return (max(e, -32) - 8) & ~7; }
+template <int D, bool BF>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_tiles_kernel(const __grid_constant__ PagedArgs a, const uint16_t *__restrict__ k_cache,
+                       const uint16_t *__restrict__ v_cache) {
+    using C = TilesCfg<D, BF>;
+    constexpr int NS = C::kSlots, NP = C::kParts;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    __shared__ TileBars B;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int *abort = &B.abort_flag;
+    const uint32_t qbase = su32(smem);  // [part][slab][128 rows][128 B]
+    const uint32_t ring = qbase + NP * C::kQPart;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            bar_init(&B.full[i], 4);
+            bar_init(&B.empty[i], 1);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            bar_init(&B.item_full[i], 1);
+            bar_init(&B.item_empty[i], 17);
+        }
+        bar_init(&B.q_full, 8);
+        bar_init(&B.q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&B.s_full[i], 1);
+            bar_init(&B.p_full[i], 8);
+            bar_init(&B.pv_full[i], 1);
+            bar_init(&B.pv_empty[i], 4);
+        }
+        bar_init(&B.group, 4);
+        for (int i = 0; i < 4; ++i) bar_init(&B.pair[i], 2);
+        bar_init(&B.mma_done, 1);
+        B.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 16) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         su32(&B.tmem)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    pdl_launch_dependents();
+    pdl_wait();  // every global-memory access below follows the previous kernel
+    find_shares<kKT, kPad, kThreads, 1>(a, kMinTiles, &B.share);
+    const uint32_t tmem = B.tmem;
+    const int first_key = a.prefix_phase ? 0 : a.prefix_len;
+
+    // registers: 96 a thread at launch; (2 x 104 + 160 + 56 + 48) x 128 in all
+    if (warp >= 16) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (warp == 16 && lane == 0) {
+            // ------------------------------------------------------ products
+            // per tile t of the share: S(t + 1) is issued before P V(t)
+            const uint32_t qk_desc = idesc_f16(kKT, BF, false), pv_desc = idesc_f16(D, BF, true);
+            uint32_t item = 0;        // pieces begun
+            int left = 0;             // tiles of the piece still without S
+            uint32_t t_s = 0, t_pv = 0;  // tiles with S, with P V issued
+            // slots in the copies' order: K0, then K(t + 1), V(t), ..., the last V
+            bool ok = true, more = true;
+            auto next_s = [&]() {
+                if (left == 0) {
+                    const int it = item % kItems;
+                    ok = wait_bar(&B.item_full[it], (item / kItems) & 1u, abort, a.error);
+                    if (!ok) return;
+                    more = !B.stop[it];
+                    if (!more) return;
+                    left = B.items[it].ntiles;
+                    bar_arrive(&B.item_empty[it]);
+                    ok = wait_bar(&B.q_full, item & 1u, abort, a.error);
+                    if (!ok) return;
+                    ++item;
+                }
+                const uint32_t ks = t_s == 0 ? 0 : 2 * t_s - 1;
+                ok = wait_bar(&B.full[ks % NS], (ks / NS) & 1u, abort, a.error);
+                if (!ok) return;
+                tc_after();
+                const uint32_t kb = ring + (ks % NS) * C::kSlot;
+                const uint32_t d = tmem + (t_s & 1) * C::kArea + C::kS0;
+                // the smallest part first: what the accumulator truncates is relative
+                // to the sum so far
+#pragma unroll 1
+                for (int part = NP - 1; part >= 0; --part) {
+                    const uint32_t q = qbase + part * C::kQPart;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+                        mma_ss(d, desc_sw128(q + (i / 4) * C::kSlab, 16) + 2 * (i % 4),
+                               desc_sw128(kb + (i / 4) * C::kSlab, 16) + 2 * (i % 4), qk_desc,
+                               (part < NP - 1 || i) ? 1u : 0u);
+                }
+                if (--left == 0) mma_commit(&B.q_empty);  // (before the softmax can go on)
+                mma_commit(&B.s_full[t_s & 1]);
+                mma_commit(&B.empty[ks % NS]);
+                ++t_s;
+            };
+            next_s();
+            while (ok && t_pv < t_s) {
+                if (more) next_s();
+                if (!ok) break;
+                // the last tile's values follow their keys at once
+                const uint32_t vs = t_pv + 1 < t_s ? 2 * t_pv + 2 : 2 * t_pv + 1;
+                const uint32_t pb = t_pv % C::kPVs;
+                ok = wait_bar(&B.full[vs % NS], (vs / NS) & 1u, abort, a.error) &&
+                     wait_bar(&B.p_full[t_pv & 1], (t_pv >> 1) & 1u, abort, a.error) &&
+                     (t_pv < C::kPVs || wait_bar(&B.pv_empty[pb], (t_pv / C::kPVs - 1) & 1u,
+                                                 abort, a.error));
+                if (!ok) break;
+                tc_after();
+                const uint32_t d = tmem + C::kPV0 + 128 * pb;
+                const uint32_t pa = tmem + (t_pv & 1) * C::kArea;
+                const uint32_t v = ring + (vs % NS) * C::kSlot;
+#pragma unroll 1
+                for (int part = NP - 1; part >= 0; --part)
+#pragma unroll
+                    for (int i = 0; i < kKT / 16; ++i)
+                        mma_ts(d, pa + 8 * NP * i + 8 * part, desc_sw128(v + i * 2048, C::kSlab),
+                               pv_desc, (part < NP - 1 || i) ? 1u : 0u);
+                mma_commit(&B.pv_full[pb]);
+                mma_commit(&B.empty[vs % NS]);
+                ++t_pv;
+            }
+            // every product issued completes before tensor memory is freed
+            mma_commit(&B.mma_done);
+            drain_bar(&B.mma_done, 0, a.error);
+        } else if (warp == 17) {
+            // -------------------------------------------- the share's pieces
+            Walk<kKT, kPad> walk;
+            walk.start(a, B.share);
+            for (uint32_t n = 0;; ++n) {
+                Piece p;
+                const bool more = walk.next(a, B.share, p);
+                const int it = n % kItems;
+                if (n >= kItems &&
+                    !warp_wait(&B.item_empty[it], (n / kItems - 1) & 1u, abort, a.error))
+                    break;
+                if (lane == 0) {
+                    B.stop[it] = !more;
+                    if (more) B.items[it] = p;
+                    bar_arrive(&B.item_full[it]);
+                }
+                __syncwarp();
+                if (!more) break;
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        // ------------------------------------------------------------ copies
+        const int ct = threadIdx.x - 384;
+        constexpr int kChunks = kKT * D / 8 / 128;  // 16-byte chunks of a slot per thread
+        uint32_t seq = 0, done = 0, tile = 0;  // slots begun, slots handed over, tiles begun
+        bool ok = true;
+        auto hand_over = [&](bool all) {
+            if (all) asm volatile("cp.async.wait_group 0;" ::: "memory");
+            else asm volatile("cp.async.wait_group 1;" ::: "memory");
+            fence_async_smem();
+            __syncwarp();
+            while (done < seq - (all ? 0 : 1)) {
+                if (lane == 0) bar_arrive(&B.full[done % NS]);
+                ++done;
+            }
+        };
+        // 128 rows of a cache from the pages that lanes 0-7 hold (row0: the first
+        // row of each 16) into the next slot
+        auto copy_slot = [&](const uint16_t *cache, int64_t row0, unsigned miss, int lo, int hi) {
+            const uint32_t sl = seq % NS;
+            if (seq >= NS) {
+                const uint32_t ph = (seq / NS - 1) & 1u;
+                // no free slot yet: what has been copied is handed over first
+                if (done < seq && !__all_sync(0xffffffffu, try_wait(su32(&B.empty[sl]), ph)))
+                    hand_over(true);
+                if (!warp_wait(&B.empty[sl], ph, abort, a.error)) {
+                    ok = false;
+                    return;
+                }
+            }
+            const uint32_t base = ring + sl * C::kSlot;
+            // thread: chunk ch of rows r0, r0 + kStep, ...; 16 rows are of one page
+            constexpr int kStep = 128 / (D / 8);
+            const int r0 = ct / (D / 8), ch = ct % (D / 8);
+            const uint32_t dst = base + (ch >> 3) * C::kSlab + r0 * 128;
+#pragma unroll 4
+            for (int j = 0; j < kChunks; ++j) {
+                const int r = r0 + j * kStep;
+                const int64_t from = __shfl_sync(0xffffffffu, row0, r >> 4) + (r & 15);
+                const bool in = !(miss >> (r >> 4) & 1) && r < hi && r >= lo;
+                copy16(dst + j * kStep * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                       cache + (in ? from * D + ch * 8 : 0), in);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            ++seq;
+            if (seq - done > 1) hand_over(false);
+        };
+        // a turn copies the keys of tile `tile` and the values of the one before;
+        // the last turn the last values alone
+        int64_t v_row0 = 0;
+        unsigned v_miss = 0;
+        int v_lo = 0, v_hi = 0, left = 0, key0 = 0;
+        Piece p = {};
+        bool more = true;
+        for (uint32_t n = 0; ok && more;) {
+            if (left == 0) {
+                const int it = n % kItems;
+                if (!warp_wait(&B.item_full[it], (n / kItems) & 1u, abort, a.error)) {
+                    ok = false;
+                    break;
+                }
+                more = !B.stop[it];
+                if (more) {
+                    p = B.items[it];
+                    left = p.ntiles;
+                    key0 = p.key0;
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&B.item_empty[it]);
+                    ++n;
+                }
+            }
+            int64_t row0 = 0;
+            unsigned miss = 0;
+            if (more) {
+                const int *pages = a.prefix_phase ? a.prefix_pages
+                                                  : a.block_table + (int64_t)p.seq * a.max_pages;
+                // lane l: the page of keys 16 (l % 8) .. of the tile
+                const int key = key0 + 16 * (lane & 7);
+                int e = -1;
+                if (key < p.keys && key + 16 > first_key) e = __ldg(pages + (key >> a.page_shift));
+                const bool there = e >= 0 && e < a.num_pages;
+                miss = ~__ballot_sync(0xffffffffu, there) & 0xffu;
+                if (there)
+                    row0 = (((int64_t)e * a.Hkv + p.head) << a.page_shift) +
+                           (key & ((1 << a.page_shift) - 1));
+                if (ct == 0) B.miss[tile % kMiss] = miss;
+                // the tile after the next into L2: two slots of copies in flight
+                // alone cover half of the memory's latency at its bandwidth
+                const int ahead = key + 2 * kKT;
+                if (warp == 12 && lane < 16 && ahead < p.keys) {
+                    const int f = __ldg(pages + (ahead >> a.page_shift));
+                    if (f >= 0 && f < a.num_pages) {
+                        const int64_t row = (((int64_t)f * a.Hkv + p.head) << a.page_shift) +
+                                            (ahead & ((1 << a.page_shift) - 1));
+                        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                                         (lane < 8 ? k_cache : v_cache) + row * D),
+                                     "r"(16 * D * 2)
+                                     : "memory");
+                    }
+                }
+            }
+#pragma unroll 1
+            for (int kv = more ? 0 : 1; kv < (tile > 0 ? 2 : 1) && ok; ++kv)
+                copy_slot(kv ? v_cache : k_cache, kv ? v_row0 : row0, kv ? v_miss : miss,
+                          kv ? v_lo : first_key - key0, kv ? v_hi : p.keys - key0);
+            v_row0 = row0;
+            v_miss = miss;
+            v_lo = first_key - key0;
+            v_hi = p.keys - key0;
+            if (more) {
+                ++tile;
+                --left;
+                key0 += kKT;
+            }
+        }
+        if (ok && done < seq) hand_over(true);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        // ---------------------------------------------- queries and softmax
+        const int g = warp >> 2, w = warp & 3;
+        const int r = 32 * w + lane;  // row of the item, tensor-memory lane
+        const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
+        uint32_t t = 0;  // tiles of the share so far
+        for (uint32_t n = 0;; ++n) {
+            const int it = n % kItems;
+            if (!warp_wait(&B.item_full[it], (n / kItems) & 1u, abort, a.error)) break;
+            if (B.stop[it]) break;
+            const Piece &p = B.items[it];  // held until the piece is done
+            {
+                // 16 rows of the queries, a row (D = 64: two) per step
+                constexpr int LPR = D / 4;      // lanes per row
+                constexpr int RPS = 32 / LPR;   // rows per step
+                constexpr int STEPS = 8 / RPS;  // steps whose loads are in flight at once
+                const int sub = lane / LPR, c4 = lane % LPR;
+                const float *q0 = a.Q + (int64_t)p.tok0 * a.ldq + p.head * a.G * D + 4 * c4;
+                const int nrows = p.ntok * a.G;
+                bool waited = n == 0;
+#pragma unroll 1
+                for (int i0 = 0; i0 < 16; i0 += 8) {
+                    float4 q[STEPS];
+#pragma unroll
+                    for (int i = 0; i < STEPS; ++i) {
+                        const int qr = 16 * warp + i0 + i * RPS + sub;
+                        const int qt = qr * a.g_inv >> 16;
+                        q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (qr < nrows)
+                            q[i] = *reinterpret_cast<const float4 *>(q0 + (int64_t)qt * a.ldq +
+                                                                     (qr - qt * a.G) * D);
+                    }
+                    // the piece before has no S to be formed any more
+                    if (!waited) {
+                        if (!warp_wait(&B.q_empty, (n - 1) & 1u, abort, a.error)) break;
+                        waited = true;
+                    }
+#pragma unroll
+                    for (int i = 0; i < STEPS; ++i) {
+                        const int qr = 16 * warp + i0 + i * RPS + sub;
+                        float mul = a.sign;
+                        if (!BF) {
+                            float top = fmaxf(fmaxf(fabsf(q[i].x), fabsf(q[i].y)),
+                                              fmaxf(fabsf(q[i].z), fabsf(q[i].w)));
+#pragma unroll
+                            for (int o = LPR / 2; o > 0; o >>= 1)
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            const int sh = shift_of((int)(__float_as_uint(top) >> 23) - 127);
+                            mul *= pow2(-sh);
+                            if (c4 == 0) B.qmul[n & 1][qr] = pow2(sh);
+                        }
+                        uint32_t x[NP], y[NP];
+                        split16<BF, NP>(q[i].x * mul, q[i].y * mul, x);
+                        split16<BF, NP>(q[i].z * mul, q[i].w * mul, y);
+                        const uint32_t at = qbase + (c4 >> 4) * C::kSlab + qr * 128 +
+                                            ((((c4 & 15) >> 1) ^ (qr & 7)) << 4) + (c4 & 1) * 8;
+#pragma unroll
+                        for (int part = 0; part < NP; ++part)
+                            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(
+                                             at + part * C::kQPart),
+                                         "r"(x[part]), "r"(y[part])
+                                         : "memory");
+                    }
+                }
+                if (!waited) break;
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&B.q_full);
+            }
+            const int tok = r * a.g_inv >> 16;
+            const int limit = tok < p.ntok ? row_limit(a, p, tok) : p.keys;
+            int key0 = p.key0 + 64 * g;  // this warp's 64 keys
+            bool ok = true;
+            for (int k = 0; k < p.ntiles; ++k, ++t, key0 += kKT) {
+                const uint32_t area = lanes + (t & 1) * C::kArea;
+                if (!warp_wait(&B.s_full[t & 1], (t >> 1) & 1u, abort, a.error)) {
+                    ok = false;
+                    break;
+                }
+                tc_after();
+                uint32_t v[2][32];
+                tmem_ld32(area + C::kS0 + 64 * g, v[0]);
+                tmem_ld32(area + C::kS0 + 64 * g + 32, v[1]);
+                tmem_ld_wait();
+                const unsigned miss = B.miss[t % kMiss] >> (4 * g);
+                const float c = BF ? a.scale : a.scale * B.qmul[n & 1][r];
+                if (__any_sync(0xffffffffu,
+                               key0 + 64 > limit || key0 < first_key || (miss & 15u) != 0)) {
+                    // keys behind the row's own, in front of the suffix or of a
+                    // missing page: bit i of `seen` is clear
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int hi = limit - key0 - 32 * q, lo = first_key - key0 - 32 * q;
+                        unsigned seen = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1;
+                        if (lo > 0) seen = lo >= 32 ? 0u : seen & (~0u << lo);
+                        if (miss >> (2 * q) & 1) seen &= 0xffff0000u;
+                        if (miss >> (2 * q + 1) & 1) seen &= 0xffffu;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(seen >> i & 1)) v[q][i] = 0xff800000u;
+                    }
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 64; i += 2)
+                    mx = fmaxf(mx, fmaxf(__uint_as_float(v[i / 32][i % 32]),
+                                         __uint_as_float(v[i / 32][i % 32 + 1])));
+                // the row's maximum, with the other half's; every logit of these
+                // rows is in registers from here on
+                B.half_max[t & 1][g][r] = mx;
+                __syncwarp();
+                if (lane == 0) bar_arrive(&B.pair[w]);
+                if (!warp_wait(&B.pair[w], t & 1u, abort, a.error)) {
+                    ok = false;
+                    break;
+                }
+                mx = fmaxf(mx, B.half_max[t & 1][1 - g][r]);
+                const float m = mx == -INFINITY ? 0.0f : fmaf(mx, c, -kBias);
+                const unsigned long long c2 = pk(c, c), m2 = pk(-m, -m);
+                unsigned long long sum2 = 0;
+                // per 16 keys 8 columns of each part
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t parts[NP][8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int e = 16 * (q & 1) + 2 * i;
+                        float x, y;
+                        upk(fma2(pk(__uint_as_float(v[q >> 1][e]),
+                                    __uint_as_float(v[q >> 1][e + 1])),
+                                 c2, m2),
+                            x, y);
+                        x = ex2(x);
+                        y = ex2(y);
+                        sum2 = add2(sum2, pk(x, y));
+                        uint32_t z[NP];
+                        split16<BF, NP>(x, y, z);
+#pragma unroll
+                        for (int part = 0; part < NP; ++part) parts[part][i] = z[part];
+                    }
+#pragma unroll
+                    for (int part = 0; part < NP; ++part)
+                        tmem_st8(area + 8 * NP * (4 * g + q) + 8 * part, parts[part]);
+                }
+                float sa, sb;
+                upk(sum2, sa, sb);
+                B.stat[t % kStats][g][r] = make_float2(mx == -INFINITY ? mx : m, sa + sb);
+                tmem_st_wait();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&B.p_full[t & 1]);
+            }
+            if (!ok) break;
+            __syncwarp();
+            if (lane == 0) bar_arrive(&B.item_empty[it]);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        // -------------------------------------------------------- the output
+        const int w = warp & 3;
+        const int row = 32 * w + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16) + C::kPV0;
+        uint32_t t = 0, met = 0;
+        // the four warps meet (bounded, so that an abort leaves nobody behind)
+        auto group_sync = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0) bar_arrive(&B.group);
+            return warp_wait(&B.group, met++ & 1u, abort, a.error);
+        };
+        for (uint32_t n = 0;; ++n) {
+            const int it = n % kItems;
+            if (!warp_wait(&B.item_full[it], (n / kItems) & 1u, abort, a.error)) break;
+            if (B.stop[it]) break;
+            const Piece &p = B.items[it];  // held until the piece is done
+            unsigned long long o2[D / 2];  // the row's output, in pairs
+            float m = -INFINITY, l = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 2; ++i) o2[i] = 0;
+            bool ok = true;
+            for (int k = 0; k < p.ntiles; ++k, ++t) {
+                const uint32_t pb = t % C::kPVs;
+                if (!warp_wait(&B.pv_full[pb], (t / C::kPVs) & 1u, abort, a.error)) {
+                    ok = false;
+                    break;
+                }
+                tc_after();
+                float2 e = B.stat[t % kStats][0][row];
+                e.y += B.stat[t % kStats][1][row].y;
+                const float top = fmaxf(m, e.x);
+                const float f = max_factor(m, top), g = max_factor(e.x, top);
+                m = top;
+                l = l * f + e.y * g;
+                const unsigned long long f2 = pk(f, f), g2 = pk(g, g);
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t v[16];
+                    tmem_ld16(lanes + 128 * pb + 16 * c, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        o2[8 * c + i] = fma2(pk(__uint_as_float(v[2 * i]),
+                                                __uint_as_float(v[2 * i + 1])),
+                                             g2, mul2(o2[8 * c + i], f2));
+                }
+                tc_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&B.pv_empty[pb]);
+            }
+            if (!ok) break;
+            const int tok = row * a.g_inv >> 16;
+            const bool live = tok < p.ntok;
+            const int64_t out =
+                live ? (int64_t)(p.tok0 + tok) * a.Hq + p.head * a.G + (row - tok * a.G) : -1;
+            // a row per thread: 32 lines per store, but code that is executed once
+            // an item has to be short (an instruction that is not in the cache
+            // costs about 20 cycles; rows turned in shared memory measured three
+            // times as long)
+            const bool whole = p.npieces == 1;
+            const int64_t part = (int64_t)(2 * blockIdx.x + p.slot) * kRows + row;
+            if (whole) {
+                const RowEnd e = row_end<D>(a, out < 0 ? 0 : out, m, l, live);
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < D / 4; ++i) {
+                        float4 v;
+                        upk(mul2(o2[2 * i], pk(e.own, e.own)), v.x, v.y);
+                        upk(mul2(o2[2 * i + 1], pk(e.own, e.own)), v.z, v.w);
+                        finish4(a, out * D + 4 * i, e.front, v);
+                    }
+                }
+            } else {
+                // this CTA's part of the item, then whoever is last joins them all
+#pragma unroll
+                for (int i = 0; i < D / 4; ++i) {
+                    float4 v;
+                    upk(o2[2 * i], v.x, v.y);
+                    upk(o2[2 * i + 1], v.z, v.w);
+                    __stcg(reinterpret_cast<float4 *>(a.part_o + part * D) + i, v);
+                }
+                __stcg(a.part_ml + part, make_float2(m, l));
+                __threadfence();
+                if (!group_sync()) break;
+                if (row == 0) {
+                    unsigned *count = a.counters + p.first;
+                    const bool last = atomicAdd(count, 1u) == (unsigned)p.npieces - 1;
+                    if (last) *count = 0;  // as the next launch wants it
+                    B.last = last;
+                }
+                if (!group_sync()) break;
+                if (B.last) {  // (rewritten only after the group has met again)
+                    __threadfence();
+                    auto from = [&](int c) {
+                        return (int64_t)(2 * (p.first + c) + (c == 0)) * kRows + 32 * w;
+                    };
+                    m = -INFINITY;
+                    for (int c = 0; c < p.npieces; ++c)
+                        m = fmaxf(m, __ldcg(a.part_ml + from(c) + lane).x);
+                    l = 0.0f;
+                    for (int c = 0; c < p.npieces; ++c) {
+                        const float2 e = __ldcg(a.part_ml + from(c) + lane);
+                        l += e.y * max_factor(e.x, m);
+                    }
+                    const RowEnd e = row_end<D>(a, out < 0 ? 0 : out, m, l, live);
+#pragma unroll 1
+                    for (int q = 0; q < D / 32; ++q) {
+                        // 32 columns of the warp's rows, whole lines; two parts' loads
+                        // at once
+                        float4 sum[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        const int col = 32 * q + 4 * (lane & 7);
+#pragma unroll 1
+                        for (int c = 0; c < p.npieces; c += 2) {
+                            const bool two = c + 1 < p.npieces;
+                            const int64_t at[2] = {from(c), from(two ? c + 1 : c)};
+                            float wt[2];
+                            float4 v[2][8];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                wt[j] = __ldcg(a.part_ml + at[j] + lane).x;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    v[j][i] = __ldcg(reinterpret_cast<const float4 *>(
+                                        a.part_o + (at[j] + 4 * i + (lane >> 3)) * D + col));
+                            }
+                            wt[0] = max_factor(wt[0], m);
+                            wt[1] = two ? max_factor(wt[1], m) : 0.0f;
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const float f =
+                                        __shfl_sync(0xffffffffu, wt[j], 4 * i + (lane >> 3));
+                                    sum[i].x += v[j][i].x * f;
+                                    sum[i].y += v[j][i].y * f;
+                                    sum[i].z += v[j][i].z * f;
+                                    sum[i].w += v[j][i].w * f;
+                                }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int rr = 4 * i + (lane >> 3);
+                            const int64_t to_row = __shfl_sync(0xffffffffu, out, rr);
+                            const float own = __shfl_sync(0xffffffffu, e.own, rr);
+                            const float front = __shfl_sync(0xffffffffu, e.front, rr);
+                            if (to_row >= 0)
+                                finish4(a, to_row * D + col, front,
+                                        make_float4(sum[i].x * own, sum[i].y * own,
+                                                    sum[i].z * own, sum[i].w * own));
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(&B.item_empty[it]);
+        }
+    }
+    tc_before();
+    __syncthreads();
+    if (warp == 16) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                     : "memory");
+    }
+}
+
+template <int D, bool BF>
+sq_status launch_tiles(const PagedArgs &a, const void *k_cache, const void *v_cache, int sms,
+                       cudaStream_t st) {
+    using C = TilesCfg<D, BF>;
+    static std::mutex mu;
+    static bool done[64] = {};
+    DeviceInfo di;
+    sq_status rc = device_info(&di);
+    if (rc != SQ_OK) return rc;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!done[di.device & 63]) {
+            if (cudaFuncSetAttribute(paged_tiles_kernel<D, BF>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     C::kSmem) != cudaSuccess)
+                return SQ_ERR_CUDA;
+            done[di.device & 63] = true;
+        }
+    }
+    return launch_pdl(paged_tiles_kernel<D, BF>, dim3((unsigned)sms), dim3(kThreads), C::kSmem, st,
+                      1, a, static_cast<const uint16_t *>(k_cache),
+                      static_cast<const uint16_t *>(v_cache));
+}
+
+}  // namespace
+
+sq_status launch_paged_tiles(const PagedArgs &a, const void *k_cache, const void *v_cache, int D,
+                             bool bf16, int sms, cudaStream_t st) {
+    if (D == 128)
+        return bf16 ? launch_tiles<128, true>(a, k_cache, v_cache, sms, st)
+                    : launch_tiles<128, false>(a, k_cache, v_cache, sms, st);
+    return bf16 ? launch_tiles<64, true>(a, k_cache, v_cache, sms, st)
+                : launch_tiles<64, false>(a, k_cache, v_cache, sms, st);
+}
+
+}  // namespace sq

@@ -23,7 +23,7 @@ static long long g_checked = 0, g_fail = 0;
             std::printf("FAIL line %d: %s\n", __LINE__, #cond);  \
     } while (0)
 
-template <int KT>
+template <int KT, int PAD>
 static void check(PagedArgs a, int grid, int min_pairs) {
     // the line, pair by pair, as the header's comment states it
     const int nb = a.prefix_phase ? 1 : a.B;
@@ -41,10 +41,11 @@ static void check(PagedArgs a, int grid, int min_pairs) {
             while (a.kstart + n * KT < last) ++n;
             CHECK(n == key_tiles<KT>(a, s, j));
             for (int h = 0; h < a.Hkv; ++h)
-                for (int k = 0; k < n; ++k) line.emplace_back(b, j, h, k);
+                for (int k = 0; k < n + PAD; ++k)  // the last PAD without work
+                    line.emplace_back(b, j, h, k < n ? k : -1);
         }
-        CHECK(a.Hkv * key_tiles_before<KT>(a, s, row_tiles(a, s)) ==
-              (int64_t)line.size() - seq_begin[b]);
+        const int64_t pairs = pairs_before<KT, PAD>(a, s, row_tiles(a, s));
+        CHECK(a.Hkv * pairs == (int64_t)line.size() - seq_begin[b]);
     }
     const int64_t total = (int64_t)line.size();
     if (total == 0) return;
@@ -67,11 +68,14 @@ static void check(PagedArgs a, int grid, int min_pairs) {
                 (b + 1 == nb ? total : seq_begin[b + 1]) > seq_begin[b])
                 sh.seq = b;
         sh.seq_begin = seq_begin[sh.seq];
-        Walk<KT> w;
+        Walk<KT, PAD> w;
         w.start(a, sh);
         Piece p;
         bool slots[2] = {false, false};
-        while (w.next(a, sh, p)) {
+        auto idle = [&]() {  // pairs without work that stand next in the share
+            while (at < sh.end && std::get<3>(line[at]) < 0) ++at;
+        };
+        for (idle(); w.next(a, sh, p); idle()) {
             const auto [b, j, h, k] = line[at];
             const Seq s = load_seq(a, b);
             CHECK(p.seq == b && p.head == h && p.ntiles >= 1);
@@ -142,8 +146,8 @@ int main() {
             a.prefix_phase = phase;
             a.kstart = phase ? 0 : a.prefix_len / KT * KT;
             const int grid = pick(1, 152), least = pick(1, 4);
-            if (KT == 16) check<16>(a, grid, least);
-            else check<128>(a, grid, least);
+            if (KT == 16) check<16, 2>(a, grid, least);
+            else check<128, 1>(a, grid, least);
         }
     }
     // the closed-form sum against a loop

@@ -43,7 +43,7 @@ def verify(sq, t, scale=None, **kw):
     return out
 
 
-HEADS = [(4, 4), (8, 2), (7, 1), (32, 8), (6, 2), (12, 1)]
+HEADS = [(4, 4), (8, 2), (7, 1), (32, 8), (6, 2), (12, 1), (24, 1), (128, 1)]
 LENS = [
     ([1], [1]),
     ([1], [300]),
@@ -78,7 +78,7 @@ def test_pages(sq, page, D, dtype):
 
 @pytest.mark.parametrize("prefix", [1, 16, 40, 64, 100, 128, 200])
 @pytest.mark.parametrize("q,kv", [([1, 1, 1], [0, 3, 150]), ([2, 1, 40, 1], [30, 1, 60, 0])])
-@pytest.mark.parametrize("Hq,Hkv,D,dtype", [(8, 2, 128, BF), (4, 4, 64, FP), (16, 1, 128, FP)])
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", [(8, 2, 128, BF), (4, 4, 64, FP), (20, 1, 128, FP)])
 def test_shared_prefix(sq, prefix, q, kv, Hq, Hkv, D, dtype):
     kv = [prefix + n for n in kv]
     verify(sq, Batch(q, kv, Hq, Hkv, D, 16 if prefix % 3 else 64, dtype, prefix=prefix,
