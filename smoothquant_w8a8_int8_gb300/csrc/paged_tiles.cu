@@ -115,7 +115,6 @@ constexpr int kThreads = 640;
 constexpr int kItems = 4;    // pieces the walk may be ahead
 constexpr int kStats = 4;    // tiles whose maxima and sums are kept
 constexpr int kMiss = 8;     // more than the tiles between a copy and its softmax
-constexpr int kPad = 2;      // an item's start and end, in key tiles
 constexpr int kMinTiles = 1; // key tiles of a CTA's share at least
 constexpr float kBias = 12.0f;  // log2 of the probabilities' factor
 
@@ -130,6 +129,9 @@ struct TilesCfg {
     // tensor memory: S and P of a tile, S's first column in it, P V
     static constexpr int kArea = 64 * kParts;
     static constexpr int kS0 = kArea - 128;
+    // an item's start and end in key tiles (bf16: 2, 4, 6, 8 measured 755, 692,
+    // 708, 735 us for two prompts of 4096 tokens; fp16: 672, 534, 506, 528)
+    static constexpr int kPad = BF ? 4 : 6;
     static constexpr int kPVs = BF ? 1 : 2;
     static constexpr int kPV0 = 2 * kArea;
 };
@@ -159,36 +161,35 @@ __device__ __forceinline__ void tc_before() {
 __device__ __forceinline__ void tc_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// shared-memory operand, 128-byte swizzle: 8-row atoms of 1024 bytes; `lead` is
-// the distance of 64-element groups of an operand that is not K-major
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lead) {
-    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(lead >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+// shared-memory operand, 128-byte swizzle: 8-row atoms of 1024 bytes.  The
+// descriptor's low word: the address in 16-byte units and `lead`, the distance of
+// 64-element groups of an operand that is not K-major; its high word is constant.
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lead) {
+    return (saddr & 0x3FFFFu) >> 4 | (lead >> 4) << 16;
 }
+constexpr uint32_t kDescHigh = 1024 >> 4 | 1u << 14 | 2u << 29;
 // kind::f16: fp32 sums of bf16 or fp16 operands, M = 128
 __host__ __device__ constexpr uint32_t idesc_f16(int n, bool bf16, bool b_by_rows) {
     return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_by_rows ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(128 >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        uint32_t acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n"
+        " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHigh)
         : "memory");
 }
 // A from tensor memory: 8 columns hold K = 16
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        uint32_t acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n"
+        " mov.b64 db, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHigh)
         : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_after();
     pdl_launch_dependents();
     pdl_wait();  // every global-memory access below follows the previous kernel
-    find_shares<kKT, kPad, kThreads, 1>(a, kMinTiles, &B.share);
+    find_shares<kKT, C::kPad, kThreads, 1>(a, kMinTiles, &B.share);
     const uint32_t tmem = B.tmem;
     const int first_key = a.prefix_phase ? 0 : a.prefix_len;
 
@@ -329,15 +330,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t d = tmem + (t_s & 1) * C::kArea + C::kS0;
                 // the smallest part first: what the accumulator truncates is relative
                 // to the sum so far
-#pragma unroll 1
-                for (int part = NP - 1; part >= 0; --part) {
-                    const uint32_t q = qbase + part * C::kQPart;
+                const uint32_t qd = desc_low(qbase, 16), kd = desc_low(kb, 16);
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
-                        mma_ss(d, desc_sw128(q + (i / 4) * C::kSlab, 16) + 2 * (i % 4),
-                               desc_sw128(kb + (i / 4) * C::kSlab, 16) + 2 * (i % 4), qk_desc,
+                for (int part = NP - 1; part >= 0; --part)
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const int step = (i / 4) * C::kSlab / 16 + 2 * (i % 4);
+                        mma_ss(d, qd + part * C::kQPart / 16 + step, kd + step, qk_desc,
                                (part < NP - 1 || i) ? 1u : 0u);
-                }
+                    }
                 if (--left == 0) mma_commit(&B.q_empty);  // (before the softmax can go on)
                 mma_commit(&B.s_full[t_s & 1]);
                 mma_commit(&B.empty[ks % NS]);
@@ -359,12 +360,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t d = tmem + C::kPV0 + 128 * pb;
                 const uint32_t pa = tmem + (t_pv & 1) * C::kArea;
                 const uint32_t v = ring + (vs % NS) * C::kSlot;
-#pragma unroll 1
+                const uint32_t vd = desc_low(v, C::kSlab);
+#pragma unroll
                 for (int part = NP - 1; part >= 0; --part)
 #pragma unroll
                     for (int i = 0; i < kKT / 16; ++i)
-                        mma_ts(d, pa + 8 * NP * i + 8 * part, desc_sw128(v + i * 2048, C::kSlab),
-                               pv_desc, (part < NP - 1 || i) ? 1u : 0u);
+                        mma_ts(d, pa + 8 * NP * i + 8 * part, vd + 128 * i, pv_desc,
+                               (part < NP - 1 || i) ? 1u : 0u);
                 mma_commit(&B.pv_full[pb]);
                 mma_commit(&B.empty[vs % NS]);
                 ++t_pv;
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             drain_bar(&B.mma_done, 0, a.error);
         } else if (warp == 17) {
             // -------------------------------------------- the share's pieces
-            Walk<kKT, kPad> walk;
+            Walk<kKT, C::kPad> walk;
             walk.start(a, B.share);
             for (uint32_t n = 0;; ++n) {
                 Piece p;
@@ -397,7 +399,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         // ------------------------------------------------------------ copies
         const int ct = threadIdx.x - 384;
-        constexpr int kChunks = kKT * D / 8 / 128;  // 16-byte chunks of a slot per thread
         uint32_t seq = 0, done = 0, tile = 0;  // slots begun, slots handed over, tiles begun
         bool ok = true;
         auto hand_over = [&](bool all) {
@@ -410,9 +411,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++done;
             }
         };
-        // 128 rows of a cache from the pages that lanes 0-7 hold (row0: the first
-        // row of each 16) into the next slot
-        auto copy_slot = [&](const uint16_t *cache, int64_t row0, unsigned miss, int lo, int hi) {
+        // 128 rows of a cache into the next slot; lane l (of 8) holds the place of
+        // rows 16 l .. 16 l + 15 in the caches, in bytes
+        auto copy_slot = [&](const uint16_t *cache, int64_t place, unsigned miss, int lo, int hi) {
             const uint32_t sl = seq % NS;
             if (seq >= NS) {
                 const uint32_t ph = (seq / NS - 1) & 1u;
@@ -424,18 +425,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return;
                 }
             }
-            const uint32_t base = ring + sl * C::kSlot;
-            // thread: chunk ch of rows r0, r0 + kStep, ...; 16 rows are of one page
+            // thread: chunk ch of rows r0, r0 + kStep, ... of every 16
             constexpr int kStep = 128 / (D / 8);
             const int r0 = ct / (D / 8), ch = ct % (D / 8);
-            const uint32_t dst = base + (ch >> 3) * C::kSlab + r0 * 128;
-#pragma unroll 4
-            for (int j = 0; j < kChunks; ++j) {
-                const int r = r0 + j * kStep;
-                const int64_t from = __shfl_sync(0xffffffffu, row0, r >> 4) + (r & 15);
-                const bool in = !(miss >> (r >> 4) & 1) && r < hi && r >= lo;
-                copy16(dst + j * kStep * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                       cache + (in ? from * D + ch * 8 : 0), in);
+            const uint32_t dst = ring + sl * C::kSlot + (ch >> 3) * C::kSlab + r0 * 128 +
+                                 (((ch & 7) ^ (r0 & 7)) << 4);
+            const char *src = reinterpret_cast<const char *>(cache) + (r0 * D + ch * 8) * 2;
+            if (miss == 0 && lo <= 0 && hi >= kKT) {
+#pragma unroll
+                for (int j = 0; j < kKT / 16; ++j) {
+                    const char *from = src + __shfl_sync(0xffffffffu, place, j);
+#pragma unroll
+                    for (int i = 0; i < 16 / kStep; ++i)
+                        copy16(dst + (16 * j + i * kStep) * 128, from + i * kStep * D * 2, true);
+                }
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < kKT / 16; ++j) {
+                    const char *from = src + __shfl_sync(0xffffffffu, place, j);
+                    const bool page = !(miss >> j & 1);
+#pragma unroll
+                    for (int i = 0; i < 16 / kStep; ++i) {
+                        const int r = 16 * j + r0 + i * kStep;
+                        const bool in = page && r < hi && r >= lo;
+                        copy16(dst + (16 * j + i * kStep) * 128,
+                               in ? from + i * kStep * D * 2 : reinterpret_cast<const char *>(cache),
+                               in);
+                    }
+                }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
             ++seq;
@@ -443,11 +460,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // a turn copies the keys of tile `tile` and the values of the one before;
         // the last turn the last values alone
-        int64_t v_row0 = 0;
+        int64_t v_place = 0;
         unsigned v_miss = 0;
         int v_lo = 0, v_hi = 0, left = 0, key0 = 0;
         Piece p = {};
         bool more = true;
+        int entry = -1;
+        // the entry of the page of keys key .. key + 15; -1 where none is wanted
+        auto page_of = [&](int key) {
+            const int *pages = a.prefix_phase ? a.prefix_pages
+                                              : a.block_table + (int64_t)p.seq * a.max_pages;
+            return key < p.keys && key + 16 > first_key ? __ldg(pages + (key >> a.page_shift)) : -1;
+        };
         for (uint32_t n = 0; ok && more;) {
             if (left == 0) {
                 const int it = n % kItems;
@@ -460,46 +484,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p = B.items[it];
                     left = p.ntiles;
                     key0 = p.key0;
+                    entry = page_of(key0 + 16 * (lane & 7));
                     __syncwarp();
                     if (lane == 0) bar_arrive(&B.item_empty[it]);
                     ++n;
                 }
             }
-            int64_t row0 = 0;
+            int64_t place = 0;
             unsigned miss = 0;
             if (more) {
-                const int *pages = a.prefix_phase ? a.prefix_pages
-                                                  : a.block_table + (int64_t)p.seq * a.max_pages;
-                // lane l: the page of keys 16 (l % 8) .. of the tile
+                // lane l: the page of keys 16 (l % 8) .. of the tile; the next tile's
+                // entry is on its way meanwhile
+                const int e = entry;
                 const int key = key0 + 16 * (lane & 7);
-                int e = -1;
-                if (key < p.keys && key + 16 > first_key) e = __ldg(pages + (key >> a.page_shift));
+                entry = left > 1 ? page_of(key + kKT) : -1;
                 const bool there = e >= 0 && e < a.num_pages;
                 miss = ~__ballot_sync(0xffffffffu, there) & 0xffu;
                 if (there)
-                    row0 = (((int64_t)e * a.Hkv + p.head) << a.page_shift) +
-                           (key & ((1 << a.page_shift) - 1));
+                    place = ((((int64_t)e * a.Hkv + p.head) << a.page_shift) +
+                             (key & ((1 << a.page_shift) - 1))) *
+                            (D * 2);
                 if (ct == 0) B.miss[tile % kMiss] = miss;
-                // the tile after the next into L2: two slots of copies in flight
-                // alone cover half of the memory's latency at its bandwidth
-                const int ahead = key + 2 * kKT;
-                if (warp == 12 && lane < 16 && ahead < p.keys) {
-                    const int f = __ldg(pages + (ahead >> a.page_shift));
-                    if (f >= 0 && f < a.num_pages) {
-                        const int64_t row = (((int64_t)f * a.Hkv + p.head) << a.page_shift) +
-                                            (ahead & ((1 << a.page_shift) - 1));
-                        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                                         (lane < 8 ? k_cache : v_cache) + row * D),
-                                     "r"(16 * D * 2)
-                                     : "memory");
-                    }
-                }
             }
 #pragma unroll 1
             for (int kv = more ? 0 : 1; kv < (tile > 0 ? 2 : 1) && ok; ++kv)
-                copy_slot(kv ? v_cache : k_cache, kv ? v_row0 : row0, kv ? v_miss : miss,
+                copy_slot(kv ? v_cache : k_cache, kv ? v_place : place, kv ? v_miss : miss,
                           kv ? v_lo : first_key - key0, kv ? v_hi : p.keys - key0);
-            v_row0 = row0;
+            v_place = place;
             v_miss = miss;
             v_lo = first_key - key0;
             v_hi = p.keys - key0;

@@ -147,7 +147,7 @@ int main() {
             a.kstart = phase ? 0 : a.prefix_len / KT * KT;
             const int grid = pick(1, 152), least = pick(1, 4);
             if (KT == 16) check<16, 2>(a, grid, least);
-            else check<128, 1>(a, grid, least);
+            else trial % 4 == 1 ? check<128, 4>(a, grid, least) : check<128, 6>(a, grid, least);
         }
     }
     // the closed-form sum against a loop
