@@ -217,8 +217,10 @@ sq_status sq_rmsnorm_quant(const float *H, const float *residual, const float *g
  *                      page_size n + page_size - 1 in column n.
  * Hq query heads share Hkv key/value heads in groups of G = Hq / Hkv
  * consecutive ones (Hq a multiple of Hkv, G <= 128, Hq <= 4096).  D is 64 or
- * 128; page_size 16, 32, 64, 128 or 256.  T, B, max_pages * page_size and
- * num_pages * Hkv * page_size at most 2^30 (SQ_ERR_UNSUPPORTED beyond).
+ * 128; page_size 16, 32, 64, 128 or 256.  T at most 2^24; B, max_pages *
+ * page_size and num_pages * Hkv * page_size at most 2^30 (SQ_ERR_UNSUPPORTED
+ * beyond; so is sq_paged_attention where the batch could need 2^31 tiles: the row
+ * tiles of T and B times Hkv times a row of the table's keys, over 16 or 128).
  * The contents of the device arrays are not checked on the host; whatever they
  * hold, no access leaves the arrays (see each function). */
 typedef enum {

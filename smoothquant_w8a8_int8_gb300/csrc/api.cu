@@ -99,7 +99,7 @@ sq_status check_paged_shape(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int c
     if (ldq % 4 != 0) return SQ_ERR_ALIGNMENT;
     // token, sequence, key and cache-row numbers are 32-bit; element offsets are not
     const int64_t lim = (int64_t)1 << 30;
-    if (T > lim || B > lim || max_pages > lim / page_size || num_pages > lim / (Hkv * page_size))
+    if (T > (int64_t)1 << 24 || B > lim || max_pages > lim / page_size || num_pages > lim / (Hkv * page_size))
         return SQ_ERR_UNSUPPORTED;
     return SQ_OK;
 }

@@ -53,54 +53,60 @@ __device__ __forceinline__ void split16(float a, float b, uint32_t (&w)[N]) {
 // threads places them.
 template <int KT, int PAD, int NT, int W>
 __device__ __forceinline__ void find_shares(const PagedArgs &a, int min_pairs, Share *out) {
-    __shared__ int64_t warp_sum[NT / 32];
+    __shared__ int warp_sum[NT / 32];
     const int nb = a.prefix_phase ? 1 : a.B;
     const int run = (nb + NT - 1) / NT;
     const int b0 = min(nb, (int)threadIdx.x * run), b1 = min(nb, b0 + run);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        const Seq s = load_seq(a, b);
-        mine += a.Hkv * pairs_before<KT, PAD>(a, s, row_tiles(a, s));
-    }
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if ((threadIdx.x & 31) >= o) incl += v;
-    }
-    if ((threadIdx.x & 31) == 31) warp_sum[threadIdx.x >> 5] = incl;
-    __syncthreads();
-    int64_t before = 0, total = 0;
-    for (int w = 0; w < NT / 32; ++w) {
-        if (w < (int)(threadIdx.x >> 5)) before += warp_sum[w];
-        total += warp_sum[w];
-    }
-    before += incl - mine;  // pairs of the runs before this thread's
-    const int64_t fit = (total + min_pairs - 1) / min_pairs;
-    const int most = W * (int)gridDim.x;
-    const int workers = fit < most ? (int)fit : most;
+    int mine = 0, before = 0;
+    // first every thread's run is summed, then the shares that begin in it are
+    // found, walking through it again
 #pragma unroll 1
-    for (int w = 0; w < W; ++w) {
-        const int c = w * (int)gridDim.x + (int)blockIdx.x;
-        const int64_t begin = c < workers ? share_begin(total, workers, c) : total;
-        if (begin < total && begin >= before && begin < before + mine) {
-            int64_t at = before;
-            int b = b0;
-            for (; b < b1 - 1; ++b) {
-                const Seq s = load_seq(a, b);
-                const int64_t n = a.Hkv * pairs_before<KT, PAD>(a, s, row_tiles(a, s));
-                if (begin < at + n) break;
-                at += n;
+    for (int pass = 0; pass < 2; ++pass) {
+        int at = before;
+#pragma unroll 1
+        for (int b = b0; b < b1; ++b) {
+            const Seq s = load_seq(a, b);
+            const int n = a.Hkv * pairs_before<KT, PAD>(a, s, row_tiles(a, s));
+            if (pass == 0) {
+                mine += n;
+                continue;
             }
-            out[w].seq = b;
-            out[w].seq_begin = at;
+#pragma unroll 1
+            for (int w = 0; w < W; ++w)
+                if (out[w].begin >= at && out[w].begin < at + n) {
+                    out[w].seq = b;
+                    out[w].seq_begin = at;
+                }
+            at += n;
         }
-        if (threadIdx.x == w) {
-            out[w].total = total;
-            out[w].workers = workers;
-            out[w].begin = begin;
-            out[w].end = c < workers ? share_begin(total, workers, c + 1) : total;
+        if (pass == 1) break;
+        int incl = mine;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if ((threadIdx.x & 31) >= o) incl += v;
         }
+        if ((threadIdx.x & 31) == 31) warp_sum[threadIdx.x >> 5] = incl;
+        __syncthreads();
+        int total = 0;
+#pragma unroll 1
+        for (int w = 0; w < NT / 32; ++w) {
+            if (w < (int)(threadIdx.x >> 5)) before += warp_sum[w];
+            total += warp_sum[w];
+        }
+        before += incl - mine;  // pairs of the runs before this thread's
+        if (threadIdx.x < W) {
+            int workers = min((total + min_pairs - 1) / min_pairs, W * (int)gridDim.x);
+            if (a.prefix_phase && total > 0) {
+                // items of one length: whole numbers of workers for each, where
+                // there are enough, so that no worker has parts of two
+                const int items = total / key_tiles<KT>(a, load_seq(a, 0), 0);
+                if (items < workers) workers -= workers % items;
+            }
+            set_shares(out[threadIdx.x], total, workers,
+                       (int)threadIdx.x * (int)gridDim.x + (int)blockIdx.x);
+        }
+        __syncthreads();
     }
     __syncthreads();
 }
@@ -151,35 +157,13 @@ __device__ __forceinline__ RowEnd row_end(const PagedArgs &a, int64_t row, float
     e.front *= inv;
     return e;
 }
-__device__ __forceinline__ void row_store(const PagedArgs &a, const RowEnd &e, int col, float2 o) {
-    if (a.prefix_phase) {
-        *reinterpret_cast<float2 *>(a.prefix_o + e.at + col) = o;
-        return;
-    }
-    float2 r = make_float2(o.x * e.own, o.y * e.own);
-    if (a.prefix_len > 0) {
-        const float2 f = *reinterpret_cast<const float2 *>(a.prefix_o + e.at + col);
-        r.x += f.x * e.front;
-        r.y += f.y * e.front;
-    }
-    *reinterpret_cast<float2 *>(a.O + e.at + col) = r;
+// Where such a row goes (its element offset in the buffer is RowEnd::at), and
+// what is added to it.
+__device__ __forceinline__ float *row_target(const PagedArgs &a) {
+    return a.prefix_phase ? a.prefix_o : a.O;
 }
-
-// four columns of a row (o scaled by RowEnd::own) to the prefix's buffer or,
-// joined with it, to the output
-__device__ __forceinline__ void finish4(const PagedArgs &a, int64_t at, float front, float4 o) {
-    if (a.prefix_phase) {
-        *reinterpret_cast<float4 *>(a.prefix_o + at) = o;
-        return;
-    }
-    if (a.prefix_len > 0) {
-        const float4 f = *reinterpret_cast<const float4 *>(a.prefix_o + at);
-        o.x += f.x * front;
-        o.y += f.y * front;
-        o.z += f.z * front;
-        o.w += f.w * front;
-    }
-    *reinterpret_cast<float4 *>(a.O + at) = o;
+__device__ __forceinline__ const float *row_front(const PagedArgs &a) {
+    return a.prefix_phase || a.prefix_len == 0 ? nullptr : a.prefix_o;
 }
 
 }  // namespace

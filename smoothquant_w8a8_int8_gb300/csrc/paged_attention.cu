@@ -101,6 +101,11 @@ sq_status launch_paged_attention(const PagedCall &c, cudaStream_t st) {
         const int r = few ? (most <= 8 ? 8 : 16) : 128, kt = few ? 16 : 128;
         a.tpt = r / a.G;
         a.kstart = phase ? 0 : a.prefix_len / kt * kt;
+        // the longest line that the sizes allow: every sequence as long as its row
+        // of the table, and a row tile of its own begun
+        const int64_t tiles = (c.T + a.tpt - 1) / a.tpt + (phase ? 0 : c.B);
+        const int64_t keys = (phase ? c.prefix_len : c.max_pages * c.page_size) / kt + 16;
+        if (tiles * c.Hkv > ((int64_t)1 << 31) / keys) return SQ_ERR_UNSUPPORTED;
         rc = few ? launch_paged_rows(a, c.k_cache, c.v_cache, (int)c.D, bf16, r, di.sms, st)
                  : launch_paged_tiles(a, c.k_cache, c.v_cache, (int)c.D, bf16, di.sms, st);
         if (rc != SQ_OK) return rc;

@@ -6,13 +6,14 @@
 // head's group) of one sequence and one key/value head; its keys are cut into
 // tiles of KT.  All (item, key tile) pairs stand in one line -- sequences,
 // then row tiles, then key/value heads, then key tiles -- each item's followed
-// by PAD pairs without work that stand for the time of its start and end, and
-// worker c of n (a CTA, or a warp) takes pairs [c W / n, (c + 1) W / n): every
+// by PAD pairs without work that stand for the time of its start and end (none
+// where all items are of one length, over a shared prefix), and worker c of n (a CTA, or a warp) takes pairs [c W / n, (c + 1) W / n): every
 // worker has the same share whatever the lengths, known only on the device, are.  An item that
 // lies in several workers' shares leaves one partial result (row maximum, sum,
 // unnormalised output) per worker in the workspace; the one that arrives last
 // (a counter) joins them in the order of the line, so that the result does not
-// depend on who is last.
+// depend on who is last.  The line is shorter than 2^31 pairs (checked on the
+// host for the longest that the sizes allow).
 #pragma once
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -83,37 +84,39 @@ SQ_HD int key_tiles(const PagedArgs &a, const Seq &s, int j) {
     const int n = tile_keys(a, s, j) - a.kstart;
     return n <= KT ? 1 : (n + KT - 1) / KT;  // at least one: its rows are written
 }
-// sum of floor((p i + q) / m) over i < n; p, q >= 0, m > 0.  The sum counts
-// lattice points below a line: whole parts of p / m and q / m are summed in
-// closed form, and what is left is the same sum with the axes exchanged.
-SQ_HD int64_t floor_sum(int64_t n, int64_t m, int64_t p, int64_t q) {
-    int64_t total = 0;
+// sum of floor((p i + q) / m) over i < n; m > 0, and m n + p + q < 2^32 (T and a
+// row of the page table are limited to that).  The sum counts lattice points
+// below a line: whole parts of p / m and q / m are summed in closed form, and
+// what is left is the same sum with the axes exchanged.
+SQ_HD int floor_sum(uint32_t n, uint32_t m, uint32_t p, uint32_t q) {
+    uint32_t total = 0;  // the line is shorter than 2^31
+#pragma unroll 1
     while (n > 0) {
-        total += (n - 1) * n / 2 * (p / m) + n * (q / m);
-        p %= m;
-        q %= m;
-        const int64_t top = p * n + q;
+        const uint32_t pm = p / m, qm = q / m;
+        total += (uint32_t)((uint64_t)(n - 1) * n / 2) * pm + n * qm;
+        p -= pm * m;
+        q -= qm * m;
+        const uint32_t top = p * n + q;
         if (top < m) break;
         n = top / m;
-        q = top % m;
-        const int64_t was = m;
+        q = top - n * m;
+        const uint32_t was = m;
         m = p;
         p = was;
     }
-    return total;
+    return (int)total;
 }
 // pairs of one key/value head's items over the first J row tiles
 template <int KT, int PAD>
-SQ_HD int64_t pairs_before(const PagedArgs &a, const Seq &s, int J) {
-    if (a.prefix_phase) return (int64_t)J * (key_tiles<KT>(a, s, 0) + PAD);
+SQ_HD int pairs_before(const PagedArgs &a, const Seq &s, int J) {
+    if (a.prefix_phase) return J * key_tiles<KT>(a, s, 0);
     const int tiles = row_tiles(a, s);
     const int whole = at_most(J, tiles - 1);  // the last row tile may hold fewer tokens
-    int64_t sum = (int64_t)J * PAD;
+    int sum = J * PAD;
     if (whole > 0) {
-        const int64_t base = s.kv - s.qlen - a.kstart;
+        const int base = s.kv - s.qlen - a.kstart;
         // row tiles whose keys fit one key tile: base + (j + 1) tpt <= KT
-        int64_t ones = KT - base < 0 ? 0 : (KT - base) / a.tpt;
-        ones = ones < whole ? ones : whole;
+        const int ones = at_most(KT < base ? 0 : (int)((uint32_t)(KT - base) / a.tpt), whole);
         sum += ones + floor_sum(whole - ones, KT, a.tpt, base + (ones + 1) * a.tpt + KT - 1);
     }
     if (J > whole && J > 0) sum += key_tiles<KT>(a, s, J - 1);
@@ -122,18 +125,41 @@ SQ_HD int64_t pairs_before(const PagedArgs &a, const Seq &s, int J) {
 
 // Where a worker's share starts.
 struct Share {
-    int64_t total;       // W
-    int64_t begin, end;  // this worker's pairs
-    int64_t seq_begin;   // the line's position of sequence `seq`
-    int seq;
+    int total;           // W
+    int begin, end;      // this worker's pairs
+    int seq, seq_begin;  // the sequence they begin in, and its position on the line
+    int each, rest;      // W / n, rounded down, and what that leaves
+    float per_pair;      // n / W
     int workers;         // workers that take a share
+    int self;            // this worker
 };
-SQ_HD int64_t share_begin(int64_t total, int workers, int c) {
-    return total * c / workers;
+// The first pair of worker c: floor(c W / n)  (n < 2^16)
+SQ_HD int share_begin(const Share &s, int c) {
+    return s.each * c + (int)((uint32_t)s.rest * (uint32_t)c / (uint32_t)s.workers);
 }
-// the worker whose share holds position x
-SQ_HD int share_of(int64_t total, int workers, int64_t x) {
-    return (int)(((x + 1) * workers - 1) / total);
+// the worker whose share holds position x: a guess that is off by one at most
+// (three roundings of 2^-24, under 2^16 workers), put right
+SQ_HD int share_of(const Share &s, int x) {
+    int c = at_most((int)((float)x * s.per_pair), s.workers - 1);
+    if (share_begin(s, c) > x) --c;
+    else if (share_begin(s, c + 1) <= x) ++c;
+    return c;
+}
+SQ_HD void set_shares(Share &s, int total, int workers, int self) {
+    s.total = total;
+    s.workers = workers;
+    s.self = self;
+    s.each = s.rest = 0;
+    s.per_pair = 0.0f;
+    s.begin = s.end = total;
+    if (workers == 0) return;
+    s.each = total / workers;
+    s.rest = total - s.each * workers;
+    s.per_pair = (float)workers / (float)total;
+    if (self < workers) {
+        s.begin = share_begin(s, self);
+        s.end = share_begin(s, self + 1);
+    }
 }
 
 // A worker's piece of an item.
@@ -151,62 +177,59 @@ struct Piece {
 // Walks the pieces of a worker's share.
 template <int KT, int PAD>
 struct Walk {
-    int64_t at, end;  // position, end of the share
+    int at, end;  // position, end of the share
     int b, j, h, k;
+    int tiles, nk, pad;
     Seq s;
-    int tiles, nk;
-    int64_t before;  // pairs_before of row tile j
 
-    SQ_HD void enter(const PagedArgs &a) {
-        s = load_seq(a, b);
-        tiles = row_tiles(a, s);
-    }
     SQ_HD void start(const PagedArgs &a, const Share &sh) {
+        pad = a.prefix_phase ? 0 : PAD;
         at = sh.begin;
         end = sh.end;
         if (at >= end) return;
         b = sh.seq;
-        enter(a);
-        const int64_t rem = at - sh.seq_begin;
-        int lo = 0, hi = tiles - 1;  // the last row tile that starts at or before rem
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (a.Hkv * pairs_before<KT, PAD>(a, s, mid) <= rem) lo = mid;
-            else hi = mid - 1;
+        s = load_seq(a, b);
+        tiles = row_tiles(a, s);
+        const int rem = at - sh.seq_begin;
+        int hi = tiles - 1, before = 0;
+        j = 0;  // the last row tile that starts at or before rem
+#pragma unroll 1
+        while (j < hi) {
+            const int mid = (j + hi + 1) / 2;
+            const int n = a.Hkv * pairs_before<KT, PAD>(a, s, mid);
+            if (n <= rem) {
+                j = mid;
+                before = n;
+            } else {
+                hi = mid - 1;
+            }
         }
-        j = lo;
-        before = pairs_before<KT, PAD>(a, s, j);
         nk = key_tiles<KT>(a, s, j);
-        const int64_t r = rem - a.Hkv * before;
-        h = (int)(r / (nk + PAD));
-        k = (int)(r % (nk + PAD));
-    }
-    // on to the next item
-    SQ_HD void advance(const PagedArgs &a) {
-        k = 0;
-        if (++h < a.Hkv) return;
-        h = 0;
-        before += nk + PAD;
-        if (++j == tiles && at < end) {
-            do {  // the next sequence with a row
-                ++b;
-                enter(a);
-            } while (tiles == 0 && b < a.B - 1);
-            j = 0;
-            before = 0;
-        }
-        if (j < tiles) nk = key_tiles<KT>(a, s, j);
+        const int r = rem - before;  // Hkv items of one length
+        h = (int)((uint32_t)r / (uint32_t)(nk + pad));
+        k = r - h * (nk + pad);
     }
     // the next piece, or false at the end of the share
     SQ_HD bool next(const PagedArgs &a, const Share &sh, Piece &p) {
-        if (at < end && k >= nk) {  // among an item's pairs without work
-            at += nk + PAD - k;
-            advance(a);
+        if (at < end && k >= nk) {
+            // past an item's work: over its pairs without work to the next item
+            at += nk + pad - k;
+            k = 0;
+            if (++h == a.Hkv) {
+                h = 0;
+                ++j;
+#pragma unroll 1
+                while (j >= tiles && b < a.B - 1 && at < end) {  // the next sequence with a row
+                    s = load_seq(a, ++b);
+                    tiles = row_tiles(a, s);
+                    j = 0;
+                }
+                if (j < tiles) nk = key_tiles<KT>(a, s, j);
+            }
         }
         if (at >= end) return false;
-        const int64_t left = end - at;
-        const int take = left < nk - k ? (int)left : nk - k;
-        const int64_t s0 = at - k;
+        const int take = at_most(end - at, nk - k);
+        const int s0 = at - k;
         p.tok0 = s.q0 + j * a.tpt;
         p.ntok = at_most(a.tpt, s.qlen - j * a.tpt);
         p.head = h;
@@ -215,15 +238,13 @@ struct Walk {
         p.ntiles = take;
         p.keys = tile_keys(a, s, j);
         p.seq = b;
-        p.first = share_of(sh.total, sh.workers, s0);
-        p.npieces = share_of(sh.total, sh.workers, s0 + nk - 1) - p.first + 1;
+        // the item's other ends, where they are not this worker's
+        p.first = k == 0 ? sh.self : share_of(sh, s0);
+        const int last = k + take == nk ? sh.self : share_of(sh, s0 + nk - 1);
+        p.npieces = last - p.first + 1;
         p.slot = k == 0 ? 1 : 0;  // begun here: slot 1; begun before: slot 0
         at += take;
         k += take;
-        if (k == nk) {
-            at += PAD;
-            advance(a);
-        }
         return true;
     }
 };

@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 l[r] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) o[i][2 * r] = o[i][2 * r + 1] = 0.0f;
+#pragma unroll 2
                 for (int c = 0; c < p.npieces; ++c) {
                     const int64_t base =
                         (int64_t)(2 * (p.first + c) + (c == 0)) * ROWS + g + 8 * r;
@@ -407,9 +408,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             if (!live[r]) continue;
             const int64_t out = (int64_t)(p.tok0 + tok[r]) * a.Hq + p.head * a.G + (g + 8 * r) % a.G;
             const RowEnd e = row_end<D>(a, out, m[r], l[r], t == 0);
+            float *dst = row_target(a) + e.at + 2 * t;
+            const float *front = row_front(a);
+            if (front) front += e.at + 2 * t;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                row_store(a, e, 8 * i + 2 * t, make_float2(o[i][2 * r], o[i][2 * r + 1]));
+            for (int i = 0; i < D / 8; ++i) {
+                float2 v = make_float2(o[i][2 * r] * e.own, o[i][2 * r + 1] * e.own);
+                if (front) {
+                    const float2 f = *reinterpret_cast<const float2 *>(front + 8 * i);
+                    v.x += f.x * e.front;
+                    v.y += f.y * e.front;
+                }
+                *reinterpret_cast<float2 *>(dst + 8 * i) = v;
+            }
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");

@@ -67,27 +67,24 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort,
-                                       unsigned *error) {
-    const uint64_t t0 = gtime();
-    for (uint32_t it = 1;; ++it) {
-        if (try_wait(bar, parity)) return true;
-        if ((it & 63u) == 0) {
-            if (*abort) return false;
-            if (gtime() - t0 > kPagedTimeoutNs) {
-                *abort = 1;
-                atomicOr(error, 1u);
-                return false;
-            }
-        }
-    }
-}
 // Bounded wait for the phase of parity `parity`; false when the CTA aborted.
+// (Short, because it is inlined: the registers are split by role, which leaves no
+// room for calls.)
 __device__ __forceinline__ bool wait_bar(const uint64_t *bar, uint32_t parity,
                                          volatile int *abort, unsigned *error) {
     const uint32_t a = su32(bar);
     if (try_wait(a, parity)) return true;
-    return wait_slow(a, parity, abort, error);
+    const uint64_t t0 = gtime();
+#pragma unroll 1
+    while (!try_wait(a, parity)) {
+        if (*abort) return false;
+        if (gtime() - t0 > kPagedTimeoutNs) {
+            *abort = 1;
+            atomicOr(error, 1u);
+            return false;
+        }
+    }
+    return true;
 }
 // Every lane waits (so that every lane sees what the barrier publishes); the
 // outcome is the warp's.
@@ -344,10 +341,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_commit(&B.empty[ks % NS]);
                 ++t_s;
             };
-            next_s();
-            while (ok && t_pv < t_s) {
+            while (ok) {
                 if (more) next_s();
                 if (!ok) break;
+                if (more && t_s - t_pv < 2) continue;  // the first tile
+                if (t_pv == t_s) break;
                 // the last tile's values follow their keys at once
                 const uint32_t vs = t_pv + 1 < t_s ? 2 * t_pv + 2 : 2 * t_pv + 1;
                 const uint32_t pb = t_pv % C::kPVs;
@@ -742,27 +740,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             // times as long)
             const bool whole = p.npieces == 1;
             const int64_t part = (int64_t)(2 * blockIdx.x + p.slot) * kRows + row;
+            RowEnd e = {1.0f, 0.0f, part * D};
+            float *dst = a.part_o;
+            const float *front = nullptr;
             if (whole) {
-                const RowEnd e = row_end<D>(a, out < 0 ? 0 : out, m, l, live);
-                if (live) {
-#pragma unroll
-                    for (int i = 0; i < D / 4; ++i) {
-                        float4 v;
-                        upk(mul2(o2[2 * i], pk(e.own, e.own)), v.x, v.y);
-                        upk(mul2(o2[2 * i + 1], pk(e.own, e.own)), v.z, v.w);
-                        finish4(a, out * D + 4 * i, e.front, v);
-                    }
-                }
+                e = row_end<D>(a, out < 0 ? 0 : out, m, l, live);
+                dst = row_target(a);
+                front = row_front(a);
             } else {
-                // this CTA's part of the item, then whoever is last joins them all
+                __stcg(a.part_ml + part, make_float2(m, l));
+            }
+            if (!whole || live) {
+                dst += e.at;
+                if (front) front += e.at;
+                const unsigned long long own2 = pk(e.own, e.own);
 #pragma unroll
                 for (int i = 0; i < D / 4; ++i) {
                     float4 v;
-                    upk(o2[2 * i], v.x, v.y);
-                    upk(o2[2 * i + 1], v.z, v.w);
-                    __stcg(reinterpret_cast<float4 *>(a.part_o + part * D) + i, v);
+                    upk(mul2(o2[2 * i], own2), v.x, v.y);
+                    upk(mul2(o2[2 * i + 1], own2), v.z, v.w);
+                    if (front) {
+                        const float4 f = *reinterpret_cast<const float4 *>(front + 4 * i);
+                        v.x += f.x * e.front;
+                        v.y += f.y * e.front;
+                        v.z += f.z * e.front;
+                        v.w += f.w * e.front;
+                    }
+                    __stcg(reinterpret_cast<float4 *>(dst) + i, v);
                 }
-                __stcg(a.part_ml + part, make_float2(m, l));
+            }
+            if (!whole) {
+                // this CTA's part of the item is out; whoever is last joins them all
                 __threadfence();
                 if (!group_sync()) break;
                 if (row == 0) {
@@ -785,53 +793,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float2 e = __ldcg(a.part_ml + from(c) + lane);
                         l += e.y * max_factor(e.x, m);
                     }
-                    const RowEnd e = row_end<D>(a, out < 0 ? 0 : out, m, l, live);
+                    e = row_end<D>(a, out < 0 ? 0 : out, m, l, live);
+                    dst = row_target(a);
+                    front = row_front(a);
 #pragma unroll 1
                     for (int q = 0; q < D / 32; ++q) {
-                        // 32 columns of the warp's rows, whole lines; two parts' loads
-                        // at once
+                        // 32 columns of the warp's rows, whole lines
                         float4 sum[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                         const int col = 32 * q + 4 * (lane & 7);
 #pragma unroll 1
-                        for (int c = 0; c < p.npieces; c += 2) {
-                            const bool two = c + 1 < p.npieces;
-                            const int64_t at[2] = {from(c), from(two ? c + 1 : c)};
-                            float wt[2];
-                            float4 v[2][8];
+                        for (int c = 0; c < p.npieces; ++c) {
+                            const float mc = __ldcg(a.part_ml + from(c) + lane).x;
+                            const float4 *src = reinterpret_cast<const float4 *>(
+                                a.part_o + (from(c) + (lane >> 3)) * D + col);
+                            float4 v[8];
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                wt[j] = __ldcg(a.part_ml + at[j] + lane).x;
+                            for (int i = 0; i < 8; ++i) v[i] = __ldcg(src + i * D);
+                            const float wt = max_factor(mc, m);
 #pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    v[j][i] = __ldcg(reinterpret_cast<const float4 *>(
-                                        a.part_o + (at[j] + 4 * i + (lane >> 3)) * D + col));
+                            for (int i = 0; i < 8; ++i) {
+                                const float f = __shfl_sync(0xffffffffu, wt, 4 * i + (lane >> 3));
+                                sum[i].x += v[i].x * f;
+                                sum[i].y += v[i].y * f;
+                                sum[i].z += v[i].z * f;
+                                sum[i].w += v[i].w * f;
                             }
-                            wt[0] = max_factor(wt[0], m);
-                            wt[1] = two ? max_factor(wt[1], m) : 0.0f;
-#pragma unroll
-                            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const float f =
-                                        __shfl_sync(0xffffffffu, wt[j], 4 * i + (lane >> 3));
-                                    sum[i].x += v[j][i].x * f;
-                                    sum[i].y += v[j][i].y * f;
-                                    sum[i].z += v[j][i].z * f;
-                                    sum[i].w += v[j][i].w * f;
-                                }
                         }
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int rr = 4 * i + (lane >> 3);
                             const int64_t to_row = __shfl_sync(0xffffffffu, out, rr);
                             const float own = __shfl_sync(0xffffffffu, e.own, rr);
-                            const float front = __shfl_sync(0xffffffffu, e.front, rr);
-                            if (to_row >= 0)
-                                finish4(a, to_row * D + col, front,
-                                        make_float4(sum[i].x * own, sum[i].y * own,
-                                                    sum[i].z * own, sum[i].w * own));
+                            const float part_f = __shfl_sync(0xffffffffu, e.front, rr);
+                            if (to_row < 0) continue;
+                            float4 v = make_float4(sum[i].x * own, sum[i].y * own,
+                                                   sum[i].z * own, sum[i].w * own);
+                            if (front) {
+                                const float4 f = *reinterpret_cast<const float4 *>(
+                                    front + to_row * D + col);
+                                v.x += f.x * part_f;
+                                v.y += f.y * part_f;
+                                v.z += f.z * part_f;
+                                v.w += f.w * part_f;
+                            }
+                            *reinterpret_cast<float4 *>(dst + to_row * D + col) = v;
                         }
                     }
                 }

@@ -41,7 +41,7 @@ static void check(PagedArgs a, int grid, int min_pairs) {
             while (a.kstart + n * KT < last) ++n;
             CHECK(n == key_tiles<KT>(a, s, j));
             for (int h = 0; h < a.Hkv; ++h)
-                for (int k = 0; k < n + PAD; ++k)  // the last PAD without work
+                for (int k = 0; k < n + (a.prefix_phase ? 0 : PAD); ++k)  // the last without work
                     line.emplace_back(b, j, h, k < n ? k : -1);
         }
         const int64_t pairs = pairs_before<KT, PAD>(a, s, row_tiles(a, s));
@@ -57,17 +57,15 @@ static void check(PagedArgs a, int grid, int min_pairs) {
     std::map<std::tuple<int, int, int>, int> want;
     for (int c = 0; c < workers; ++c) {
         Share sh;
-        sh.total = total;
-        sh.workers = workers;
-        sh.begin = share_begin(total, workers, c);
-        sh.end = share_begin(total, workers, c + 1);
+        set_shares(sh, (int)total, workers, c);
+        CHECK(sh.begin == total * c / workers && sh.end == total * (c + 1) / workers);
         CHECK(sh.begin == at && sh.end > sh.begin);
         sh.seq = 0;
         for (int b = 0; b < nb; ++b)
             if (seq_begin[b] <= sh.begin &&
                 (b + 1 == nb ? total : seq_begin[b + 1]) > seq_begin[b])
                 sh.seq = b;
-        sh.seq_begin = seq_begin[sh.seq];
+        sh.seq_begin = (int)seq_begin[sh.seq];
         Walk<KT, PAD> w;
         w.start(a, sh);
         Piece p;
@@ -105,10 +103,12 @@ static void check(PagedArgs a, int grid, int min_pairs) {
     }
     CHECK(at == total);
     for (auto &e : parts) CHECK((int)e.second.size() == want[e.first]);
+    Share sh;
+    set_shares(sh, (int)total, workers, 0);
     for (int64_t x = 0; x < total; x += 1 + total / 97) {
-        const int c = share_of(total, workers, x);
-        CHECK(c >= 0 && c < workers && share_begin(total, workers, c) <= x &&
-              x < share_begin(total, workers, c + 1));
+        const int c = share_of(sh, (int)x);
+        CHECK(c >= 0 && c < workers && total * c / workers <= x &&
+              x < total * (c + 1) / workers);
     }
 }
 
@@ -152,9 +152,9 @@ int main() {
     }
     // the closed-form sum against a loop
     for (int trial = 0; trial < 20000; ++trial) {
-        const int64_t n = pick(0, 60), m = pick(1, 130), p = pick(0, 300), q = pick(0, 3000);
+        const int n = pick(0, 60), m = pick(1, 130), p = pick(0, 300), q = pick(0, 3000);
         int64_t want = 0;
-        for (int64_t i = 0; i < n; ++i) want += (p * i + q) / m;
+        for (int i = 0; i < n; ++i) want += (p * i + q) / m;
         CHECK(floor_sum(n, m, p, q) == want);
     }
     std::printf("%lld checks, %lld failures\n", g_checked, g_fail);

@@ -57,7 +57,7 @@ SHAPE = [
     (dict(D=96), UNSUP), (dict(D=0), INVALID), (dict(page_size=48), UNSUP),
     (dict(page_size=8), UNSUP), (dict(page_size=512), UNSUP), (dict(ctype=2), INVALID),
     (dict(ctype=-1), INVALID), (dict(num_pages=-1), INVALID), (dict(num_pages=0), INVALID),
-    (dict(B=-1), INVALID), (dict(max_pages=-1), INVALID), (dict(T=(1 << 30) + 1), UNSUP),
+    (dict(B=-1), INVALID), (dict(max_pages=-1), INVALID), (dict(T=(1 << 24) + 1), UNSUP),
     (dict(max_pages=1 << 27), UNSUP), (dict(num_pages=1 << 26), UNSUP),
     (dict(num_pages=1 << 62), UNSUP), (dict(max_pages=1 << 62), UNSUP),
     (dict(ldq=508), INVALID), (dict(ldq=514), ALIGN), (dict(Hq=516, Hkv=4), UNSUP),
