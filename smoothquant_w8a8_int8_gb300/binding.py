@@ -159,26 +159,40 @@ def _need(t: torch.Tensor, dtype, name: str, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-@contextlib.contextmanager
-def _on(t: torch.Tensor, stream=None):
+class _on:
     """Makes t's device and the given stream (t's device's current one if None)
     current, so that what a call allocates belongs to the stream that uses it;
-    yields the stream's handle."""
-    if stream is None and t.device.index == torch.cuda.current_device():
-        yield _stream()
-        return
-    with torch.cuda.device(t.device):
-        s = stream if stream is not None else torch.cuda.current_stream()
-        if s.device != t.device:
-            raise ValueError(f"the stream is on {s.device}, the tensors on {t.device}")
-        with torch.cuda.stream(s):
-            yield _stream(s)
+    yields the stream's handle.  (A class, and the raw handle: these calls may
+    take less time on the device than a generator and a Stream object on the
+    host.)"""
+    __slots__ = ("dev", "stream", "held")
+
+    def __init__(self, t: torch.Tensor, stream=None):
+        self.dev, self.stream, self.held = t.device, stream, None
+
+    def __enter__(self):
+        if self.stream is None and self.dev.index == torch.cuda.current_device():
+            return torch._C._cuda_getCurrentRawStream(self.dev.index)
+        if self.stream is not None and self.stream.device != self.dev:
+            raise ValueError(f"the stream is on {self.stream.device}, the tensors on {self.dev}")
+        self.held = contextlib.ExitStack()
+        self.held.enter_context(torch.cuda.device(self.dev))
+        if self.stream is not None:
+            self.held.enter_context(torch.cuda.stream(self.stream))
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.held is not None:
+            self.held.close()
+        return False
 
 
-def _same_device(ref: torch.Tensor, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} must be on {ref.device}, is on {t.device}")
+def _arg(t: torch.Tensor, dtype, name: str, shape, dev):
+    """_need and the device, in one pass over a good tensor; returns its address."""
+    if t.dtype is not dtype or t.device != dev or t.shape != shape or not t.is_contiguous():
+        _need(t, dtype, name, shape)
+        raise ValueError(f"{name} must be on {dev}, is on {t.device}")
+    return t.data_ptr()
 
 
 def operand_bytes(rows: int, K: int) -> int:
@@ -337,36 +351,34 @@ def rmsnorm_quant(H: torch.Tensor, gamma: torch.Tensor, eps: float, s: torch.Ten
     there is a residual).  `out` may give those six (all but x_scale may be
     None); its R may be H or the residual itself."""
     _need(H, torch.float32, "H")
+    if H.dim() != 2:
+        raise ValueError("H must have shape (M, K)")
     M, K = H.shape
-    for t, n in ((gamma, "gamma"), (s, "s")):
-        _need(t, torch.float32, n, (K,))
-    if residual is not None:
-        _need(residual, torch.float32, "residual", (M, K))
+    dev, f32 = H.device, torch.float32
+    def at(t, dtype, name, shape):
+        return None if t is None else _arg(t, dtype, name, shape, dev)
+
     with _on(H, stream) as st:
         if out is not None:
             Xq, sx, Xop, Y, l1, R = out
-            for t, n, dt, shape in ((Xq, "Xq", torch.int8, (M, K)),
-                                    (sx, "x_scale", torch.float32, (M,)),
-                                    (Xop, "Xop", torch.bfloat16, (M, K)),
-                                    (Y, "Y", torch.float32, (M, K)),
-                                    (l1, "l1", torch.int32, (M,)),
-                                    (R, "R", torch.float32, (M, K))):
-                if t is not None:
-                    _need(t, dt, n, shape)
+            if sx is None:
+                raise ValueError("out must give x_scale")
+            outs = (at(R, f32, "R", (M, K)), at(Y, f32, "Y", (M, K)),
+                    at(Xq, torch.int8, "Xq", (M, K)), at(sx, f32, "x_scale", (M,)),
+                    at(Xop, torch.bfloat16, "Xop", (M, K)), at(l1, torch.int32, "l1", (M,)))
         else:
-            new = lambda want, dt, *shape: (  # noqa: E731
-                torch.empty(shape, dtype=dt, device=H.device) if want else None)
-            Xq = new(want_q, torch.int8, M, K)
-            sx = new(True, torch.float32, M)
-            Xop = new(want_op, torch.bfloat16, M, K)
-            Y = new(want_y, torch.float32, M, K)
-            l1 = new(want_l1, torch.int32, M)
-            R = new(residual is not None if want_sum is None else want_sum, torch.float32, M, K)
-        _same_device(H, gamma=gamma, s=s, residual=residual, Xq=Xq, x_scale=sx, Xop=Xop, Y=Y,
-                     l1=l1, R=R)
-        _check(load().sq_rmsnorm_quant(_p(H), _p(residual), _p(gamma), float(eps), _p(s), M, K,
-                                       float(static_scale), _p(R), _p(Y), _p(Xq), _p(sx), _p(Xop),
-                                       _p(l1), st), "sq_rmsnorm_quant")
+            Xq = torch.empty(M, K, dtype=torch.int8, device=dev) if want_q else None
+            sx = torch.empty(M, dtype=f32, device=dev)
+            Xop = torch.empty(M, K, dtype=torch.bfloat16, device=dev) if want_op else None
+            Y = torch.empty_like(H) if want_y else None
+            l1 = torch.empty(M, dtype=torch.int32, device=dev) if want_l1 else None
+            R = torch.empty_like(H) if (residual is not None if want_sum is None
+                                        else want_sum) else None
+            outs = [None if t is None else t.data_ptr() for t in (R, Y, Xq, sx, Xop, l1)]
+        _check(load().sq_rmsnorm_quant(
+            H.data_ptr(), at(residual, f32, "residual", (M, K)), at(gamma, f32, "gamma", (K,)),
+            float(eps), at(s, f32, "s", (K,)), M, K, float(static_scale), *outs, st),
+            "sq_rmsnorm_quant")
     return Xq, sx, Xop, Y, l1, R
 
 
@@ -378,10 +390,9 @@ def rope_table(inv_freq: torch.Tensor, positions: int, out=None, stream=None) ->
     with _on(inv_freq, stream) as st:
         if out is None:
             out = torch.empty(int(positions), n, 2, dtype=torch.float32, device=inv_freq.device)
-        _need(out, torch.float32, "table", (int(positions), n, 2))
-        _same_device(inv_freq, table=out)
-        _check(load().sq_rope_table(_p(inv_freq), int(positions), 2 * n, _p(out), st),
-               "sq_rope_table")
+        _check(load().sq_rope_table(inv_freq.data_ptr(), int(positions), 2 * n,
+                                    _arg(out, torch.float32, "table", (int(positions), n, 2),
+                                         inv_freq.device), st), "sq_rope_table")
     return out
 
 
@@ -396,46 +407,43 @@ def empty_kv_cache(num_pages: int, kv_heads: int, page_size: int, D: int,
                  for _ in range(2))
 
 
-def _rows_of(t: torch.Tensor, cols: int, name: str, rows: Optional[int] = None) -> int:
+def _rows_of(t: torch.Tensor, cols: int, name: str, dev, rows: Optional[int] = None) -> int:
     """A 2-D fp32 view of `cols` columns whose rows may lie apart (a block of
     columns of a wider matrix); returns the row stride."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.float32:
-        raise ValueError(f"{name} must be {torch.float32}, got {t.dtype}")
+    if t.dtype is not torch.float32 or t.device != dev:
+        raise ValueError(f"{name} must be {torch.float32} on {dev}, is {t.dtype} on {t.device}")
     if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
         raise ValueError(f"{name} must have shape ({'T' if rows is None else rows}, {cols}), "
                          f"got {tuple(t.shape)}")
+    apart, step = t.stride()
     if t.shape[0] <= 1:  # a single row's stride says nothing
-        if t.shape[0] == 1 and cols > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name}'s columns must be contiguous")
-        return max(cols, 4)
-    if (cols > 1 and t.stride(1) != 1) or t.stride(0) < cols:
+        apart = cols
+    if (t.numel() and step != 1) or apart < cols:
         raise ValueError(f"{name}'s columns must be contiguous and its rows apart")
-    return t.stride(0)
+    return apart
 
 
 def _need_paged(k_cache, v_cache, block_table, q_start, kv_len):
     """Checks the cache and the batch's tables; returns (type, pages, Hkv, page size, D, B,
-    table width)."""
-    if k_cache.dtype not in _CACHE_TYPES:
+    table width) and the five addresses."""
+    ctype = _CACHE_TYPES.get(k_cache.dtype)
+    if ctype is None:
         raise ValueError(f"k_cache must be bfloat16 or float16, got {k_cache.dtype}")
     if k_cache.dim() != 4:
         raise ValueError("k_cache must have shape (num_pages, kv_heads, page_size, D)")
-    _need(k_cache, k_cache.dtype, "k_cache")
-    _need(v_cache, k_cache.dtype, "v_cache", k_cache.shape)
     if kv_len.dim() != 1:
         raise ValueError("kv_len must have one dimension")
     B = kv_len.shape[0]
-    _need(kv_len, torch.int32, "kv_len")
-    _need(q_start, torch.int32, "q_start", (B + 1,))
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must have shape ({B}, max_pages)")
-    _need(block_table, torch.int32, "block_table")
-    _same_device(k_cache, v_cache=v_cache, block_table=block_table, q_start=q_start,
-                 kv_len=kv_len)
-    pages, Hkv, page_size, D = k_cache.shape
-    return _CACHE_TYPES[k_cache.dtype], pages, Hkv, page_size, D, B, block_table.shape[1]
+    _need(k_cache, k_cache.dtype, "k_cache")
+    dev, i32, shape = k_cache.device, torch.int32, k_cache.shape
+    pages, Hkv, page_size, D = shape
+    width = block_table.shape[1]
+    return (ctype, pages, Hkv, page_size, D, B, width), (
+        k_cache.data_ptr(), _arg(v_cache, k_cache.dtype, "v_cache", shape, dev),
+        _arg(block_table, i32, "block_table", (B, width), dev),
+        _arg(q_start, i32, "q_start", (B + 1,), dev), _arg(kv_len, i32, "kv_len", (B,), dev))
 
 
 def kv_append(QKV: torch.Tensor, Hq: int, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -446,27 +454,28 @@ def kv_append(QKV: torch.Tensor, Hq: int, k_cache: torch.Tensor, v_cache: torch.
     [T, (Hq + 2 Hkv) * D] and appends keys and values to the paged cache;
     returns the rotated queries [T, Hq * D].  rope: rope_table's [positions, n,
     2], None for no rotation.  q_out may be the view QKV[:, :Hq * D] (in place)."""
-    ctype, pages, Hkv, page_size, D, B, width = _need_paged(k_cache, v_cache, block_table,
-                                                            q_start, kv_len)
-    _need(QKV, torch.float32, "QKV")
-    if QKV.dim() != 2 or QKV.shape[1] != (Hq + 2 * Hkv) * D:
-        raise ValueError(f"QKV must have shape (T, {(Hq + 2 * Hkv) * D}), got {tuple(QKV.shape)}")
+    (ctype, pages, Hkv, page_size, D, B, width), (k, v, table, starts, lens) = _need_paged(
+        k_cache, v_cache, block_table, q_start, kv_len)
+    dev, f32 = k_cache.device, torch.float32
+    if QKV.dim() != 2:
+        raise ValueError(f"QKV must have shape (T, {(Hq + 2 * Hkv) * D})")
     T = QKV.shape[0]
+    qkv = _arg(QKV, f32, "QKV", (T, (Hq + 2 * Hkv) * D), dev)
     rot = positions = 0
+    rope_at = None
     if rope is not None:
         if rope.dim() != 3 or rope.shape[2] != 2:
             raise ValueError("rope must have shape (positions, n, 2)")
-        _need(rope, torch.float32, "rope")
+        rope_at = _arg(rope, f32, "rope", rope.shape, dev)
         positions, rot = rope.shape[0], 2 * rope.shape[1]
     with _on(QKV, stream) as st:
         if q_out is None:
-            q_out = torch.empty(T, Hq * D, dtype=torch.float32, device=QKV.device)
-        ldq = _rows_of(q_out, Hq * D, "q_out", T)
-        _same_device(QKV, k_cache=k_cache, rope=rope, q_out=q_out)
-        _check(load().sq_kv_append(_p(QKV), T, Hq, Hkv, D, _p(rope), positions, rot,
-                                   int(bool(interleaved)), _p(q_start), _p(kv_len), B,
-                                   _p(block_table), width, _p(k_cache), _p(v_cache), ctype, pages,
-                                   page_size, _p(q_out), ldq, st), "sq_kv_append")
+            q_out = torch.empty(T, Hq * D, dtype=f32, device=dev)
+        ldq = _rows_of(q_out, Hq * D, "q_out", dev, T)
+        _check(load().sq_kv_append(qkv, T, Hq, Hkv, D, rope_at, positions, rot,
+                                   1 if interleaved else 0, starts, lens, B, table, width, k, v,
+                                   ctype, pages, page_size, q_out.data_ptr(), ldq, st),
+               "sq_kv_append")
     return q_out
 
 
@@ -493,35 +502,34 @@ def paged_attention(Q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     call at a time uses (empty_workspace(paged_attention_workspace_bytes(...)));
     a fresh one is made if None.  With `out`, rows of no sequence are left as
     they are; without it they are zeros."""
-    ctype, pages, Hkv, page_size, D, B, width = _need_paged(k_cache, v_cache, block_table,
-                                                            q_start, kv_len)
+    (ctype, pages, Hkv, page_size, D, B, width), (k, v, table, starts, lens) = _need_paged(
+        k_cache, v_cache, block_table, q_start, kv_len)
+    dev = k_cache.device
     if Q.dim() != 2 or Q.shape[1] % D != 0 or Q.shape[1] == 0:
         raise ValueError(f"Q must have shape (T, heads * {D}), got {tuple(Q.shape)}")
     T, Hq = Q.shape[0], Q.shape[1] // D
-    ldq = _rows_of(Q, Hq * D, "Q")
-    if prefix_len and prefix_pages is None:
-        raise ValueError("prefix_len without prefix_pages")
+    ldq = _rows_of(Q, Hq * D, "Q", dev)
+    pages_at = None
     if prefix_pages is not None:
-        _need(prefix_pages, torch.int32, "prefix_pages")
         if prefix_pages.dim() != 1 or prefix_pages.shape[0] * page_size < prefix_len:
             raise ValueError(f"prefix_pages must name every page of {prefix_len} positions")
+        pages_at = _arg(prefix_pages, torch.int32, "prefix_pages", prefix_pages.shape, dev)
+    elif prefix_len:
+        raise ValueError("prefix_len without prefix_pages")
     if scale is None:
         scale = 1.0 / float(D) ** 0.5
     with _on(Q, stream) as st:
         if out is None:
-            out = torch.zeros(T, Hq * D, dtype=torch.float32, device=Q.device)
-        _need(out, torch.float32, "out", (T, Hq * D))
+            out = torch.zeros(T, Hq * D, dtype=torch.float32, device=dev)
         if workspace is None:
             workspace = empty_workspace(
-                paged_attention_workspace_bytes(T, Hq, Hkv, D, prefix_len), Q.device)
-        wp, wn = _workspace(workspace)
-        _same_device(Q, k_cache=k_cache, prefix_pages=prefix_pages, workspace=workspace, out=out)
-        _check(load().sq_paged_attention(_p(Q), ldq, T, Hq, Hkv, D, _p(k_cache), _p(v_cache),
-                                         ctype, pages, page_size, _p(block_table), width,
-                                         _p(q_start), _p(kv_len), B,
-                                         T if max_q is None else int(max_q), _p(prefix_pages),
-                                         int(prefix_len), float(scale), _p(out), wp, wn, st),
-               "sq_paged_attention")
+                paged_attention_workspace_bytes(T, Hq, Hkv, D, prefix_len), dev)
+        _check(load().sq_paged_attention(
+            Q.data_ptr(), ldq, T, Hq, Hkv, D, k, v, ctype, pages, page_size, table, width, starts,
+            lens, B, T if max_q is None else int(max_q), pages_at, int(prefix_len), float(scale),
+            _arg(out, torch.float32, "out", (T, Hq * D), dev),
+            _arg(workspace, torch.uint8, "workspace", workspace.shape, dev), workspace.numel(),
+            st), "sq_paged_attention")
     return out
 
 

@@ -63,7 +63,7 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
     return *reinterpret_cast<uint32_t *>(&v);
 }
 
-// One block per token.  A unit is 8 elements of a head: for the "half" pairs
+// A row of blocks per token.  A unit is 8 elements of a head: for the "half" pairs
 // elements 4u.. and rot/2 + 4u.., otherwise elements 8u...
 template <bool BF>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(
@@ -87,7 +87,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(
             page = __ldg(block_table + b * max_pages + pos / page_size);
         const bool stored = page >= 0 && page < num_pages;
         const float *src = QKV + t * heads * D;
-        for (int u = threadIdx.x; u < heads * upd; u += kAppendThreads) {
+        for (int u = blockIdx.y * kAppendThreads + threadIdx.x; u < heads * upd;
+             u += kAppendThreads * gridDim.y) {
             const int head = u / upd, e = u % upd;
             const bool turn = head < Hq + Hkv && e < rot / 8;
             const bool split = turn && !interleaved;
@@ -163,9 +164,12 @@ sq_status launch_kv_append(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv,
     DeviceInfo di;
     sq_status rc = device_info(&di);
     if (rc != SQ_OK) return rc;
+    // a few tokens: a unit per thread; many: a block per token
+    const int64_t units = (Hq + 2 * Hkv) * D / 8;
+    const int64_t gy = T <= 2 * di.sms ? (units + kAppendThreads - 1) / kAppendThreads : 1;
     const int64_t grid = std::min<int64_t>(T, (int64_t)di.sms * 64);
     return launch_pdl(cache_type == SQ_CACHE_BF16 ? kv_append_kernel<true> : kv_append_kernel<false>,
-                      dim3((unsigned)grid), dim3(kAppendThreads), 0, st, 1, QKV, T, (int)Hq,
+                      dim3((unsigned)grid, (unsigned)gy), dim3(kAppendThreads), 0, st, 1, QKV, T, (int)Hq,
                       (int)Hkv, (int)D, rope, rope_positions, (int)rot, interleaved, q_start,
                       kv_len, (int)B, block_table, max_pages, static_cast<uint16_t *>(k_cache),
                       static_cast<uint16_t *>(v_cache), num_pages, (int)page_size, Q, ldq);

@@ -19,20 +19,20 @@
 namespace sq {
 namespace {
 
-// rows of up to 4096 elements: 256 threads of 4 float4; up to 8192: 8 float4;
-// up to 16384: 512 threads of 8 float4
 constexpr int kMaxRow = 16384;
 
-// A group of tpr threads owns a row.  STATIC: the given scale; otherwise the
-// row's own.  The smoothing factors, negated, and their reciprocals stand in
-// shared-memory tables, and the codes come from p = RN(RN(y RN(1/s)) RN(1/scale))
-// with the elements within 2^-14 of a half-integer on IEEE divisions: the same
-// codes as the division's (p is within 4.2e-5 of fl(fl(y/s)/scale) for
-// |quotient| <= 127.0001).  A row whose maximum is NaN or outside
-// [2^-60, 2^100], and every row when a static scale lies outside [2^-60, 2^60]
-// (fast == 0), takes IEEE divisions throughout.
-template <bool STATIC, int VPT, int NT>
-__global__ void __launch_bounds__(NT, VPT == 4 ? 4 : 512 / NT) rmsnorm_quant_kernel(
+// A group of tpr threads (whole warps) owns a row, VPT float4 of it in each
+// thread's registers.  STATIC: the given scale; otherwise the row's own.  The
+// smoothing factors, negated, and their reciprocals stand in shared-memory
+// tables, or, for a block of one row (ONE), in registers: few rows are bound by
+// latency, and a table costs them a round trip and a barrier.  The codes come
+// from p = RN(RN(y RN(1/s)) RN(1/scale)) with the elements within 2^-14 of a
+// half-integer on IEEE divisions: the same codes as the division's (p is within
+// 4.2e-5 of fl(fl(y/s)/scale) for |quotient| <= 127.0001).  A row whose maximum
+// is NaN or outside [2^-60, 2^100], and every row when a static scale lies
+// outside [2^-60, 2^60] (fast == 0), takes IEEE divisions throughout.
+template <bool STATIC, int VPT, bool ONE>
+__global__ void __launch_bounds__(1024, 1) rmsnorm_quant_kernel(
     const float *H, const float *residual, const float *__restrict__ gamma, float eps,
     const float *__restrict__ s, int64_t rows, int K4, int tpr, float *R, float *Y,
     int8_t *__restrict__ q, float *__restrict__ scale, __nv_bfloat16 *__restrict__ op,
@@ -40,47 +40,88 @@ __global__ void __launch_bounds__(NT, VPT == 4 ? 4 : 512 / NT) rmsnorm_quant_ker
     extern __shared__ float4 qtab[];
     float4 *nstab = qtab;      // -s
     float4 *ytab = qtab + K4;  // RN(1/s) or NaN
-    __shared__ float red2[2][NT / 32];
+    __shared__ float red2[2][32];
     pdl_launch_dependents();
     pdl_wait();
     int rb = 0;  // the slot array of the group's next reduction (see row_group_reduce)
-    const int rpb = NT / tpr;
+    const int rpb = blockDim.x / tpr;
     const int g = threadIdx.x / tpr;
     const int t = threadIdx.x % tpr;
     const float4 *s4 = reinterpret_cast<const float4 *>(s);
     const float4 *g4 = reinterpret_cast<const float4 *>(gamma);
-    for (int j = threadIdx.x; j < K4; j += NT) {
-        const float4 v = __ldg(s4 + j);
-        nstab[j] = make_float4(-v.x, -v.y, -v.z, -v.w);
-        ytab[j] = make_float4(smooth_recip(v.x), smooth_recip(v.y), smooth_recip(v.z),
-                              smooth_recip(v.w));
+    const int64_t tiles = (rows + rpb - 1) / rpb;
+    // the row `ahead` tiles on into L2, while the next one is worked on
+    auto prefetch = [&](int64_t tile) {
+        const int64_t row = tile * rpb + g;
+        if (ONE || t != 0 || tile >= tiles || row >= rows) return;
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(H + row * K4 * 4),
+                     "r"(K4 * 16)
+                     : "memory");
+        if (residual)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                             residual + row * K4 * 4),
+                         "r"(K4 * 16)
+                         : "memory");
+    };
+    float4 ns_r[VPT], ys_r[VPT], g_r[VPT];  // (ONE)
+    if (!ONE) {
+        prefetch(blockIdx.x);
+        for (int j = threadIdx.x; j < K4; j += blockDim.x) {
+            const float4 v = __ldg(s4 + j);
+            nstab[j] = make_float4(-v.x, -v.y, -v.z, -v.w);
+            ytab[j] = make_float4(smooth_recip(v.x), smooth_recip(v.y), smooth_recip(v.z),
+                                  smooth_recip(v.w));
+        }
+        __syncthreads();
     }
-    __syncthreads();
     const unsigned long long magic2 = pk(kRoundMagic, kRoundMagic);
     const float Kf = (float)(4 * K4);
-    const int64_t tiles = (rows + rpb - 1) / rpb;
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int64_t row = tile * rpb + g;
         const bool valid = row < rows;
         const int64_t off = (valid ? row : 0) * K4;
         const float4 *h4 = reinterpret_cast<const float4 *>(H) + off;
+        const float4 *r4 = reinterpret_cast<const float4 *>(residual) + off;
         float4 v[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int j = t + i * tpr;
             v[i] = (valid && j < K4) ? __ldcs(h4 + j) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if (residual) {
-            const float4 *r4 = reinterpret_cast<const float4 *>(residual) + off;
+        if (ONE) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int j = t + i * tpr;
-                if (valid && j < K4) {
-                    const float4 r = __ldcs(r4 + j);
-                    v[i] = make_float4(v[i].x + r.x, v[i].y + r.y, v[i].z + r.z, v[i].w + r.w);
-                }
+                ns_r[i] = j < K4 ? __ldg(s4 + j) : make_float4(1.f, 1.f, 1.f, 1.f);
+                g_r[i] = j < K4 ? __ldg(g4 + j) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
         }
+        if (residual) {
+            float4 r[VPT];
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int j = t + i * tpr;
+                r[i] = (valid && j < K4) ? __ldcs(r4 + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            prefetch(tile + gridDim.x);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                v[i] = make_float4(v[i].x + r[i].x, v[i].y + r[i].y, v[i].z + r[i].z,
+                                   v[i].w + r[i].w);
+        } else {
+            prefetch(tile + gridDim.x);
+        }
+        if (ONE) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const float4 x = ns_r[i];
+                ys_r[i] = make_float4(smooth_recip(x.x), smooth_recip(x.y), smooth_recip(x.z),
+                                      smooth_recip(x.w));
+                ns_r[i] = make_float4(-x.x, -x.y, -x.z, -x.w);
+            }
+        }
+        auto neg_s = [&](int i, int j) { return ONE ? ns_r[i] : nstab[j]; };
+        auto recip_s = [&](int i, int j) { return ONE ? ys_r[i] : ytab[j]; };
         float sq = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -100,7 +141,7 @@ __global__ void __launch_bounds__(NT, VPT == 4 ? 4 : 512 / NT) rmsnorm_quant_ker
         for (int i = 0; i < VPT; ++i) {
             const int j = t + i * tpr;
             if (j >= K4) continue;
-            const float4 gv = __ldg(g4 + j);
+            const float4 gv = ONE ? g_r[i] : __ldg(g4 + j);
             float4 y;
             y.x = __fmul_rn(__fmul_rn(v[i].x, rstd), gv.x);
             y.y = __fmul_rn(__fmul_rn(v[i].y, rstd), gv.y);
@@ -109,7 +150,7 @@ __global__ void __launch_bounds__(NT, VPT == 4 ? 4 : 512 / NT) rmsnorm_quant_ker
             if (Y && valid) reinterpret_cast<float4 *>(Y)[off + j] = y;
             v[i] = y;
             if (!STATIC) {
-                const float4 ys = ytab[j], ns = nstab[j];
+                const float4 ys = recip_s(i, j), ns = neg_s(i, j);
                 const unsigned long long x01 = pk(y.x, y.y), x23 = pk(y.z, y.w);
                 const unsigned long long y01 = pk(ys.x, ys.y), y23 = pk(ys.z, ys.w);
                 const unsigned long long q01 = mul2(x01, y01), q23 = mul2(x23, y23);
@@ -129,10 +170,11 @@ __global__ void __launch_bounds__(NT, VPT == 4 ? 4 : 512 / NT) rmsnorm_quant_ker
         if (!STATIC) {
             if (exact) {
                 float me = 0.0f;
+#pragma unroll
                 for (int i = 0; i < VPT; ++i) {
                     const int j = t + i * tpr;
                     if (j >= K4) continue;
-                    const float4 ns = nstab[j];
+                    const float4 ns = neg_s(i, j);
                     me = fmaxf(me, fmaxf(abs_quotient(v[i].x, -ns.x), abs_quotient(v[i].y, -ns.y)));
                     me = fmaxf(me, fmaxf(abs_quotient(v[i].z, -ns.z), abs_quotient(v[i].w, -ns.w)));
                 }
@@ -144,54 +186,38 @@ __global__ void __launch_bounds__(NT, VPT == 4 ? 4 : 512 / NT) rmsnorm_quant_ker
         float a1 = 0.0f;
         if (valid) {
             if (t == 0) scale[row] = sc;
-            if (exact) {
-                for (int i = 0; i < VPT; ++i) {
-                    const int j = t + i * tpr;
-                    if (j >= K4) continue;
-                    const float4 ns = nstab[j];
-                    const float c0 = exact_code(v[i].x, -ns.x, sc);
-                    const float c1 = exact_code(v[i].y, -ns.y, sc);
-                    const float c2 = exact_code(v[i].z, -ns.z, sc);
-                    const float c3 = exact_code(v[i].w, -ns.w, sc);
-                    store4_codes(c0, c1, c2, c3, (off + j) * 4, q, op);
-                    a1 += (fabsf(c0) + fabsf(c1)) + (fabsf(c2) + fabsf(c3));
-                }
-            } else {
-                const float rsc = __frcp_rn(sc);
-                const unsigned long long r2 = pk(rsc, rsc);
+            const float rsc = __frcp_rn(sc);
+            const unsigned long long r2 = pk(rsc, rsc);
 #pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    const int j = t + i * tpr;
-                    if (j >= K4) continue;
-                    const float4 ys = ytab[j];
-                    const unsigned long long p01 =
-                        mul2(mul2(pk(v[i].x, v[i].y), pk(ys.x, ys.y)), r2);
-                    const unsigned long long p23 =
-                        mul2(mul2(pk(v[i].z, v[i].w), pk(ys.z, ys.w)), r2);
-                    const unsigned long long t01 = sub2(add2(p01, magic2), magic2);
-                    const unsigned long long t23 = sub2(add2(p23, magic2), magic2);
-                    float c[4], d[4];
-                    upk(t01, c[0], c[1]);
-                    upk(t23, c[2], c[3]);
-                    upk(sub2(p01, t01), d[0], d[1]);
-                    upk(sub2(p23, t23), d[2], d[3]);
-                    // NaN kept: a column whose s has no reciprocal
-                    const float dm = max3_nan(fabsf(d[0]), fabsf(d[1]),
-                                              max2_nan(fabsf(d[2]), fabsf(d[3])));
-                    if (!(dm <= kTieLimit)) {
-                        const float4 ns = nstab[j];
-                        if (!(fabsf(d[0]) <= kTieLimit)) c[0] = exact_code(v[i].x, -ns.x, sc);
-                        if (!(fabsf(d[1]) <= kTieLimit)) c[1] = exact_code(v[i].y, -ns.y, sc);
-                        if (!(fabsf(d[2]) <= kTieLimit)) c[2] = exact_code(v[i].z, -ns.z, sc);
-                        if (!(fabsf(d[3]) <= kTieLimit)) c[3] = exact_code(v[i].w, -ns.w, sc);
-                    }
-                    if (STATIC) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) c[e] = fminf(127.0f, fmaxf(-127.0f, c[e]));
-                    }
-                    store4_codes(c[0], c[1], c[2], c[3], (off + j) * 4, q, op);
-                    a1 += (fabsf(c[0]) + fabsf(c[1])) + (fabsf(c[2]) + fabsf(c[3]));
+            for (int i = 0; i < VPT; ++i) {
+                const int j = t + i * tpr;
+                if (j >= K4) continue;
+                const float4 ys = recip_s(i, j);
+                const unsigned long long p01 = mul2(mul2(pk(v[i].x, v[i].y), pk(ys.x, ys.y)), r2);
+                const unsigned long long p23 = mul2(mul2(pk(v[i].z, v[i].w), pk(ys.z, ys.w)), r2);
+                const unsigned long long t01 = sub2(add2(p01, magic2), magic2);
+                const unsigned long long t23 = sub2(add2(p23, magic2), magic2);
+                float c[4], d[4];
+                upk(t01, c[0], c[1]);
+                upk(t23, c[2], c[3]);
+                upk(sub2(p01, t01), d[0], d[1]);
+                upk(sub2(p23, t23), d[2], d[3]);
+                // NaN kept: a column whose s has no reciprocal
+                const float dm = max3_nan(fabsf(d[0]), fabsf(d[1]),
+                                          max2_nan(fabsf(d[2]), fabsf(d[3])));
+                if (exact || !(dm <= kTieLimit)) {
+                    const float4 ns = neg_s(i, j);
+                    if (exact || !(fabsf(d[0]) <= kTieLimit)) c[0] = exact_code(v[i].x, -ns.x, sc);
+                    if (exact || !(fabsf(d[1]) <= kTieLimit)) c[1] = exact_code(v[i].y, -ns.y, sc);
+                    if (exact || !(fabsf(d[2]) <= kTieLimit)) c[2] = exact_code(v[i].z, -ns.z, sc);
+                    if (exact || !(fabsf(d[3]) <= kTieLimit)) c[3] = exact_code(v[i].w, -ns.w, sc);
                 }
+                if (STATIC) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[e] = fminf(127.0f, fmaxf(-127.0f, c[e]));
+                }
+                store4_codes(c[0], c[1], c[2], c[3], (off + j) * 4, q, op);
+                a1 += (fabsf(c[0]) + fabsf(c[1])) + (fabsf(c[2]) + fabsf(c[3]));
             }
         }
         if (l1) {
@@ -217,41 +243,37 @@ sq_status launch_rmsnorm_quant(const float *H, const float *residual, const floa
     if (rc != SQ_OK) return rc;
     if (K > kMaxRow) return SQ_ERR_UNSUPPORTED;
     const int K4 = (int)(K / 4);
-    const int vi = K <= 4096 ? 0 : K <= 8192 ? 1 : 2;
-    const int ki = static_scale > 0.0f ? 1 : 0;
+    const bool one = rows <= di.sms && K4 <= 2048;
+    // one row per block: as few float4 per thread as 1024 threads allow; else four
+    const int vpt = !one ? 4 : K4 <= 1024 ? 1 : 2;
+    const int tpr = ((K4 + vpt - 1) / vpt + 31) / 32 * 32;
+    const int nt = one ? tpr : tpr * std::max(1, 256 / tpr);
     static const RmsKern kerns[2][3] = {
-        {rmsnorm_quant_kernel<false, 4, 256>, rmsnorm_quant_kernel<false, 8, 256>,
-         rmsnorm_quant_kernel<false, 8, 512>},
-        {rmsnorm_quant_kernel<true, 4, 256>, rmsnorm_quant_kernel<true, 8, 256>,
-         rmsnorm_quant_kernel<true, 8, 512>}};
+        {rmsnorm_quant_kernel<false, 1, true>, rmsnorm_quant_kernel<false, 2, true>,
+         rmsnorm_quant_kernel<false, 4, false>},
+        {rmsnorm_quant_kernel<true, 1, true>, rmsnorm_quant_kernel<true, 2, true>,
+         rmsnorm_quant_kernel<true, 4, false>}};
+    const int ki = static_scale > 0.0f ? 1 : 0, vi = one ? vpt - 1 : 2;
     const RmsKern kern = kerns[ki][vi];
-    const int vpt = vi == 0 ? 4 : 8, nt = vi == 2 ? 512 : 256;
-    int tpr = 32;
-    while (tpr * vpt < K4) tpr <<= 1;
-    const int64_t tiles = (rows + nt / tpr - 1) / (nt / tpr);
     // the range of scales for which the product decides the code (see the kernel)
     const int fast = static_scale >= 0x1p-60f && static_scale <= 0x1p60f;
-    const int smem = K4 * 32;
-    static std::mutex mu;
-    static int occ[64][2][3] = {};  // resident blocks at the widest row of each variant
-    int resident = 0;
-    {
+    const int smem = one ? 0 : K4 * 32;
+    const int64_t tiles = (rows + nt / tpr - 1) / (nt / tpr);
+    int64_t grid = tiles;
+    if (!one) {
+        static std::mutex mu;
+        static bool opted[64][2] = {};
         std::lock_guard<std::mutex> lock(mu);
-        int &o = occ[di.device & 63][ki][vi];
-        const int widest = (vi == 0 ? 4096 : vi == 1 ? 8192 : kMaxRow) * 8;
+        bool &o = opted[di.device & 63][ki];
         if (!o) {
-            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, widest) !=
-                    cudaSuccess ||
-                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, kern, nt, widest) !=
-                    cudaSuccess ||
-                o < 1) {
-                o = 0;
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kMaxRow * 8) != cudaSuccess)
                 return SQ_ERR_CUDA;
-            }
+            o = true;
         }
-        resident = o;
+        // 64 registers a thread: 1024 threads per SM; twice what fits at once
+        grid = std::min<int64_t>(tiles, 2 * (int64_t)di.sms * std::max(1, 1024 / nt));
     }
-    const int64_t grid = std::min<int64_t>(tiles, 2 * (int64_t)di.sms * resident);
     return launch_pdl(kern, dim3((unsigned)grid), dim3((unsigned)nt), (size_t)smem, st, 1, H,
                       residual, gamma, eps, s, rows, K4, tpr, R, Y, q, scale, op, l1,
                       static_scale, fast);
