@@ -127,43 +127,25 @@ __device__ __forceinline__ int row_limit(const PagedArgs &a, const Piece &p, int
     return min(a.prefix_len, kv - end + tok + 1);
 }
 
-// A row's last step, from its maximum m (log2 units) and sum l: the factors of
-// its own unnormalised output and of the prefix's, or the prefix's buffer.
-// row = token * Hq + query head; `first`: the caller that stores m and l.
-struct RowEnd {
-    float own, front;
-    int64_t at;
-};
-template <int D>
-__device__ __forceinline__ RowEnd row_end(const PagedArgs &a, int64_t row, float m, float l,
-                                          bool first) {
-    RowEnd e;
-    e.at = row * D;
-    e.own = 1.0f;
-    e.front = 0.0f;
+// Where a row of an item starts: with no key, or, at the suffix's first key, with
+// the prefix's maximum, sum and output (so that its loads are on their way while
+// the item's first keys are).  row = token * Hq + query head.
+__device__ __forceinline__ bool starts_with_prefix(const PagedArgs &a, const Piece &p) {
+    return !a.prefix_phase && a.prefix_len > 0 && p.key0 == a.kstart;
+}
+// A row's last step, from its maximum m (log2 units) and sum l: the factor of its
+// output on the way to the prefix's buffer (with m and l, stored by the caller
+// that is `first`) or to the result.
+__device__ __forceinline__ float row_factor(const PagedArgs &a, int64_t row, float m, float l,
+                                            bool first) {
     if (a.prefix_phase) {
         if (first) a.prefix_ml[row] = make_float2(m, l);
-        return e;
+        return 1.0f;
     }
-    if (a.prefix_len > 0) {
-        const float2 f = a.prefix_ml[row];
-        const float top = fmaxf(m, f.x);
-        e.own = max_factor(m, top);
-        e.front = max_factor(f.x, top);
-        l = l * e.own + f.y * e.front;
-    }
-    const float inv = l > 0.0f ? __frcp_rn(l) : 0.0f;  // no key: zeros
-    e.own *= inv;
-    e.front *= inv;
-    return e;
+    return l > 0.0f ? __frcp_rn(l) : 0.0f;  // no key: zeros
 }
-// Where such a row goes (its element offset in the buffer is RowEnd::at), and
-// what is added to it.
 __device__ __forceinline__ float *row_target(const PagedArgs &a) {
     return a.prefix_phase ? a.prefix_o : a.O;
-}
-__device__ __forceinline__ const float *row_front(const PagedArgs &a) {
-    return a.prefix_phase || a.prefix_len == 0 ? nullptr : a.prefix_o;
 }
 
 }  // namespace

@@ -136,7 +136,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     // ---- the copies: one step of the share per call, or nothing at its end
     Walk<kKT, kPad> walk;
     walk.start(a, share);
-    int npieces = 0, left = 0, key = 0, held = -1, entry = -1, filled = 0;
+    int npieces = 0, left = 0, key = 0, held = -1, entry = -1;
+    int buf = 0;  // the ring's buffer that is filled next
     int64_t head_row = 0;  // the piece's head, in cache rows of a page
     int keys = 0;
     unsigned holes = 0;    // bit i: the page of the step in buffer i is missing
@@ -166,24 +167,39 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             }
             const int e = __shfl_sync(0xffffffffu, entry, idx & 31);
             const bool there = e >= 0 && e < a.num_pages;
-            holes = (holes & ~(1u << (filled % ST))) | (there ? 0u : 1u << (filled % ST));
+            holes = (holes & ~(1u << buf)) | (there ? 0u : 1u << buf);
             const int64_t row0 = (there ? (((int64_t)e * a.Hkv) << a.page_shift) + head_row : 0) +
                                  (key & ((1 << a.page_shift) - 1));
-            const uint32_t dst = ring + (filled % ST) * C::kStepBytes;
+            // lane: chunk lane % (D / 8) of row lane / (D / 8) of every kStride rows; the
+            // step's 16 rows are contiguous in the cache
+            constexpr int kLanes = D / 8, kCopies = kKT * kLanes / 32, kStride = 32 / kLanes;
+            const int r0 = lane / kLanes, ch = lane % kLanes;
+            const uint32_t dst = ring + buf * C::kStepBytes + r0 * D * 2;
+            const int64_t from = row0 * D + lane * 8;
+            const uint16_t *ks = k_cache + from, *vs = v_cache + from;
+            if (there && key + kKT <= keys && key >= first_key) {
 #pragma unroll
-            for (int j = 0; j < kKT * D / 8 / 32; ++j) {
-                const int c = j * 32 + lane;
-                const int r = c / (D / 8), ch = c % (D / 8);
-                const bool in = there && key + r < keys && key + r >= first_key;
-                const int64_t off = (row0 + r) * D + ch * 8;
-                const uint32_t d = dst + r * D * 2 + ((ch ^ (r & 7)) << 4);
-                copy16(d, k_cache + (in ? off : 0), in);
-                copy16(d + kKT * D * 2, v_cache + (in ? off : 0), in);
+                for (int j = 0; j < kCopies; ++j) {
+                    const uint32_t d =
+                        dst + j * 512 + (((ch ^ r0) ^ (j * kStride & 7)) << 4);
+                    copy16(d, ks + j * 256, true);
+                    copy16(d + kKT * D * 2, vs + j * 256, true);
+                }
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < kCopies; ++j) {
+                    const int r = r0 + j * kStride;
+                    const bool in = there && key + r < keys && key + r >= first_key;
+                    const uint32_t d =
+                        dst + j * 512 + (((ch ^ r0) ^ (j * kStride & 7)) << 4);
+                    copy16(d, in ? ks + j * 256 : k_cache, in);
+                    copy16(d + kKT * D * 2, in ? vs + j * 256 : v_cache, in);
+                }
             }
             key += kKT;
             --left;
         }
-        ++filled;
+        if (++buf == ST) buf = 0;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll 1
@@ -191,7 +207,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     __syncwarp();
 
     const int g = lane >> 2, t = lane & 3;  // fragment row and column pair
-    int step = 0;
+    int cur = 0;  // the ring's buffer of the step
     for (int n = 0; n < npieces; ++n) {
         const Piece p = pieces[warp][n % kPieces];
         // this thread's rows of the item: g and, of 16, g + 8
@@ -207,6 +223,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             qrow[i] = a.Q + (int64_t)(p.tok0 + tok[i]) * a.ldq +
                       (p.head * a.G + row % a.G) * D + 2 * t;
         }
+        auto out_row = [&](int r) {
+            return (int64_t)(p.tok0 + tok[r]) * a.Hq + p.head * a.G + (g + 8 * r) % a.G;
+        };
         uint32_t qf[D / 16][S][4];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
@@ -230,12 +249,25 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         for (int r = 0; r < R; ++r) {
             m[r] = -INFINITY;
             l[r] = 0.0f;
+            if (live[r] && starts_with_prefix(a, p)) {
+                const int64_t row = out_row(r);
+                const float2 f = __ldcg(a.prefix_ml + row);
+                m[r] = f.x;
+                l[r] = t == 0 ? f.y : 0.0f;  // (the row's four threads' sums are added)
+                const float *src = a.prefix_o + row * D + 2 * t;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src + 8 * i));
+                    o[i][2 * r] = v.x;
+                    o[i][2 * r + 1] = v.y;
+                }
+            }
         }
         int key0 = p.key0;
-        for (int it = 0; it < p.ntiles; ++it, ++step, key0 += kKT) {
+        for (int it = 0; it < p.ntiles; ++it, key0 += kKT) {
             asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
             __syncwarp();
-            const uint32_t ks = ring + (step % ST) * C::kStepBytes;
+            const uint32_t ks = ring + cur * C::kStepBytes;
             const uint32_t vs = ks + kKT * D * 2;
             // logits of the rows x 16 keys
             float s[2][2][4];
@@ -268,7 +300,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             bool cut = key0 < first_key;
 #pragma unroll
             for (int r = 0; r < R; ++r) cut = cut || key0 + kKT > limit[r];
-            const bool missing = holes >> (step % ST) & 1;
+            const bool missing = holes >> cur & 1;
             if (__any_sync(0xffffffffu, cut || missing)) {
 #pragma unroll
                 for (int r = 0; r < R; ++r)
@@ -349,6 +381,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             }
             __syncwarp();  // the step's buffer is free
             copy_step();
+            if (++cur == ST) cur = 0;
         }
         __syncwarp();  // the copies' next piece is in shared memory
 #pragma unroll
@@ -406,21 +439,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (!live[r]) continue;
-            const int64_t out = (int64_t)(p.tok0 + tok[r]) * a.Hq + p.head * a.G + (g + 8 * r) % a.G;
-            const RowEnd e = row_end<D>(a, out, m[r], l[r], t == 0);
-            float *dst = row_target(a) + e.at + 2 * t;
-            const float *front = row_front(a);
-            if (front) front += e.at + 2 * t;
+            const int64_t row = out_row(r);
+            const float f = row_factor(a, row, m[r], l[r], t == 0);
+            float *dst = row_target(a) + row * D + 2 * t;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                float2 v = make_float2(o[i][2 * r] * e.own, o[i][2 * r + 1] * e.own);
-                if (front) {
-                    const float2 f = *reinterpret_cast<const float2 *>(front + 8 * i);
-                    v.x += f.x * e.front;
-                    v.y += f.y * e.front;
-                }
-                *reinterpret_cast<float2 *>(dst + 8 * i) = v;
-            }
+            for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<float2 *>(dst + 8 * i) =
+                    make_float2(o[i][2 * r] * f, o[i][2 * r + 1] * f);
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");

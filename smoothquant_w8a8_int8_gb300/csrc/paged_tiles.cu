@@ -146,7 +146,7 @@ struct TileBars {
     Share share;
     float2 stat[kStats][2][kRows];  // a tile's row maxima (log2 units) and half sums
     float half_max[2][2][kRows];    // a tile's row maxima over its halves
-    float qmul[2][kRows];        // what the rows' queries were divided by
+    float qmul[2][kRows];           // what the rows' queries were divided by
 };
 
 __device__ __forceinline__ void fence_async_smem() {
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = B.tmem;
     const int first_key = a.prefix_phase ? 0 : a.prefix_len;
 
-    // registers: 96 a thread at launch; (2 x 104 + 160 + 56 + 48) x 128 in all
+    // registers: 96 a thread at launch; (2 x 104 + 168 + 56 + 48) x 128 in all
     if (warp >= 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == 16 && lane == 0) {
@@ -533,59 +533,63 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (B.stop[it]) break;
             const Piece &p = B.items[it];  // held until the piece is done
             {
-                // 16 rows of the queries, a row (D = 64: two) per step
+                // 16 rows of the queries, a row (D = 64: two) per step: copied as they
+                // are into the place of their parts, then split there.  (Short loops:
+                // this runs once an item, and an instruction that is not in the cache
+                // costs more than it saves; unrolled, with the rows in registers, it
+                // took 7800 cycles.)
                 constexpr int LPR = D / 4;      // lanes per row
                 constexpr int RPS = 32 / LPR;   // rows per step
-                constexpr int STEPS = 8 / RPS;  // steps whose loads are in flight at once
                 const int sub = lane / LPR, c4 = lane % LPR;
-                const float *q0 = a.Q + (int64_t)p.tok0 * a.ldq + p.head * a.G * D + 4 * c4;
-                const int nrows = p.ntok * a.G;
-                bool waited = n == 0;
-#pragma unroll 1
-                for (int i0 = 0; i0 < 16; i0 += 8) {
-                    float4 q[STEPS];
-#pragma unroll
-                    for (int i = 0; i < STEPS; ++i) {
-                        const int qr = 16 * warp + i0 + i * RPS + sub;
-                        const int qt = qr * a.g_inv >> 16;
-                        q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (qr < nrows)
-                            q[i] = *reinterpret_cast<const float4 *>(q0 + (int64_t)qt * a.ldq +
-                                                                     (qr - qt * a.G) * D);
-                    }
-                    // the piece before has no S to be formed any more
-                    if (!waited) {
-                        if (!warp_wait(&B.q_empty, (n - 1) & 1u, abort, a.error)) break;
-                        waited = true;
-                    }
-#pragma unroll
-                    for (int i = 0; i < STEPS; ++i) {
-                        const int qr = 16 * warp + i0 + i * RPS + sub;
-                        float mul = a.sign;
-                        if (!BF) {
-                            float top = fmaxf(fmaxf(fabsf(q[i].x), fabsf(q[i].y)),
-                                              fmaxf(fabsf(q[i].z), fabsf(q[i].w)));
-#pragma unroll
-                            for (int o = LPR / 2; o > 0; o >>= 1)
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                            const int sh = shift_of((int)(__float_as_uint(top) >> 23) - 127);
-                            mul *= pow2(-sh);
-                            if (c4 == 0) B.qmul[n & 1][qr] = pow2(sh);
-                        }
-                        uint32_t x[NP], y[NP];
-                        split16<BF, NP>(q[i].x * mul, q[i].y * mul, x);
-                        split16<BF, NP>(q[i].z * mul, q[i].w * mul, y);
-                        const uint32_t at = qbase + (c4 >> 4) * C::kSlab + qr * 128 +
-                                            ((((c4 & 15) >> 1) ^ (qr & 7)) << 4) + (c4 & 1) * 8;
-#pragma unroll
-                        for (int part = 0; part < NP; ++part)
-                            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(
-                                             at + part * C::kQPart),
-                                         "r"(x[part]), "r"(y[part])
-                                         : "memory");
-                    }
+                const int part4 = c4 / (D / 8), in4 = c4 % (D / 8);
+                // lane l (of 16) knows where row l is
+                const int lr = 16 * warp + (lane & 15), lt = lr * a.g_inv >> 16;
+                int64_t place = -1;
+                if (lt < p.ntok)
+                    place = (int64_t)(p.tok0 + lt) * a.ldq + (p.head * a.G + (lr - lt * a.G)) * D;
+                // the piece before has no S to be formed any more
+                if (n > 0 && !warp_wait(&B.q_empty, (n - 1) & 1u, abort, a.error)) break;
+                const uint32_t rows = qbase + (16 * warp + sub) * 128;
+                const uint32_t raw = rows + part4 * C::kQPart + (in4 >> 3) * C::kSlab;
+                const uint32_t to = rows + (c4 >> 4) * C::kSlab + (c4 & 1) * 8;
+#pragma unroll 2
+                for (int i = 0; i < 16; i += RPS) {
+                    const int64_t at = __shfl_sync(0xffffffffu, place, i + sub);
+                    copy16(raw + i * 128 + (((in4 & 7) ^ ((i + sub) & 7)) << 4),
+                           a.Q + (at < 0 ? 0 : at + 4 * c4), at >= 0);
                 }
-                if (!waited) break;
+                asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 2
+                for (int i = 0; i < 16; i += RPS) {
+                    float4 q;
+                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
+                                 : "r"(raw + i * 128 + (((in4 & 7) ^ ((i + sub) & 7)) << 4))
+                                 : "memory");
+                    float mul = a.sign;
+                    if (!BF) {
+                        // (the rows of a step have one factor)
+                        const float top = fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)),
+                                                fmaxf(fabsf(q.z), fabsf(q.w)));
+                        const unsigned e =
+                            __reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23;
+                        const int sh = shift_of((int)e - 127);
+                        mul *= pow2(-sh);
+                        if (c4 == 0) B.qmul[n & 1][16 * warp + i + sub] = pow2(sh);
+                    }
+                    uint32_t x[NP], y[NP];
+                    split16<BF, NP>(q.x * mul, q.y * mul, x);
+                    split16<BF, NP>(q.z * mul, q.w * mul, y);
+                    __syncwarp();  // every lane has its numbers of these rows
+                    const uint32_t at =
+                        to + i * 128 + ((((c4 & 15) >> 1) ^ ((i + sub) & 7)) << 4);
+#pragma unroll
+                    for (int part = 0; part < NP; ++part)
+                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at +
+                                                                              part * C::kQPart),
+                                     "r"(x[part]), "r"(y[part])
+                                     : "memory");
+                }
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) bar_arrive(&B.q_full);
@@ -678,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) bar_arrive(&B.item_empty[it]);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         // -------------------------------------------------------- the output
         const int w = warp & 3;
         const int row = 32 * w + lane;
@@ -699,6 +703,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.0f;
 #pragma unroll
             for (int i = 0; i < D / 2; ++i) o2[i] = 0;
+            const int tok = row * a.g_inv >> 16;
+            const bool live = tok < p.ntok;
+            const int64_t out =
+                live ? (int64_t)(p.tok0 + tok) * a.Hq + p.head * a.G + (row - tok * a.G) : -1;
+            if (live && starts_with_prefix(a, p)) {
+                const float2 f = __ldcg(a.prefix_ml + out);
+                m = f.x;
+                l = f.y;
+                const ulonglong2 *src =
+                    reinterpret_cast<const ulonglong2 *>(a.prefix_o + out * D);
+#pragma unroll
+                for (int i = 0; i < D / 4; ++i) {
+                    const ulonglong2 v = __ldcg(src + i);
+                    o2[2 * i] = v.x;
+                    o2[2 * i + 1] = v.y;
+                }
+            }
             bool ok = true;
             for (int k = 0; k < p.ntiles; ++k, ++t) {
                 const uint32_t pb = t % C::kPVs;
@@ -730,42 +751,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) bar_arrive(&B.pv_empty[pb]);
             }
             if (!ok) break;
-            const int tok = row * a.g_inv >> 16;
-            const bool live = tok < p.ntok;
-            const int64_t out =
-                live ? (int64_t)(p.tok0 + tok) * a.Hq + p.head * a.G + (row - tok * a.G) : -1;
             // a row per thread: 32 lines per store, but code that is executed once
             // an item has to be short (an instruction that is not in the cache
             // costs about 20 cycles; rows turned in shared memory measured three
             // times as long)
             const bool whole = p.npieces == 1;
             const int64_t part = (int64_t)(2 * blockIdx.x + p.slot) * kRows + row;
-            RowEnd e = {1.0f, 0.0f, part * D};
-            float *dst = a.part_o;
-            const float *front = nullptr;
+            float *dst = a.part_o + part * D;
+            float factor = 1.0f;
             if (whole) {
-                e = row_end<D>(a, out < 0 ? 0 : out, m, l, live);
-                dst = row_target(a);
-                front = row_front(a);
+                factor = row_factor(a, out < 0 ? 0 : out, m, l, live);
+                dst = row_target(a) + out * D;
             } else {
                 __stcg(a.part_ml + part, make_float2(m, l));
             }
             if (!whole || live) {
-                dst += e.at;
-                if (front) front += e.at;
-                const unsigned long long own2 = pk(e.own, e.own);
+                const unsigned long long f2 = pk(factor, factor);
 #pragma unroll
                 for (int i = 0; i < D / 4; ++i) {
                     float4 v;
-                    upk(mul2(o2[2 * i], own2), v.x, v.y);
-                    upk(mul2(o2[2 * i + 1], own2), v.z, v.w);
-                    if (front) {
-                        const float4 f = *reinterpret_cast<const float4 *>(front + 4 * i);
-                        v.x += f.x * e.front;
-                        v.y += f.y * e.front;
-                        v.z += f.z * e.front;
-                        v.w += f.w * e.front;
-                    }
+                    upk(mul2(o2[2 * i], f2), v.x, v.y);
+                    upk(mul2(o2[2 * i + 1], f2), v.z, v.w);
                     __stcg(reinterpret_cast<float4 *>(dst) + i, v);
                 }
             }
@@ -793,9 +799,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float2 e = __ldcg(a.part_ml + from(c) + lane);
                         l += e.y * max_factor(e.x, m);
                     }
-                    e = row_end<D>(a, out < 0 ? 0 : out, m, l, live);
+                    factor = row_factor(a, out < 0 ? 0 : out, m, l, live);
                     dst = row_target(a);
-                    front = row_front(a);
 #pragma unroll 1
                     for (int q = 0; q < D / 32; ++q) {
                         // 32 columns of the warp's rows, whole lines
@@ -825,20 +830,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 8; ++i) {
                             const int rr = 4 * i + (lane >> 3);
                             const int64_t to_row = __shfl_sync(0xffffffffu, out, rr);
-                            const float own = __shfl_sync(0xffffffffu, e.own, rr);
-                            const float part_f = __shfl_sync(0xffffffffu, e.front, rr);
-                            if (to_row < 0) continue;
-                            float4 v = make_float4(sum[i].x * own, sum[i].y * own,
-                                                   sum[i].z * own, sum[i].w * own);
-                            if (front) {
-                                const float4 f = *reinterpret_cast<const float4 *>(
-                                    front + to_row * D + col);
-                                v.x += f.x * part_f;
-                                v.y += f.y * part_f;
-                                v.z += f.z * part_f;
-                                v.w += f.w * part_f;
-                            }
-                            *reinterpret_cast<float4 *>(dst + to_row * D + col) = v;
+                            const float f = __shfl_sync(0xffffffffu, factor, rr);
+                            if (to_row >= 0)
+                                *reinterpret_cast<float4 *>(dst + to_row * D + col) =
+                                    make_float4(sum[i].x * f, sum[i].y * f, sum[i].z * f,
+                                                sum[i].w * f);
                         }
                     }
                 }
