@@ -131,7 +131,7 @@ __device__ __forceinline__ int row_limit(const PagedArgs &a, const Piece &p, int
 // the prefix's maximum, sum and output (so that its loads are on their way while
 // the item's first keys are).  row = token * Hq + query head.
 __device__ __forceinline__ bool starts_with_prefix(const PagedArgs &a, const Piece &p) {
-    return !a.prefix_phase && a.prefix_len > 0 && p.key0 == a.kstart;
+    return !a.prefix_phase && a.prefix_len > 0 && a.front_tiles == 0 && p.key0 == a.kstart;
 }
 // A row's last step, from its maximum m (log2 units) and sum l: the factor of its
 // output on the way to the prefix's buffer (with m and l, stored by the caller

@@ -33,6 +33,29 @@ sq_status error_word(int device, unsigned **out) {
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
+// Whether a row tile's work fits the kernel for few rows (per key/value head).
+bool few_rows(int64_t tokens, int G) { return std::max<int64_t>(1, tokens) * G <= 16; }
+
+// Whether the shared prefix is read in front of every item's own keys instead of
+// once for all rows, in a launch of its own.  What the launch costs by itself is
+// the start and the end of its items, the prefix's state written and read back,
+// and the wait for it; what it saves is the prefix's key tiles for the row tiles
+// that it has fewer of, one for every sequence at most.  Measured (heads 32 / 8
+// of 128, bf16, own keys up to 512, one token a sequence; separate against in
+// front): 16 sequences behind 1000 positions 57 and 27 us, 64: 66 and 53; 64
+// behind 3000: 74 and 115, 16 behind 8000: 90 and 82.  The times meet at 40 to 50
+// key tiles of 128 per SM, and at 20 to 27 with many rows (fp16, 5 to 8 tokens,
+// 24 sequences behind 1000: 88 and 72 us, behind 3000: 92 and 102).  Where the
+// sequences fill two row tiles each and more, the prefix in front costs less than
+// its state's way through memory whatever its length (bf16, 64 sequences of 1 to
+// 257 tokens behind 1000 positions: 944 and 782 us, behind 8000: 2838 and 2792).
+bool prefix_in_front(const PagedArgs &a, int64_t max_q, int sms) {
+    const bool few = few_rows(max_q, a.G);
+    if (!few && (int64_t)a.T * a.G >= 256 * (int64_t)a.B) return true;
+    const int64_t tiles = (int64_t)std::min(a.B, a.T) * a.Hkv * ((a.prefix_len + 127) / 128);
+    return tiles <= (few ? 40 : 20) * (int64_t)sms;
+}
+
 }  // namespace
 
 // counters | partial maxima and sums | partial outputs | the prefix's maxima
@@ -92,19 +115,23 @@ sq_status launch_paged_attention(const PagedCall &c, cudaStream_t st) {
     a.scale = std::max(fabsf(c.scale) * 1.4426950408889634f, 1e-30f);
     a.sign = c.scale < 0.0f ? -1.0f : 1.0f;
     const bool bf16 = c.cache_type == SQ_CACHE_BF16;
-    for (int phase = c.prefix_len > 0 ? 1 : 0; phase >= 0; --phase) {
+    const bool front = c.prefix_len > 0 && prefix_in_front(a, std::min(c.max_q, c.T), di.sms);
+    for (int phase = c.prefix_len > 0 && !front ? 1 : 0; phase >= 0; --phase) {
         a.prefix_phase = phase;
-        const int64_t most = std::max<int64_t>(1, phase ? c.T : std::min(c.max_q, c.T)) * a.G;
+        const int64_t most = phase ? c.T : std::min(c.max_q, c.T);
         // up to 16 rows per key/value head: the warp-level products; more: tensor
         // memory's
-        const bool few = most <= 16;
-        const int r = few ? (most <= 8 ? 8 : 16) : 128, kt = few ? 16 : 128;
+        const bool few = few_rows(most, a.G);
+        const int r = few ? (std::max<int64_t>(1, most) * a.G <= 8 ? 8 : 16) : 128;
+        const int kt = few ? 16 : 128;
         a.tpt = r / a.G;
         a.kstart = phase ? 0 : a.prefix_len / kt * kt;
+        a.front_tiles = front ? (a.prefix_len + kt - 1) / kt : 0;
+        a.front_shift = front ? a.front_tiles * kt - a.kstart : 0;
         // the longest line that the sizes allow: every sequence as long as its row
         // of the table, and a row tile of its own begun
         const int64_t tiles = (c.T + a.tpt - 1) / a.tpt + (phase ? 0 : c.B);
-        const int64_t keys = (phase ? c.prefix_len : c.max_pages * c.page_size) / kt + 16;
+        const int64_t keys = ((phase ? 0 : c.max_pages * c.page_size) + c.prefix_len) / kt + 16;
         if (tiles * c.Hkv > ((int64_t)1 << 31) / keys) return SQ_ERR_UNSUPPORTED;
         rc = few ? launch_paged_rows(a, c.k_cache, c.v_cache, (int)c.D, bf16, r, di.sms, st)
                  : launch_paged_tiles(a, c.k_cache, c.v_cache, (int)c.D, bf16, di.sms, st);

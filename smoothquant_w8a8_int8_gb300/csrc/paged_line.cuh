@@ -38,6 +38,9 @@ struct PagedArgs {
     int num_pages, page_shift;
     int prefix_len;
     int kstart;          // first key of the suffix's first key tile
+    int front_tiles;     // key tiles of the prefix in front of each item's own keys: 0
+                         // where the prefix is a launch of its own
+    int front_shift;     // front_tiles KT - kstart: 0, or KT for a prefix that ends in a tile
     int cap;             // keys a row of the page table can name
     float scale;         // |scale| log2 e; the sign is folded into the queries
     float sign;
@@ -82,7 +85,8 @@ SQ_HD int tile_keys(const PagedArgs &a, const Seq &s, int j) {
 template <int KT>
 SQ_HD int key_tiles(const PagedArgs &a, const Seq &s, int j) {
     const int n = tile_keys(a, s, j) - a.kstart;
-    return n <= KT ? 1 : (n + KT - 1) / KT;  // at least one: its rows are written
+    // at least one: its rows are written
+    return a.front_tiles + (n <= KT ? 1 : (n + KT - 1) / KT);
 }
 // sum of floor((p i + q) / m) over i < n; m > 0, and m n + p + q < 2^32 (T and a
 // row of the page table are limited to that).  The sum counts lattice points
@@ -114,6 +118,7 @@ SQ_HD int pairs_before(const PagedArgs &a, const Seq &s, int J) {
     const int whole = at_most(J, tiles - 1);  // the last row tile may hold fewer tokens
     int sum = J * PAD;
     if (whole > 0) {
+        sum += whole * a.front_tiles;
         const int base = s.kv - s.qlen - a.kstart;
         // row tiles whose keys fit one key tile: base + (j + 1) tpt <= KT
         const int ones = at_most(KT < base ? 0 : (int)((uint32_t)(KT - base) / a.tpt), whole);
@@ -167,12 +172,31 @@ struct Piece {
     int tok0, ntok;     // tokens of the row tile
     int head;           // key/value head
     int pos0;           // position of token tok0 (suffix)
-    int key0, ntiles;   // first key and key tiles of the piece
+    int key0, ntiles;   // first key and key tiles of the piece (see key_range)
     int keys;           // one past the last key any row attends to
     int seq;
     int first, npieces;  // first worker of the item; npieces = 1: the whole item
     int slot;           // the worker's partial slot
 };
+
+// An item's key tiles are numbered on: those of the prefix in front of the item's
+// own, whose numbers end at kstart, and then its own from there.  The tile in
+// which a prefix ends comes twice, once for the prefix and once for the
+// sequence's own keys.
+struct KeyRange {
+    int key;      // the first key of the tile
+    int lo, hi;   // keys of it that a row with `limit` keys sees: from lo, before hi
+    bool front;   // the prefix's pages
+};
+SQ_HD KeyRange key_range(const PagedArgs &a, int key0, int limit) {
+    KeyRange r;
+    r.front = key0 < a.kstart;
+    r.key = r.front ? key0 + a.front_shift : key0;
+    r.lo = r.front || a.prefix_phase ? 0 : a.prefix_len;
+    r.hi = r.front ? at_most(limit, a.prefix_len) : limit;
+    r.front = r.front || a.prefix_phase;
+    return r;
+}
 
 // Walks the pieces of a worker's share.
 template <int KT, int PAD>
@@ -234,7 +258,7 @@ struct Walk {
         p.ntok = at_most(a.tpt, s.qlen - j * a.tpt);
         p.head = h;
         p.pos0 = s.kv - s.qlen + j * a.tpt;
-        p.key0 = a.kstart + k * KT;
+        p.key0 = a.kstart + (k - a.front_tiles) * KT;
         p.ntiles = take;
         p.keys = tile_keys(a, s, j);
         p.seq = b;

@@ -131,7 +131,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const Share &share = shares[warp];
     const int worker = warp * gridDim.x + blockIdx.x;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * ST * C::kStepBytes;
-    const int first_key = a.prefix_phase ? 0 : a.prefix_len;
 
     // ---- the copies: one step of the share per call, or nothing at its end
     Walk<kKT, kPad> walk;
@@ -141,7 +140,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     int64_t head_row = 0;  // the piece's head, in cache rows of a page
     int keys = 0;
     unsigned holes = 0;    // bit i: the page of the step in buffer i is missing
-    const int *pages = nullptr;
+    const int *table = nullptr;
     auto copy_step = [&]() {
         if (left == 0) {
             Piece p;
@@ -152,24 +151,26 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 key = p.key0;
                 keys = p.keys;
                 head_row = (int64_t)p.head << a.page_shift;
-                pages = a.prefix_phase ? a.prefix_pages
-                                       : a.block_table + (int64_t)p.seq * a.max_pages;
+                table = a.block_table + (int64_t)p.seq * a.max_pages;
                 held = -1;
             }
         }
         if (left > 0) {
             // lane i holds the page-table entry 32 held + i
-            const int idx = key >> a.page_shift;
-            if (idx >> 5 != held) {
+            const KeyRange kr = key_range(a, key, keys);
+            const int idx = kr.key >> a.page_shift;
+            if (idx >> 5 != held || key == a.kstart) {
                 held = idx >> 5;
                 const int at = (held << 5) + lane;
-                entry = (int64_t)at << a.page_shift < keys ? __ldg(pages + at) : -1;
+                entry = (int64_t)at << a.page_shift < kr.hi
+                            ? __ldg((kr.front ? a.prefix_pages : table) + at)
+                            : -1;
             }
             const int e = __shfl_sync(0xffffffffu, entry, idx & 31);
             const bool there = e >= 0 && e < a.num_pages;
             holes = (holes & ~(1u << buf)) | (there ? 0u : 1u << buf);
             const int64_t row0 = (there ? (((int64_t)e * a.Hkv) << a.page_shift) + head_row : 0) +
-                                 (key & ((1 << a.page_shift) - 1));
+                                 (kr.key & ((1 << a.page_shift) - 1));
             // lane: chunk lane % (D / 8) of row lane / (D / 8) of every kStride rows; the
             // step's 16 rows are contiguous in the cache
             constexpr int kLanes = D / 8, kCopies = kKT * kLanes / 32, kStride = 32 / kLanes;
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             const uint32_t dst = ring + buf * C::kStepBytes + r0 * D * 2;
             const int64_t from = row0 * D + lane * 8;
             const uint16_t *ks = k_cache + from, *vs = v_cache + from;
-            if (there && key + kKT <= keys && key >= first_key) {
+            if (there && kr.key + kKT <= kr.hi && kr.key >= kr.lo) {
 #pragma unroll
                 for (int j = 0; j < kCopies; ++j) {
                     const uint32_t d =
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll 1
                 for (int j = 0; j < kCopies; ++j) {
                     const int r = r0 + j * kStride;
-                    const bool in = there && key + r < keys && key + r >= first_key;
+                    const bool in = there && kr.key + r < kr.hi && kr.key + r >= kr.lo;
                     const uint32_t d =
                         dst + j * 512 + (((ch ^ r0) ^ (j * kStride & 7)) << 4);
                     copy16(d, in ? ks + j * 256 : k_cache, in);
@@ -297,17 +298,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             }
             // keys that are masked: behind the row's own, in front of the
             // suffix, or of a page that is missing
-            bool cut = key0 < first_key;
-#pragma unroll
-            for (int r = 0; r < R; ++r) cut = cut || key0 + kKT > limit[r];
+            const KeyRange kr = key_range(a, key0, limit[0]);
+            const int hi1 = R == 1 ? 0 : key_range(a, key0, limit[R - 1]).hi;
+            bool cut = kr.key < kr.lo || kr.key + kKT > kr.hi ||
+                       (R > 1 && kr.key + kKT > hi1);
             const bool missing = holes >> cur & 1;
             if (__any_sync(0xffffffffu, cut || missing)) {
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int k = key0 + 8 * (i >> 1) + 2 * t + (i & 1);
-                        if (missing || k >= limit[r] || k < first_key) x[r][i] = -INFINITY;
+                        const int k = kr.key + 8 * (i >> 1) + 2 * t + (i & 1);
+                        if (missing || k >= (r ? hi1 : kr.hi) || k < kr.lo) x[r][i] = -INFINITY;
                     }
             }
             float grow[R];

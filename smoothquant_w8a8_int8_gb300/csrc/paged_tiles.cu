@@ -292,7 +292,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();  // every global-memory access below follows the previous kernel
     find_shares<kKT, C::kPad, kThreads, 1>(a, kMinTiles, &B.share);
     const uint32_t tmem = B.tmem;
-    const int first_key = a.prefix_phase ? 0 : a.prefix_len;
 
     // registers: 96 a thread at launch; (2 x 104 + 168 + 56 + 48) x 128 in all
     if (warp >= 16) {
@@ -464,11 +463,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         Piece p = {};
         bool more = true;
         int entry = -1;
-        // the entry of the page of keys key .. key + 15; -1 where none is wanted
-        auto page_of = [&](int key) {
-            const int *pages = a.prefix_phase ? a.prefix_pages
-                                              : a.block_table + (int64_t)p.seq * a.max_pages;
-            return key < p.keys && key + 16 > first_key ? __ldg(pages + (key >> a.page_shift)) : -1;
+        // lane l: the entry of the page of keys 16 (l % 8) .. of a tile; -1 where none is
+        // wanted
+        auto page_of = [&](const KeyRange &r) {
+            const int *pages = r.front ? a.prefix_pages
+                                       : a.block_table + (int64_t)p.seq * a.max_pages;
+            const int key = r.key + 16 * (lane & 7);
+            return key < r.hi && key + 16 > r.lo ? __ldg(pages + (key >> a.page_shift)) : -1;
         };
         for (uint32_t n = 0; ok && more;) {
             if (left == 0) {
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p = B.items[it];
                     left = p.ntiles;
                     key0 = p.key0;
-                    entry = page_of(key0 + 16 * (lane & 7));
+                    entry = page_of(key_range(a, key0, p.keys));
                     __syncwarp();
                     if (lane == 0) bar_arrive(&B.item_empty[it]);
                     ++n;
@@ -490,12 +491,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             int64_t place = 0;
             unsigned miss = 0;
+            int lo = 0, hi = 0;
             if (more) {
-                // lane l: the page of keys 16 (l % 8) .. of the tile; the next tile's
-                // entry is on its way meanwhile
+                // the next tile's entry is on its way meanwhile
                 const int e = entry;
-                const int key = key0 + 16 * (lane & 7);
-                entry = left > 1 ? page_of(key + kKT) : -1;
+                const KeyRange r = key_range(a, key0, p.keys);
+                const int key = r.key + 16 * (lane & 7);
+                lo = r.lo - r.key;
+                hi = r.hi - r.key;
+                entry = left > 1 ? page_of(key_range(a, key0 + kKT, p.keys)) : -1;
                 const bool there = e >= 0 && e < a.num_pages;
                 miss = ~__ballot_sync(0xffffffffu, there) & 0xffu;
                 if (there)
@@ -507,11 +511,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int kv = more ? 0 : 1; kv < (tile > 0 ? 2 : 1) && ok; ++kv)
                 copy_slot(kv ? v_cache : k_cache, kv ? v_place : place, kv ? v_miss : miss,
-                          kv ? v_lo : first_key - key0, kv ? v_hi : p.keys - key0);
+                          kv ? v_lo : lo, kv ? v_hi : hi);
             v_place = place;
             v_miss = miss;
-            v_lo = first_key - key0;
-            v_hi = p.keys - key0;
+            v_lo = lo;
+            v_hi = hi;
             if (more) {
                 ++tile;
                 --left;
@@ -596,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int tok = r * a.g_inv >> 16;
             const int limit = tok < p.ntok ? row_limit(a, p, tok) : p.keys;
-            int key0 = p.key0 + 64 * g;  // this warp's 64 keys
+            int key0 = p.key0;
             bool ok = true;
             for (int k = 0; k < p.ntiles; ++k, ++t, key0 += kKT) {
                 const uint32_t area = lanes + (t & 1) * C::kArea;
@@ -611,13 +615,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_wait();
                 const unsigned miss = B.miss[t % kMiss] >> (4 * g);
                 const float c = BF ? a.scale : a.scale * B.qmul[n & 1][r];
-                if (__any_sync(0xffffffffu,
-                               key0 + 64 > limit || key0 < first_key || (miss & 15u) != 0)) {
+                const KeyRange kr = key_range(a, key0, limit);
+                const int at = kr.key + 64 * g;  // this warp's 64 keys
+                if (__any_sync(0xffffffffu, at + 64 > kr.hi || at < kr.lo || (miss & 15u) != 0)) {
                     // keys behind the row's own, in front of the suffix or of a
                     // missing page: bit i of `seen` is clear
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const int hi = limit - key0 - 32 * q, lo = first_key - key0 - 32 * q;
+                        const int hi = kr.hi - at - 32 * q, lo = kr.lo - at - 32 * q;
                         unsigned seen = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1;
                         if (lo > 0) seen = lo >= 32 ? 0u : seen & (~0u << lo);
                         if (miss >> (2 * q) & 1) seen &= 0xffff0000u;

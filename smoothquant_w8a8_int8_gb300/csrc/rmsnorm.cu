@@ -271,8 +271,8 @@ sq_status launch_rmsnorm_quant(const float *H, const float *residual, const floa
                 return SQ_ERR_CUDA;
             o = true;
         }
-        // 64 registers a thread: 1024 threads per SM; twice what fits at once
-        grid = std::min<int64_t>(tiles, 2 * (int64_t)di.sms * std::max(1, 1024 / nt));
+        // 64 registers a thread: 1024 threads per SM; as many blocks as fit at once
+        grid = std::min<int64_t>(tiles, (int64_t)di.sms * std::max(1, 1024 / nt));
     }
     return launch_pdl(kern, dim3((unsigned)grid), dim3((unsigned)nt), (size_t)smem, st, 1, H,
                       residual, gamma, eps, s, rows, K4, tpr, R, Y, q, scale, op, l1,

@@ -39,7 +39,20 @@ static void check(PagedArgs a, int grid, int min_pairs) {
                 last = a.prefix_phase ? a.prefix_len : s.kv - s.qlen + i + 1;
             int n = 1;
             while (a.kstart + n * KT < last) ++n;
+            n += a.front_tiles;
             CHECK(n == key_tiles<KT>(a, s, j));
+            // its tiles hold every key that it attends to (here) once, in order
+            int key = a.prefix_phase || a.front_tiles ? 0 : a.prefix_len;
+            for (int k = 0; k < n; ++k) {
+                const KeyRange r = key_range(a, a.kstart + (k - a.front_tiles) * KT, last);
+                const int lo = std::max(r.lo, r.key), hi = std::min(r.hi, r.key + KT);
+                CHECK(r.key >= 0 && r.key % KT == 0);
+                CHECK(r.front == (a.prefix_phase || lo < a.prefix_len));
+                if (lo >= hi) continue;
+                CHECK(lo == key);
+                key = hi;
+            }
+            CHECK(last <= key);
             for (int h = 0; h < a.Hkv; ++h)
                 for (int k = 0; k < n + (a.prefix_phase ? 0 : PAD); ++k)  // the last without work
                     line.emplace_back(b, j, h, k < n ? k : -1);
@@ -78,7 +91,8 @@ static void check(PagedArgs a, int grid, int min_pairs) {
             const Seq s = load_seq(a, b);
             CHECK(p.seq == b && p.head == h && p.ntiles >= 1);
             CHECK(p.tok0 == s.q0 + j * a.tpt && p.ntok == std::min(a.tpt, s.qlen - j * a.tpt));
-            CHECK(p.key0 == a.kstart + k * KT && p.keys == tile_keys(a, s, j));
+            CHECK(p.key0 == a.kstart + (k - a.front_tiles) * KT);
+            CHECK(p.keys == tile_keys(a, s, j));
             if (!a.prefix_phase) CHECK(p.pos0 == s.kv - s.qlen + j * a.tpt);
             for (int i = 0; i < p.ntiles; ++i)
                 CHECK(at + i < total && line[at + i] == std::make_tuple(b, j, h, k + i));
@@ -145,6 +159,9 @@ int main() {
         for (int phase = a.prefix_len ? 1 : 0; phase >= 0; --phase) {
             a.prefix_phase = phase;
             a.kstart = phase ? 0 : a.prefix_len / KT * KT;
+            // the prefix in front of every item's own keys, or not
+            a.front_tiles = phase || trial % 5 < 2 ? 0 : (a.prefix_len + KT - 1) / KT;
+            a.front_shift = a.front_tiles ? a.front_tiles * KT - a.kstart : 0;
             const int grid = pick(1, 152), least = pick(1, 4);
             if (KT == 16) check<16, 2>(a, grid, least);
             else trial % 4 == 1 ? check<128, 4>(a, grid, least) : check<128, 6>(a, grid, least);

@@ -90,6 +90,57 @@ def test_prefix_longer_than_a_sequence(sq):
     verify(sq, Batch([1, 3, 2, 1], [50, 2, 0, 200], 8, 2, 128, 32, BF, prefix=150, seed=3).cuda())
 
 
+def many_behind(prefix, tiles_per_sm, Hkv, tail, **kw):
+    """A batch of single tokens (and `tail`) so large that its shared prefix,
+    read for every sequence, would be more than tiles_per_sm key tiles of 128
+    for each multiprocessor: it is attended to in a launch of its own then."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n = tiles_per_sm * sms // (Hkv * -(-prefix // 128)) + 1
+    q = [1] * n + list(tail)
+    kv = [prefix + (i * 7) % 40 for i in range(len(q))]
+    kv[1], kv[2] = prefix // 2, 0                     # ends inside the prefix; has no key
+    return Batch(q, [max(a, b) if b > 1 else a for a, b in zip(kv, q)], kw.pop("Hq"), Hkv,
+                 kw.pop("D"), kw.pop("page"), kw.pop("dtype"), prefix=prefix, front=1, behind=2,
+                 **kw)
+
+
+@pytest.mark.parametrize("prefix,tiles_per_sm,Hkv,tail,kw", [
+    (100, 40, 8, [0, 2, 1], dict(Hq=8, D=64, page=16, dtype=BF)),
+    (128, 40, 8, [], dict(Hq=16, D=128, page=64, dtype=FP)),
+    (70, 20, 8, [17, 0, 40], dict(Hq=8, D=128, page=32, dtype=BF)),
+    (130, 20, 8, [33, 1], dict(Hq=8, D=64, page=256, dtype=FP)),
+    (60000, 40, 4, [], dict(Hq=4, D=64, page=256, dtype=BF)),    # few rows behind a long prefix
+    (31000, 40, 2, [1], dict(Hq=2, D=128, page=16, dtype=FP)),
+])
+def test_prefix_in_a_launch_of_its_own(sq, prefix, tiles_per_sm, Hkv, tail, kw):
+    t = many_behind(prefix, tiles_per_sm, Hkv, tail, seed=prefix, **kw).cuda()
+    verify(sq, t)
+    ws = sq.empty_workspace(sq.paged_attention_workspace_bytes(t.T, t.Hq, t.Hkv, t.D, t.prefix))
+    first = call(sq, t, workspace=ws)
+    out = torch.zeros_like(first)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(sq, t, workspace=ws, out=out)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, first)
+        assert torch.equal(call(sq, t, workspace=ws), first)
+    assert sq.device_status() == sq.SQ_OK
+
+
+@pytest.mark.parametrize("prefix", [1, 127, 128, 129, 300])
+@pytest.mark.parametrize("q,kv", [([1, 3, 1], [40, 2, 500]), ([130, 1, 260], [0, 0, 30])])
+@pytest.mark.parametrize("D,dtype,page", [(128, BF, 256), (64, FP, 16)])
+def test_prefix_in_front_of_own_keys(sq, prefix, q, kv, D, dtype, page):
+    """Few sequences, or long ones: the prefix's key tiles stand in front of each
+    item's own; the tile in which it ends is read from both page lists."""
+    kv = [prefix + max(a, b) for a, b in zip(q, kv)]
+    kv[1] = min(kv[1], prefix) // 2 + 1                # ends inside the prefix
+    verify(sq, Batch(q, kv, 8, 4, D, page, dtype, prefix=prefix, seed=prefix + D,
+                     behind=1).cuda())
+
+
 def test_many_sequences(sq):
     q = [1 + (i % 3 == 0) for i in range(300)]
     kv = [(37 * i) % 200 for i in range(300)]
