@@ -10,7 +10,7 @@ namespace {
 
 __device__ unsigned int g_paged_error;
 
-constexpr int64_t kCounterBytes = 16384;
+constexpr int64_t kCounterBytes = 2 * kMaxWorkers * 4;
 constexpr int64_t kPieceRows = 128;  // rows of a partial result, the largest kernel's
 
 // Device address of the error word, looked up on a device's first call.
@@ -76,7 +76,7 @@ sq_status launch_paged_attention(const PagedCall &c, cudaStream_t st) {
     DeviceInfo di;
     sq_status rc = device_info(&di);
     if (rc != SQ_OK) return rc;
-    if (di.sms * 8 * 4 > kCounterBytes) return SQ_ERR_UNSUPPORTED;
+    if (di.sms * 8 > kMaxWorkers) return SQ_ERR_UNSUPPORTED;
     PagedArgs a = {};
     if ((rc = error_word(di.device, &a.error)) != SQ_OK) return rc;
     a.Q = c.Q;

@@ -36,7 +36,13 @@ namespace {
 constexpr int kKT = 16;       // keys per step
 constexpr int kWarps = 8;
 constexpr int kPad = 2;       // an item's start and end, in steps
-constexpr int kMinSteps = 4;  // steps of a worker's share at least
+// Steps of a worker's share at least: 4, 6 and 10 measured 15, 17 and 19 us (one
+// token, 300 or 600 keys)
+constexpr int kMinSteps = 4;
+// Pieces of an item that are joined in one go (0.2 us each): 8, 16 and 32 measured
+// 27, 27 and 31 us (8 tokens, 2000 keys); all in one go took 298 instead of 40 us
+// for one key/value head's 100,000 keys
+constexpr int kJoin = 16;
 constexpr int kPieces = 8;    // more than the steps that the copies are ahead
 
 template <int D>
@@ -392,51 +398,70 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
         }
         if (p.npieces > 1) {
-            // this worker's part of the item, then whoever is last joins them all
+            // this worker's part of the item; whoever is last of a group, and then of
+            // the groups, joins them all
+            auto part_row = [&](int c) {  // piece c of the item
+                return (int64_t)(2 * (p.first + c) + (c == 0)) * ROWS + g;
+            };
+            auto put_part = [&](int64_t at) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int64_t base = (int64_t)(2 * worker + p.slot) * ROWS + g + 8 * r;
-                float *d = a.part_o + base * D + 2 * t;
+                for (int r = 0; r < R; ++r) {
+                    float *d = a.part_o + (at + 8 * r) * D + 2 * t;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                    __stcg(reinterpret_cast<float2 *>(d + 8 * i),
-                           make_float2(o[i][2 * r], o[i][2 * r + 1]));
-                if (t == 0) __stcg(a.part_ml + base, make_float2(m[r], l[r]));
-            }
-            __threadfence();
-            __syncwarp();
-            unsigned last = 0;
-            if (lane == 0) {
-                unsigned *count = a.counters + p.first;
-                last = atomicAdd(count, 1u) == (unsigned)p.npieces - 1;
-                if (last) *count = 0;  // as the next launch wants it
-            }
-            if (!__shfl_sync(0xffffffffu, last, 0)) continue;
-            __threadfence();
+                    for (int i = 0; i < D / 8; ++i)
+                        __stcg(reinterpret_cast<float2 *>(d + 8 * i),
+                               make_float2(o[i][2 * r], o[i][2 * r + 1]));
+                    if (t == 0) __stcg(a.part_ml + at + 8 * r, make_float2(m[r], l[r]));
+                }
+            };
+            const int width = join_width(p.npieces, kJoin);
+            Join join = join_of(p, worker - p.first, width);
+            bool joined = true;
+            int64_t at = part_row(worker - p.first);
+            for (;;) {
+                put_part(at);
+                __threadfence();
+                __syncwarp();
+                unsigned last = 0;
+                if (lane == 0) {
+                    last = atomicAdd(a.counters + join.counter, 1u) == (unsigned)join.n - 1;
+                    if (last) a.counters[join.counter] = 0;  // as the next launch wants it
+                }
+                if (!__shfl_sync(0xffffffffu, last, 0)) {
+                    joined = false;
+                    break;
+                }
+                __threadfence();
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                m[r] = -INFINITY;
-                l[r] = 0.0f;
+                for (int r = 0; r < R; ++r) {
+                    m[r] = -INFINITY;
+                    l[r] = 0.0f;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) o[i][2 * r] = o[i][2 * r + 1] = 0.0f;
+                    for (int i = 0; i < D / 8; ++i) o[i][2 * r] = o[i][2 * r + 1] = 0.0f;
 #pragma unroll 2
-                for (int c = 0; c < p.npieces; ++c) {
-                    const int64_t base =
-                        (int64_t)(2 * (p.first + c) + (c == 0)) * ROWS + g + 8 * r;
-                    const float2 f = __ldcg(a.part_ml + base);
-                    const float top = fmaxf(m[r], f.x);
-                    const float fo = max_factor(m[r], top), fp = max_factor(f.x, top);
-                    m[r] = top;
-                    l[r] = l[r] * fo + f.y * fp;
-                    const float *src = a.part_o + base * D + 2 * t;
+                    for (int c = 0; c < join.n; ++c) {
+                        const int64_t base = part_row(join.first + c * join.step) + 8 * r;
+                        const float2 f = __ldcg(a.part_ml + base);
+                        const float top = fmaxf(m[r], f.x);
+                        const float fo = max_factor(m[r], top), fp = max_factor(f.x, top);
+                        m[r] = top;
+                        l[r] = l[r] * fo + f.y * fp;
+                        const float *src = a.part_o + base * D + 2 * t;
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(src + 8 * i));
-                        o[i][2 * r] = o[i][2 * r] * fo + v.x * fp;
-                        o[i][2 * r + 1] = o[i][2 * r + 1] * fo + v.y * fp;
+                        for (int i = 0; i < D / 8; ++i) {
+                            const float2 v = __ldcg(reinterpret_cast<const float2 *>(src + 8 * i));
+                            o[i][2 * r] = o[i][2 * r] * fo + v.x * fp;
+                            o[i][2 * r + 1] = o[i][2 * r + 1] * fo + v.y * fp;
+                        }
                     }
                 }
+                if (join.all) break;
+                // the group's sum in the place of its first piece
+                __syncwarp();
+                at = part_row(join.first);
+                join = join_of_groups(p, width);
             }
+            if (!joined) continue;
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {

@@ -24,7 +24,7 @@ static long long g_checked = 0, g_fail = 0;
     } while (0)
 
 template <int KT, int PAD>
-static void check(PagedArgs a, int grid, int min_pairs) {
+static void check(PagedArgs a, int grid, int min_pairs, int most) {
     // the line, pair by pair, as the header's comment states it
     const int nb = a.prefix_phase ? 1 : a.B;
     std::vector<std::tuple<int, int, int, int>> line;  // (sequence, row tile, head, key tile)
@@ -117,6 +117,32 @@ static void check(PagedArgs a, int grid, int min_pairs) {
     }
     CHECK(at == total);
     for (auto &e : parts) CHECK((int)e.second.size() == want[e.first]);
+    // the joins: every piece once, in groups whose counters are nobody else's
+    std::map<int, std::tuple<std::tuple<int, int, int>, int>> group;
+    for (auto &e : parts) {
+        Piece p;
+        p.first = e.second[0];
+        p.npieces = (int)e.second.size();
+        const int width = join_width(p.npieces, most);
+        CHECK(width >= 1 && (width == p.npieces) == (p.npieces <= most));
+        int pieces = 0;
+        for (int c = 0; c < p.npieces; ++c) {
+            const Join j = join_of(p, c, width);
+            CHECK(j.first <= c && c < j.first + j.n && j.step == 1 && j.n <= width);
+            CHECK(j.first + j.n <= p.npieces && j.all == (p.npieces <= most));
+            CHECK(j.counter >= 0 && j.counter < 2 * kMaxWorkers);
+            const auto who = std::make_tuple(e.first, j.first);
+            CHECK(!group.count(j.counter) || group[j.counter] == who);
+            group[j.counter] = who;
+            if (c == j.first) pieces += j.n;
+            if (j.all) continue;
+            const Join k = join_of_groups(p, width);
+            CHECK(j.first % k.step == 0 && j.first / k.step < k.n && k.all && k.first == 0);
+            CHECK((k.n - 1) * k.step < p.npieces && k.n * k.step >= p.npieces);
+            CHECK(k.counter == p.first);
+        }
+        CHECK(pieces == p.npieces);
+    }
     Share sh;
     set_shares(sh, (int)total, workers, 0);
     for (int64_t x = 0; x < total; x += 1 + total / 97) {
@@ -162,9 +188,10 @@ int main() {
             // the prefix in front of every item's own keys, or not
             a.front_tiles = phase || trial % 5 < 2 ? 0 : (a.prefix_len + KT - 1) / KT;
             a.front_shift = a.front_tiles ? a.front_tiles * KT - a.kstart : 0;
-            const int grid = pick(1, 152), least = pick(1, 4);
-            if (KT == 16) check<16, 2>(a, grid, least);
-            else trial % 4 == 1 ? check<128, 4>(a, grid, least) : check<128, 6>(a, grid, least);
+            const int grid = pick(1, 152), least = pick(1, 4), most = pick(2, 16);
+            if (KT == 16) check<16, 2>(a, grid, least, most);
+            else trial % 4 == 1 ? check<128, 4>(a, grid, least, most)
+                                : check<128, 6>(a, grid, least, most);
         }
     }
     // the closed-form sum against a loop

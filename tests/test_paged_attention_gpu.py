@@ -90,6 +90,21 @@ def test_prefix_longer_than_a_sequence(sq):
     verify(sq, Batch([1, 3, 2, 1], [50, 2, 0, 200], 8, 2, 128, 32, BF, prefix=150, seed=3).cuda())
 
 
+@pytest.mark.parametrize("q,kv,Hq,Hkv,D,dtype", [
+    ([1], [20011], 4, 1, 64, FP),                # a thousand pieces of few rows
+    ([2, 1], [9000, 12000], 8, 1, 128, BF),
+    ([8], [12001], 16, 1, 128, BF),              # dozens of pieces of many rows
+    ([33, 5], [5000, 9000], 8, 2, 64, FP),
+])
+def test_pieces_joined_by_groups(sq, q, kv, Hq, Hkv, D, dtype):
+    t = Batch(q, kv, Hq, Hkv, D, 64, dtype, seed=sum(kv)).cuda()
+    ws = sq.empty_workspace(sq.paged_attention_workspace_bytes(t.T, Hq, Hkv, D))
+    first = verify(sq, t, workspace=ws)
+    for _ in range(5):
+        assert torch.equal(call(sq, t, workspace=ws), first)
+    assert int(ws[:16384].max()) == 0, "a counter was left behind"
+
+
 def many_behind(prefix, tiles_per_sm, Hkv, tail, **kw):
     """A batch of single tokens (and `tail`) so large that its shared prefix,
     read for every sequence, would be more than tiles_per_sm key tiles of 128
