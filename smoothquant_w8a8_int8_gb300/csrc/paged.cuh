@@ -47,6 +47,30 @@ __device__ __forceinline__ void split16(float a, float b, uint32_t (&w)[N]) {
     }
 }
 
+__device__ __forceinline__ void lds4(uint32_t (&w)[4], uint32_t addr) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// Bits 15 and 31: the 16-bit numbers of the pair that are not finite (an exponent
+// of ones; adding its lowest bit carries into the sign's place).
+template <bool BF>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+    return ((w & (BF ? 0x7f807f80u : 0x7c007c00u)) + (BF ? 0x00800080u : 0x04000400u)) &
+           0x80008000u;
+}
+// the pair with zeros in their places
+template <bool BF>
+__device__ __forceinline__ uint32_t finite_part(uint32_t w) {
+    const uint32_t f = not_finite<BF>(w);
+    return w & ((f & 0x8000u ? 0u : 0xffffu) | (f >> 31 ? 0u : 0xffff0000u));
+}
+template <bool BF>
+__device__ __forceinline__ float widen16(uint32_t low) {
+    return BF ? __uint_as_float(low << 16) : __half2float(__ushort_as_half((uint16_t)low));
+}
+
 // The line's length and the shares of this block's W workers (worker w of block
 // c is number w gridDim.x + c, so that neighbours on the line are on different
 // SMs), by all NT threads: each sums a run of sequences, a scan over the

@@ -309,7 +309,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             bool cut = kr.key < kr.lo || kr.key + kKT > kr.hi ||
                        (R > 1 && kr.key + kKT > hi1);
             const bool missing = holes >> cur & 1;
-            if (__any_sync(0xffffffffu, cut || missing)) {
+            cut = __any_sync(0xffffffffu, cut);
+            if (cut || missing) {
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -340,6 +341,54 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                         o[i][2 * r] *= grow[r];
                         o[i][2 * r + 1] *= grow[r];
                     }
+            }
+            if (cut) {
+                // a masked key's probability is zero, but its value need not be
+                // finite, and zero times that is NaN: such values are added to the
+                // rows that see them and taken out of the step
+                constexpr int kChunks = kKT * D / 8 / 32;  // 16-byte chunks per lane
+                uint32_t bad = 0;
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) {
+                    uint32_t w[4];
+                    lds4(w, vs + (i * 32 + lane) * 16);
+                    bad |= not_finite<BF>(w[0]) | not_finite<BF>(w[1]) | not_finite<BF>(w[2]) |
+                           not_finite<BF>(w[3]);
+                }
+                if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll 1
+                    for (int k = 0; k < kKT; ++k) {
+                        const int at = kr.key + k;
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i) {
+                            uint32_t w;
+                            asm volatile("ld.shared.b32 %0, [%1];"
+                                         : "=r"(w)
+                                         : "r"(vs + k * D * 2 + ((i ^ (k & 7)) << 4) + 4 * t)
+                                         : "memory");
+                            const uint32_t f = not_finite<BF>(w);
+#pragma unroll
+                            for (int r = 0; r < R; ++r) {
+                                if (at < kr.lo || at >= (r ? hi1 : kr.hi)) continue;
+                                if (f & 0x8000u) o[i][2 * r] += widen16<BF>(w & 0xffffu);
+                                if (f >> 31) o[i][2 * r + 1] += widen16<BF>(w >> 16);
+                            }
+                        }
+                    }
+                    __syncwarp();
+#pragma unroll 1
+                    for (int i = 0; i < kChunks; ++i) {
+                        uint32_t w[4];
+                        lds4(w, vs + (i * 32 + lane) * 16);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[j] = finite_part<BF>(w[j]);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         vs + (i * 32 + lane) * 16),
+                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                     : "memory");
+                    }
+                    __syncwarp();
+                }
             }
             uint32_t pf[S][4];
 #pragma unroll

@@ -149,6 +149,7 @@ struct TileBars {
     unsigned miss[kMiss];  // bit i: keys 16 i .. 16 i + 15 of the tile are of a missing page
     Piece items[kItems];
     int stop[kItems];
+    int bad[kItems];  // values of a piece that are not finite were taken out of its tiles
     Share share;
     float2 stat[kStats][2][kRows];  // a tile's row maxima (log2 units) and half sums
     float half_max[2][2][kRows];    // a tile's row maxima over its halves
@@ -281,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_init(&B.group, 4);
         for (int i = 0; i < 4; ++i) bar_init(&B.pair[i], 2);
         bar_init(&B.mma_done, 1);
+        for (int i = 0; i < kItems; ++i) B.bad[i] = 0;
         B.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -388,6 +390,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n >= kItems &&
                     !warp_wait(&B.item_empty[it], (n / kItems - 1) & 1u, abort, a.error))
                     break;
+                if (more && a.prefix_phase) {
+                    // what every row sees: of the prefix, the least that any does
+                    int least = a.prefix_len;
+                    for (int i = lane; i < p.ntok; i += 32) least = min(least, row_limit(a, p, i));
+                    p.pos0 = __reduce_min_sync(0xffffffffu, least) - 1;
+                }
                 if (lane == 0) {
                     B.stop[it] = !more;
                     if (more) B.items[it] = p;
@@ -404,9 +412,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ct = threadIdx.x - 384;
         uint32_t seq = 0, done = 0, tile = 0;  // slots begun, slots handed over, tiles begun
         bool ok = true;
+        // thread: chunk ch of rows r0, r0 + kRowStep, ... of a slot
+        constexpr int kRowStep = 128 / (D / 8);
+        const int r0 = ct / (D / 8), ch = ct % (D / 8);
+        const uint32_t my_chunk =
+            (ch >> 3) * C::kSlab + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4);
+        uint32_t scan = 0;  // 4 bits per slot: 1 + the piece's slot where values are looked at
         auto hand_over = [&](bool all) {
             if (all) asm volatile("cp.async.wait_group 0;" ::: "memory");
             else asm volatile("cp.async.wait_group 1;" ::: "memory");
+            if (scan != 0) {
+                // A masked key's probability is zero, but its value need not be
+                // finite, and zero times that is NaN: in tiles of which a row does not
+                // see every key such values are taken out here (each thread its own
+                // copies) and left to the item's end.
+                for (uint32_t d = done; d < seq - (all ? 0 : 1); ++d) {
+                    const int s4 = 4 * (d % NS);
+                    const uint32_t who = scan >> s4 & 15u;
+                    if (who == 0) continue;
+                    scan &= ~(15u << s4);
+                    const uint32_t from = ring + (d % NS) * C::kSlot + my_chunk;
+                    uint32_t bad = 0;
+#pragma unroll 4
+                    for (int j = 0; j < kKT / kRowStep; ++j) {
+                        uint32_t w[4];
+                        lds4(w, from + j * kRowStep * 128);
+                        bad |= not_finite<BF>(w[0]) | not_finite<BF>(w[1]) |
+                               not_finite<BF>(w[2]) | not_finite<BF>(w[3]);
+                    }
+                    if (bad) {
+                        B.bad[who - 1] = 1;
+#pragma unroll 1
+                        for (int j = 0; j < 4 * (kKT / kRowStep); ++j) {
+                            const uint32_t at = from + (j >> 2) * kRowStep * 128 + 4 * (j & 3);
+                            uint32_t w;
+                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at),
+                                         "r"(finite_part<BF>(w))
+                                         : "memory");
+                        }
+                    }
+                }
+            }
             fence_async_smem();
             __syncwarp();
             while (done < seq - (all ? 0 : 1)) {
@@ -416,7 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // 128 rows of a cache into the next slot; lane l (of 8) holds the place of
         // rows 16 l .. 16 l + 15 in the caches, in bytes
-        auto copy_slot = [&](const uint16_t *cache, int64_t place, unsigned miss, int lo, int hi) {
+        auto copy_slot = [&](const uint16_t *cache, int64_t place, unsigned miss, int lo, int hi,
+                             uint32_t look) {
             const uint32_t sl = seq % NS;
             if (seq >= NS) {
                 const uint32_t ph = (seq / NS - 1) & 1u;
@@ -428,19 +476,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return;
                 }
             }
-            // thread: chunk ch of rows r0, r0 + kStep, ... of every 16
-            constexpr int kStep = 128 / (D / 8);
-            const int r0 = ct / (D / 8), ch = ct % (D / 8);
-            const uint32_t dst = ring + sl * C::kSlot + (ch >> 3) * C::kSlab + r0 * 128 +
-                                 (((ch & 7) ^ (r0 & 7)) << 4);
+            const uint32_t dst = ring + sl * C::kSlot + my_chunk;
+            scan |= look << 4 * sl;
             const char *src = reinterpret_cast<const char *>(cache) + (r0 * D + ch * 8) * 2;
             if (miss == 0 && lo <= 0 && hi >= kKT) {
 #pragma unroll
                 for (int j = 0; j < kKT / 16; ++j) {
                     const char *from = src + __shfl_sync(0xffffffffu, place, j);
 #pragma unroll
-                    for (int i = 0; i < 16 / kStep; ++i)
-                        copy16(dst + (16 * j + i * kStep) * 128, from + i * kStep * D * 2, true);
+                    for (int i = 0; i < 16 / kRowStep; ++i)
+                        copy16(dst + (16 * j + i * kRowStep) * 128, from + i * kRowStep * D * 2, true);
                 }
             } else {
 #pragma unroll 1
@@ -448,11 +493,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const char *from = src + __shfl_sync(0xffffffffu, place, j);
                     const bool page = !(miss >> j & 1);
 #pragma unroll
-                    for (int i = 0; i < 16 / kStep; ++i) {
-                        const int r = 16 * j + r0 + i * kStep;
+                    for (int i = 0; i < 16 / kRowStep; ++i) {
+                        const int r = 16 * j + r0 + i * kRowStep;
                         const bool in = page && r < hi && r >= lo;
-                        copy16(dst + (16 * j + i * kStep) * 128,
-                               in ? from + i * kStep * D * 2 : reinterpret_cast<const char *>(cache),
+                        copy16(dst + (16 * j + i * kRowStep) * 128,
+                               in ? from + i * kRowStep * D * 2 : reinterpret_cast<const char *>(cache),
                                in);
                     }
                 }
@@ -466,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int64_t v_place = 0;
         unsigned v_miss = 0;
         int v_lo = 0, v_hi = 0, left = 0, key0 = 0;
+        uint32_t v_look = 0;
         Piece p = {};
         bool more = true;
         int entry = -1;
@@ -498,6 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int64_t place = 0;
             unsigned miss = 0;
             int lo = 0, hi = 0;
+            uint32_t look = 0;
             if (more) {
                 // the next tile's entry is on its way meanwhile
                 const int e = entry;
@@ -505,6 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int key = r.key + 16 * (lane & 7);
                 lo = r.lo - r.key;
                 hi = r.hi - r.key;
+                if (key_range(a, key0, p.pos0 + 1).hi < r.key + kKT)
+                    look = 1 + (n - 1) % kItems;  // (the piece's first row does not see all)
                 entry = left > 1 ? page_of(key_range(a, key0 + kKT, p.keys)) : -1;
                 const bool there = e >= 0 && e < a.num_pages;
                 miss = ~__ballot_sync(0xffffffffu, there) & 0xffu;
@@ -517,11 +566,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int kv = more ? 0 : 1; kv < (tile > 0 ? 2 : 1) && ok; ++kv)
                 copy_slot(kv ? v_cache : k_cache, kv ? v_place : place, kv ? v_miss : miss,
-                          kv ? v_lo : lo, kv ? v_hi : hi);
+                          kv ? v_lo : lo, kv ? v_hi : hi, kv ? v_look : 0u);
             v_place = place;
             v_miss = miss;
             v_lo = lo;
             v_hi = hi;
+            v_look = look;
             if (more) {
                 ++tile;
                 --left;
@@ -785,6 +835,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                     upk(mul2(o2[2 * i + 1], f2), v.z, v.w);
                     __stcg(reinterpret_cast<float4 *>(dst) + i, v);
                 }
+            }
+            if (B.bad[it]) {
+                // values that the copies took out of the tiles that not every row sees
+                // in full: added to the rows that see them
+                float *own = dst;
+                if (live) {
+                    const int limit = row_limit(a, p, tok);
+                    int k0 = p.key0;
+#pragma unroll 1
+                    for (int k = 0; k < p.ntiles; ++k, k0 += kKT) {
+                        const KeyRange kr = key_range(a, k0, limit);
+                        if (key_range(a, k0, p.pos0 + 1).hi >= kr.key + kKT) continue;
+                        const int *pages = kr.front ? a.prefix_pages
+                                                    : a.block_table + (int64_t)p.seq * a.max_pages;
+                        const int to = min(kr.hi, kr.key + kKT);
+#pragma unroll 1
+                        for (int key = max(kr.lo, kr.key); key < to; ++key) {
+                            const int e = __ldg(pages + (key >> a.page_shift));
+                            if (e < 0 || e >= a.num_pages) continue;
+                            const uint16_t *v =
+                                v_cache + ((((int64_t)e * a.Hkv + p.head) << a.page_shift) +
+                                           (key & ((1 << a.page_shift) - 1))) * D;
+#pragma unroll 1
+                            for (int c = 0; c < D; ++c) {
+                                const uint32_t x = v[c];
+                                if (not_finite<BF>(x)) __stcg(own + c, __ldcg(own + c) + widen16<BF>(x));
+                            }
+                        }
+                    }
+                }
+                if (!group_sync()) break;
+                if (row == 0) B.bad[it] = 0;
             }
             if (!whole) {
                 // this CTA's part of the item is out; whoever is last of a group, and

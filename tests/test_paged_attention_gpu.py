@@ -156,6 +156,62 @@ def test_prefix_in_front_of_own_keys(sq, prefix, q, kv, D, dtype, page):
                      behind=1).cuda())
 
 
+def poisoned(sq, t, places):
+    """`places`: (sequence, position) whose values are NaN in column 5 and infinite in
+    column 38 of every head.  Outputs are the formula's: not finite in those columns
+    for the rows that attend to the position, untouched everywhere else."""
+    t.cuda()
+    ref, bound = attention_ref(t, t.D ** -0.5)
+    hit = torch.zeros(t.T, t.Hq, t.D, dtype=torch.bool)
+    for b, pos in places:
+        page, row = t.row(b, pos)
+        t.v_d[page, :, row, 5] = float("nan")
+        t.v_d[page, :, row, 38] = float("inf")
+        for c in range(t.B) if pos < t.prefix else [b]:
+            first = t.kv_lens[c] - t.q_lens[c]
+            for i in range(t.q_lens[c]):
+                if first + i >= pos:
+                    hit[int(t.q_start[c]) + i, :, (5, 38)] = True
+    hit = hit.view(t.T, -1)
+    out = torch.full((t.T, t.Hq * t.D), 7.0, device="cuda")
+    got = call(sq, t, out=out).double().cpu()
+    no_seq = torch.isnan(ref)
+    assert torch.all(got[no_seq] == 7.0)
+    assert not torch.isfinite(got[hit]).any(), "a value that is seen was lost"
+    rest = ~hit & ~no_seq
+    assert torch.isfinite(got[rest]).all(), "a masked value was seen"
+    assert float(((got - ref).abs() - bound)[rest].max()) <= 0
+    assert sq.device_status() == sq.SQ_OK
+
+
+@pytest.mark.parametrize("D,dtype", [(64, BF), (128, FP), (128, BF), (64, FP)])
+@pytest.mark.parametrize("q,kv,Hq,Hkv,places", [
+    ([3, 2], [40, 17], 4, 2, [(0, 39), (1, 16)]),               # few rows: a draft's last token
+    ([4, 1], [4, 60], 2, 2, [(0, 2), (1, 59)]),
+    ([40, 30], [40, 300], 8, 2, [(0, 39), (0, 17), (1, 299)]),  # chunks
+    ([300], [300], 4, 2, [(0, 128), (0, 250), (0, 299)]),
+    ([16, 1], [9000, 5], 16, 1, [(0, 8990), (1, 4)]),           # many pieces
+])
+def test_values_that_are_not_finite_in_masked_places(sq, q, kv, Hq, Hkv, places, D, dtype):
+    poisoned(sq, Batch(q, kv, Hq, Hkv, D, 32, dtype, seed=sum(kv)), places)
+
+
+@pytest.mark.parametrize("prefix", [40, 130, 300])
+@pytest.mark.parametrize("q", [[1, 2, 1], [1, 70, 20]])
+def test_values_that_are_not_finite_in_a_prefix(sq, prefix, q):
+    """Sequences that end inside the prefix do not see its last positions."""
+    kv = [prefix // 2, prefix + 80, max(prefix - 1, q[2])]
+    for D, dtype in ((64, FP), (128, BF)):
+        poisoned(sq, Batch(q, kv, 8, 4, D, 16, dtype, prefix=prefix, seed=prefix),
+                 [(1, prefix - 1), (1, prefix // 2 + 1), (1, prefix + 79)])
+
+
+@pytest.mark.parametrize("tiles_per_sm,tail", [(40, []), (20, [30])])
+def test_values_that_are_not_finite_in_a_prefix_of_its_own(sq, tiles_per_sm, tail):
+    t = many_behind(100, tiles_per_sm, 8, tail, Hq=8, D=64, page=32, dtype=BF, seed=3)
+    poisoned(sq, t, [(5, 99), (5, 60), (9, t.kv_lens[9] - 1)])
+
+
 def test_many_sequences(sq):
     q = [1 + (i % 3 == 0) for i in range(300)]
     kv = [(37 * i) % 200 for i in range(300)]
