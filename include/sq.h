@@ -263,20 +263,24 @@ sq_status sq_kv_append(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv, int
  *   O[t][h D + d] = sum_{k <= p} P[k] V[k][d],   P = softmax_k(scale Q[t][h] . K[k]).
  * Positions k < prefix_len are read from page prefix_pages[k / page_size] for
  * every sequence -- a prefix that the batch shares, read and multiplied once for
- * all of it -- and the others from block_table; prefix_len need not be a
- * multiple of page_size, 0 means none (prefix_pages may then be NULL).  Entries
- * of block_table in front of page prefix_len / page_size are not used.
+ * all of it (or for each sequence, where that is faster: few sequences, or long
+ * ones) -- and the others from block_table; prefix_len need not be a multiple of
+ * page_size, 0 means none (prefix_pages may then be NULL).  Entries of block_table
+ * in front of page prefix_len / page_size are not used.
  * A token with no key at or before its position (kv_len[b] = 0, or more tokens
  * than kv_len[b]) gets zeros.  Keys whose page entry is outside [0, num_pages)
  * are left out, as if masked; kv_len is taken as at most max_pages * page_size,
- * and cache rows at or behind kv_len are not used, whatever they hold.
+ * and cache rows at or behind kv_len are not used, whatever they hold; nor do keys
+ * and values of positions behind a token's own reach its row, finite or not.
  * Q fp32, rows of ldq floats (ldq >= Hq D, a multiple of 4); O fp32 [T][Hq D],
  * overlapping nothing.  max_q: the most tokens of a sequence; it chooses the
  * kernel only, results do not depend on it but for rounding.
- * Queries and probabilities enter the tensor cores as pairs of 16-bit numbers
- * of the cache's type and products are summed in fp32, as are the softmax's
- * maxima and sums: O agrees with the exact attention over the stored rows to
- * about 2^-18 of max |V| (bf16) or 2^-21 (fp16; |Q| at most 65504).
+ * Queries and probabilities enter the tensor cores as sums of 16-bit numbers of
+ * the cache's type, three for bf16 (exact) and two for fp16 (within 2^-22; |Q| at
+ * most 65504), and products are summed in fp32, as are the softmax's maxima and
+ * sums: O agrees with the exact attention over the stored rows as far as fp32
+ * logits and sums do, to a few 2^-21 of max |V| where logits are of order one.
+ * Results are the same bits from call to call.
  * workspace (16-byte aligned, zero-filled once before its first use): at least
  * sq_paged_attention_workspace_bytes bytes; it serves one call at a time, on
  * the rules of sq_linear_i8_ws (calls that share one must be ordered; after

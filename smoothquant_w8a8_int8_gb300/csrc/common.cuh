@@ -208,6 +208,7 @@ sq_status launch_rmsnorm_quant(const float *H, const float *residual, const floa
                                float eps, const float *s, int64_t rows, int64_t K,
                                float static_scale, float *R, float *Y, int8_t *q, float *scale,
                                __nv_bfloat16 *op, int32_t *l1, cudaStream_t st);
+// The rotation's table, and the append to the paged cache with the rotation.
 sq_status launch_rope_table(const float *inv_freq, int64_t positions, int64_t rot, float *table,
                             cudaStream_t st);
 sq_status launch_kv_append(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
@@ -216,12 +217,11 @@ sq_status launch_kv_append(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv,
                            int64_t B, const int32_t *block_table, int64_t max_pages,
                            void *k_cache, void *v_cache, int cache_type, int64_t num_pages,
                            int64_t page_size, float *Q, int64_t ldq, cudaStream_t st);
-// A 2-D TMA tensor map over a row-major bf16 or fp16 matrix, as make_map_f32.
-sq_status make_map_16(void *map, bool bf16, const void *base, int64_t rows, int64_t cols,
-                      int box_rows, int box_cols);
+// The error word of the attention over the paged cache, and its workspace.
 sq_status paged_take_error(cudaStream_t st);
 sq_status paged_workspace_bytes(int64_t T, int64_t Hq, int64_t D, int64_t prefix_len,
                                 size_t *bytes);
+// Attention over the paged cache (the arguments of sq_paged_attention, checked).
 struct PagedCall {
     const float *Q;
     int64_t ldq, T, Hq, Hkv, D;

@@ -9,7 +9,9 @@
 // pairs (j, j + rot/2) or, interleaved, (2j, 2j + 1).  Queries leave in fp32;
 // keys and values are rounded once, to the cache's 16-bit type, into row
 // p % page_size of page block_table[b][p / page_size].
-// Memory-bound: every projected element is read once and written once.
+// Memory-bound: every projected element is read once and written once.  Measured:
+// 7976 tokens of 32 / 8 heads of 128, bf16: 54 us, 6.8 TB/s, the measured copy
+// rate; 64 tokens 5 us, latency.
 #include "common.cuh"
 
 #include <cuda_fp16.h>
@@ -164,15 +166,18 @@ sq_status launch_kv_append(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv,
     DeviceInfo di;
     sq_status rc = device_info(&di);
     if (rc != SQ_OK) return rc;
-    // a few tokens: a unit per thread; many: a block per token
+    // a few tokens: a unit per thread; many: a block per token (32 / 8 heads of 128,
+    // cold L2, launch included: 64 tokens 7.8 and 9.9 us, 256: 8.6 and 9.7, 512: 11.9
+    // and 12.5, 1024: 16.7 and 16.0, 2048: 24.8 and 22.9)
     const int64_t units = (Hq + 2 * Hkv) * D / 8;
     const int64_t gy = T <= 2 * di.sms ? (units + kAppendThreads - 1) / kAppendThreads : 1;
     const int64_t grid = std::min<int64_t>(T, (int64_t)di.sms * 64);
-    return launch_pdl(cache_type == SQ_CACHE_BF16 ? kv_append_kernel<true> : kv_append_kernel<false>,
-                      dim3((unsigned)grid, (unsigned)gy), dim3(kAppendThreads), 0, st, 1, QKV, T, (int)Hq,
-                      (int)Hkv, (int)D, rope, rope_positions, (int)rot, interleaved, q_start,
-                      kv_len, (int)B, block_table, max_pages, static_cast<uint16_t *>(k_cache),
-                      static_cast<uint16_t *>(v_cache), num_pages, (int)page_size, Q, ldq);
+    return launch_pdl(
+        cache_type == SQ_CACHE_BF16 ? kv_append_kernel<true> : kv_append_kernel<false>,
+        dim3((unsigned)grid, (unsigned)gy), dim3(kAppendThreads), 0, st, 1, QKV, T, (int)Hq,
+        (int)Hkv, (int)D, rope, rope_positions, (int)rot, interleaved, q_start, kv_len, (int)B,
+        block_table, max_pages, static_cast<uint16_t *>(k_cache),
+        static_cast<uint16_t *>(v_cache), num_pages, (int)page_size, Q, ldq);
 }
 
 }  // namespace sq

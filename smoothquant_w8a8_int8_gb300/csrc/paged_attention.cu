@@ -33,7 +33,14 @@ sq_status error_word(int device, unsigned **out) {
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
-// Whether a row tile's work fits the kernel for few rows (per key/value head).
+// Whether a sequence's rows (tokens x heads of a key/value head's group) go to the
+// kernel for few rows: one tile of at most 16 of its rows, whose cost is the cache's
+// way through the SMs.  The other kernel's tile of 128 rows costs the same for 8
+// rows as for 128.  Measured at 16 rows, few against many (32 / 8 heads of 128, 4
+// tokens a sequence; us): 1 sequence of 300 keys 21 and 27, 16 of 4000 84 and 98
+// (bf16), 80 and 80 (fp16), 64 of 4000 203 and 307, 184 and 234, heads of 64 129
+// and 248, 119 and 191.  Two tiles of few rows read and multiply everything twice:
+// 406 against 307 us.
 bool few_rows(int64_t tokens, int G) { return std::max<int64_t>(1, tokens) * G <= 16; }
 
 // Whether the shared prefix is read in front of every item's own keys instead of
@@ -119,8 +126,6 @@ sq_status launch_paged_attention(const PagedCall &c, cudaStream_t st) {
     for (int phase = c.prefix_len > 0 && !front ? 1 : 0; phase >= 0; --phase) {
         a.prefix_phase = phase;
         const int64_t most = phase ? c.T : std::min(c.max_q, c.T);
-        // up to 16 rows per key/value head: the warp-level products; more: tensor
-        // memory's
         const bool few = few_rows(most, a.G);
         const int r = few ? (std::max<int64_t>(1, most) * a.G <= 8 ? 8 : 16) : 128;
         const int kt = few ? 16 : 128;

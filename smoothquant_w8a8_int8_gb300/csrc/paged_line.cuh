@@ -7,9 +7,10 @@
 // tiles of KT.  All (item, key tile) pairs stand in one line -- sequences,
 // then row tiles, then key/value heads, then key tiles -- each item's followed
 // by PAD pairs without work that stand for the time of its start and end (none
-// where all items are of one length, over a shared prefix), and worker c of n (a CTA, or a warp) takes pairs [c W / n, (c + 1) W / n): every
-// worker has the same share whatever the lengths, known only on the device, are.  An item that
-// lies in several workers' shares leaves one partial result (row maximum, sum,
+// where all items are of one length, over a shared prefix), and worker c of n (a
+// CTA, or a warp) takes pairs [c W / n, (c + 1) W / n): every worker has the same
+// share whatever the lengths, known only on the device, are.  An item that lies in
+// several workers' shares leaves one partial result (row maximum, sum,
 // unnormalised output) per worker in the workspace; the one that arrives last
 // (a counter) joins them in the order of the line, so that the result does not
 // depend on who is last.  The line is shorter than 2^31 pairs (checked on the

@@ -20,6 +20,11 @@
 // The products run on the warp-level tensor instructions (m16n8k16, 8 cycles
 // each per SM quarter): 16 rows are too few for tensor memory's 128.
 //
+// Measured (32 / 8 heads of 128, bf16): a step of 64 sequences of up to 8192 keys
+// 160 us, 6.5 TB/s, 96 % of the measured copy rate; one token behind 300 keys 13
+// us, behind 4000 21, behind 100,000 83 (4.8 TB/s): those are bound by latency, the
+// start's chain of dependent loads and the pieces' join.
+//
 // Precision: keys and values enter as stored.  The fp32 queries and
 // probabilities are split over several 16-bit numbers (split16): two for fp16
 // (within 2^-22), three for bf16 (exact).

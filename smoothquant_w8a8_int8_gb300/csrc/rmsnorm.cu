@@ -10,7 +10,11 @@
 // scale = fl(max|v| / 127) or the given one, code = round-half-even(fl(v / scale)).
 // The row stays in registers from the one read of H and the residual to the
 // codes: 8 bytes read and 4 + 2 written per element with the sum and the
-// operand asked for, which is what bounds the kernel.
+// operand asked for.  Bound: memory and the codes' arithmetic together (54
+// instructions an element: the definition's divisions, by reciprocals that are
+// corrected or checked; 59 % of the issue slots).  Measured: 8192 x 4096 with
+// sum and operand 85 us, 5.5 TB/s, 81 % of the measured copy rate; 1237 x 5136
+// with a static scale 25 us; 16 x 4096 6.4 us, latency.
 #include "row_codes.cuh"
 
 #include <algorithm>
@@ -243,10 +247,17 @@ sq_status launch_rmsnorm_quant(const float *H, const float *residual, const floa
     if (rc != SQ_OK) return rc;
     if (K > kMaxRow) return SQ_ERR_UNSUPPORTED;
     const int K4 = (int)(K / 4);
-    const bool one = rows <= di.sms && K4 <= 2048;
-    // one row per block: as few float4 per thread as 1024 threads allow; else four
-    const int vpt = !one ? 4 : K4 <= 1024 ? 1 : 2;
-    const int tpr = ((K4 + vpt - 1) / vpt + 31) / 32 * 32;
+    // A block per row, its threads holding as few float4 as 1024 of them allow and
+    // the column's factors in registers, while all rows are on the GPU at once; else
+    // four float4 a thread and the factors in shared memory, and several rows per
+    // block.  Measured, block per row against the other: 16 x 4096 8.7 and 11.8 us,
+    // 152 x 4096 9.8 and 13.9, 304 x 4096 15.9 and 14.6, 152 x 8192 11.9 and 14.7,
+    // 608 x 1024 8.8 and 9.9, 608 x 4096 24.2 and 16.1 (cold L2, launch included).
+    const int vpt1 = K4 <= 1024 ? 1 : 2;
+    const int tpr1 = ((K4 + vpt1 - 1) / vpt1 + 31) / 32 * 32;
+    const bool one = K4 <= 2048 && rows <= (int64_t)di.sms * (1024 / tpr1);
+    const int vpt = one ? vpt1 : 4;
+    const int tpr = one ? tpr1 : ((K4 + 3) / 4 + 31) / 32 * 32;
     const int nt = one ? tpr : tpr * std::max(1, 256 / tpr);
     static const RmsKern kerns[2][3] = {
         {rmsnorm_quant_kernel<false, 1, true>, rmsnorm_quant_kernel<false, 2, true>,
