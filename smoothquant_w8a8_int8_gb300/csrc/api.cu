@@ -1,6 +1,6 @@
 // C-ABI boundary: argument checks, then one launch per call on the caller's
 // stream.  Declarations and the contract of every entry point are in sq.h.
-#include "common.cuh"
+#include "decoder.cuh"
 
 #include <cmath>
 #include <mutex>

@@ -12,7 +12,7 @@
 // Memory-bound: every projected element is read once and written once.  Measured:
 // 7976 tokens of 32 / 8 heads of 128, bf16: 54 us, 6.8 TB/s, the measured copy
 // rate; 64 tokens 5 us, latency.
-#include "common.cuh"
+#include "decoder.cuh"
 
 #include <cuda_fp16.h>
 

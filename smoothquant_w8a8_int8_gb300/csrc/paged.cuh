@@ -1,7 +1,7 @@
 // Shared parts of the attention kernels over the paged cache: the workers'
 // shares, the split of fp32 numbers over 16-bit ones, and the rows' last step.
 #pragma once
-#include "common.cuh"
+#include "decoder.cuh"
 #include "paged_line.cuh"
 
 #include <cuda_fp16.h>

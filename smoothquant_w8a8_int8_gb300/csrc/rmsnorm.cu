@@ -15,6 +15,7 @@
 // corrected or checked; 59 % of the issue slots).  Measured: 8192 x 4096 with
 // sum and operand 85 us, 5.5 TB/s, 81 % of the measured copy rate; 1237 x 5136
 // with a static scale 25 us; 16 x 4096 6.4 us, latency.
+#include "decoder.cuh"
 #include "row_codes.cuh"
 
 #include <algorithm>
