@@ -249,7 +249,7 @@ sq_status sq_rope_table(const float *inv_freq, int64_t positions, int64_t rot, f
  * other row of the cache is touched.  A token whose position is negative or has
  * no row in `rope` gets a zero query row and is not stored; one whose page is
  * outside the table or [0, num_pages) is not stored.  Two tokens of one call
- * with the same page and row leave one of the two.
+ * with the same page and row leave one of the two in each element.
  * Pointers 16-byte aligned but for the int32 arrays. */
 sq_status sq_kv_append(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
                        const float *rope, int64_t rope_positions, int64_t rot, int interleaved,
