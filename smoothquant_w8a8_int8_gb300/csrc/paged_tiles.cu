@@ -160,7 +160,8 @@ struct TileBars {
     unsigned miss[kMiss];  // bit i: keys 16 i .. 16 i + 15 of the tile are of a missing page
     Piece items[kItems];
     int stop[kItems];
-    int bad[kItems];  // values of a piece that are not finite were taken out of its tiles
+    int bad_from[kItems], bad_to[kItems];  // the tiles (of the share) of a piece that values
+                                           // which are not finite were taken out of
     Share share;
     float2 stat[kStats][2][kRows];  // a tile's row maxima (log2 units) and half sums
     float half_max[2][2][kRows];    // a tile's row maxima over its halves
@@ -294,7 +295,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_init(&B.group, 4);
         for (int i = 0; i < 4; ++i) bar_init(&B.pair[i], 2);
         bar_init(&B.mma_done, 1);
-        for (int i = 0; i < kItems; ++i) B.bad[i] = 0;
+        for (int i = 0; i < kItems; ++i) {
+            B.bad_from[i] = 0x7fffffff;
+            B.bad_to[i] = -1;
+        }
         B.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -453,7 +457,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                not_finite<BF>(w[2]) | not_finite<BF>(w[3]);
                     }
                     if (bad) {
-                        B.bad[who - 1] = 1;
+                        const int t = (int)(d - 1) / 2;  // the tile whose values slot d holds
+                        atomicMin(&B.bad_from[who - 1], t);
+                        atomicMax(&B.bad_to[who - 1], t);
 #pragma unroll 1
                         for (int j = 0; j < 4 * (kKT / kRowStep); ++j) {
                             const uint32_t at = from + (j >> 2) * kRowStep * 128 + 4 * (j & 3);
@@ -849,15 +855,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __stcg(reinterpret_cast<float4 *>(dst) + i, v);
                 }
             }
-            if (B.bad[it]) {
+            if (B.bad_to[it] >= 0) {
                 // values that the copies took out of the tiles that not every row sees
                 // in full: added to the rows that see them
                 float *own = dst;
                 if (live) {
                     const int limit = row_limit(a, p, tok);
-                    int k0 = p.key0;
+                    const int t0 = (int)t - p.ntiles;  // the piece's first tile
 #pragma unroll 1
-                    for (int k = 0; k < p.ntiles; ++k, k0 += kKT) {
+                    for (int k = B.bad_from[it] - t0; k <= B.bad_to[it] - t0; ++k) {
+                        const int k0 = p.key0 + k * kKT;
                         const KeyRange kr = key_range(a, k0, limit);
                         if (key_range(a, k0, p.pos0 + 1).hi >= kr.key + kKT) continue;
                         const int *pages = kr.front ? a.prefix_pages
@@ -871,16 +878,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 v_cache + ((((int64_t)e * a.Hkv + p.head) << a.page_shift) +
                                            (key & ((1 << a.page_shift) - 1))) * D;
 #pragma unroll 1
-                            for (int c = 0; c < D; ++c) {
-                                const uint32_t x = v[c];
-                                if (not_finite<BF>(x))
-                                    __stcg(own + c, __ldcg(own + c) + widen16<BF>(x));
+                            for (int c = 0; c < D; c += 8) {
+                                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(v + c));
+                                if (!(not_finite<BF>(x.x) | not_finite<BF>(x.y) |
+                                      not_finite<BF>(x.z) | not_finite<BF>(x.w)))
+                                    continue;
+#pragma unroll 1
+                                for (int i = c; i < c + 8; ++i) {
+                                    const uint32_t y = v[i];
+                                    if (not_finite<BF>(y))
+                                        __stcg(own + i, __ldcg(own + i) + widen16<BF>(y));
+                                }
                             }
                         }
                     }
                 }
                 if (!group_sync()) break;
-                if (row == 0) B.bad[it] = 0;
+                if (row == 0) {
+                    B.bad_from[it] = 0x7fffffff;
+                    B.bad_to[it] = -1;
+                }
             }
             if (!whole) {
                 // this CTA's part of the item is out; whoever is last of a group, and
