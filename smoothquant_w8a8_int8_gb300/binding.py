@@ -171,7 +171,7 @@ class _on:
         self.dev, self.stream, self.held = t.device, stream, None
 
     def __enter__(self):
-        if self.stream is None and self.dev.index == torch.cuda.current_device():
+        if self.stream is None and self.dev.index == torch._C._cuda_getDevice():
             return torch._C._cuda_getCurrentRawStream(self.dev.index)
         if self.stream is not None and self.stream.device != self.dev:
             raise ValueError(f"the stream is on {self.stream.device}, the tensors on {self.dev}")
@@ -375,7 +375,7 @@ def rmsnorm_quant(H: torch.Tensor, gamma: torch.Tensor, eps: float, s: torch.Ten
             R = torch.empty_like(H) if (residual is not None if want_sum is None
                                         else want_sum) else None
             outs = [None if t is None else t.data_ptr() for t in (R, Y, Xq, sx, Xop, l1)]
-        _check(load().sq_rmsnorm_quant(
+        _check((_lib or load()).sq_rmsnorm_quant(
             H.data_ptr(), at(residual, f32, "residual", (M, K)), at(gamma, f32, "gamma", (K,)),
             float(eps), at(s, f32, "s", (K,)), M, K, float(static_scale), *outs, st),
             "sq_rmsnorm_quant")
@@ -472,7 +472,7 @@ def kv_append(QKV: torch.Tensor, Hq: int, k_cache: torch.Tensor, v_cache: torch.
         if q_out is None:
             q_out = torch.empty(T, Hq * D, dtype=f32, device=dev)
         ldq = _rows_of(q_out, Hq * D, "q_out", dev, T)
-        _check(load().sq_kv_append(qkv, T, Hq, Hkv, D, rope_at, positions, rot,
+        _check((_lib or load()).sq_kv_append(qkv, T, Hq, Hkv, D, rope_at, positions, rot,
                                    1 if interleaved else 0, starts, lens, B, table, width, k, v,
                                    ctype, pages, page_size, q_out.data_ptr(), ldq, st),
                "sq_kv_append")
@@ -524,7 +524,7 @@ def paged_attention(Q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         if workspace is None:
             workspace = empty_workspace(
                 paged_attention_workspace_bytes(T, Hq, Hkv, D, prefix_len), dev)
-        _check(load().sq_paged_attention(
+        _check((_lib or load()).sq_paged_attention(
             Q.data_ptr(), ldq, T, Hq, Hkv, D, k, v, ctype, pages, page_size, table, width, starts,
             lens, B, T if max_q is None else int(max_q), pages_at, int(prefix_len), float(scale),
             _arg(out, torch.float32, "out", (T, Hq * D), dev),
