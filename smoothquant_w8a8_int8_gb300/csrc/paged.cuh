@@ -21,6 +21,12 @@ __device__ __forceinline__ float max_factor(float a, float b) {
     return a == -INFINITY ? 0.0f : ex2(a - b);
 }
 
+// 2^e, e in [-126, 127]
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+// The multiple of 8 that scales numbers whose largest has the exponent e into
+// fp16's range, the largest into [2^8, 2^16); tiny and zero rows as if e = -32.
+__device__ __forceinline__ int shift_of(int e) { return (max(e, -32) - 8) & ~7; }
+
 // N pairs of 16-bit numbers of the cache's type that sum to (a, b), a in the
 // low half.  Three bf16 numbers hold an fp32 number exactly: each takes the
 // next 8 bits of its significand, by masking (the conversion instructions run
@@ -47,6 +53,12 @@ __device__ __forceinline__ void split16(float a, float b, uint32_t (&w)[N]) {
     }
 }
 
+// 16 bytes of global memory into shared memory, asynchronously, or zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
 __device__ __forceinline__ void lds4(uint32_t (&w)[4], uint32_t addr) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])

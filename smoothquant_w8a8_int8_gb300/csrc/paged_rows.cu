@@ -27,7 +27,7 @@
 //
 // Precision: keys and values enter as stored.  The fp32 queries and
 // probabilities are split over several 16-bit numbers (split16): two for fp16
-// (within 2^-22), three for bf16 (exact).
+// (within 2^-22 of a row's largest), three for bf16 (exact).
 // Up to 8 rows, two of the parts share an instruction's 16 rows (the first in
 // rows 0-7, the second in rows 8-15) and the two halves are added in fp32.
 #include "paged.cuh"
@@ -84,12 +84,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
-                 : "memory");
-}
-// 16 bytes of global memory, or zeros
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(there ? 16 : 0)
                  : "memory");
 }
 
@@ -238,6 +232,26 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         auto out_row = [&](int r) {
             return (int64_t)(p.tok0 + tok[r]) * a.Hq + p.head * a.G + (g + 8 * r) % a.G;
         };
+        // fp16 queries are scaled row by row by a power of two into fp16's range
+        float mul[R], scale[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mul[r] = a.sign;
+            scale[r] = a.scale;
+            if (BF) continue;
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const float2 q = live[r] ? *reinterpret_cast<const float2 *>(qrow[r] + 8 * i)
+                                         : make_float2(0.f, 0.f);
+                top = fmaxf(top, fmaxf(fabsf(q.x), fabsf(q.y)));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int sh = shift_of((int)(__float_as_uint(top) >> 23) - 127);
+            mul[r] *= pow2(-sh);
+            scale[r] *= pow2(sh);
+        }
         uint32_t qf[D / 16][S][4];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
@@ -249,8 +263,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     const float2 q =
                         live[r] ? *reinterpret_cast<const float2 *>(qrow[r] + 16 * i + 8 * h)
                                 : make_float2(0.f, 0.f);
-                    x[r][0] = q.x * a.sign;
-                    x[r][1] = q.y * a.sign;
+                    x[r][0] = q.x * mul[r];
+                    x[r][1] = q.y * mul[r];
                 }
                 F::fill(x, 2 * h, qf[i]);
             }
@@ -331,7 +345,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 float mx = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = mx == -INFINITY ? m[r] : fmaxf(m[r], mx * a.scale);
+                const float mn = mx == -INFINITY ? m[r] : fmaxf(m[r], mx * scale[r]);
                 any = any || mn > m[r];
                 grow[r] = mn > m[r] ? max_factor(m[r], mn) : 1.0f;
                 m[r] = mn;
@@ -400,7 +414,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[r][i] = x[r][i] == -INFINITY ? 0.0f : ex2(fmaf(x[r][i], a.scale, -m[r]));
+                    x[r][i] = x[r][i] == -INFINITY ? 0.0f : ex2(fmaf(x[r][i], scale[r], -m[r]));
                     l[r] += x[r][i];
                 }
 #pragma unroll

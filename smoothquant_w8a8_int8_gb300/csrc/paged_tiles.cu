@@ -249,17 +249,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
 __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(there ? 16 : 0)
-                 : "memory");
-}
-// 2^e, e in [-126, 127]
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
-// The multiple of 8 that scales numbers whose largest has the exponent e into
-// fp16's range, the largest into [2^8, 2^16); tiny and zero rows as if e = -32.
-__device__ __forceinline__ int shift_of(int e) { return (max(e, -32) - 8) & ~7; }
-
 template <int D, bool BF>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tiles_kernel(const __grid_constant__ PagedArgs a, const uint16_t *__restrict__ k_cache,

@@ -212,6 +212,18 @@ def test_values_that_are_not_finite_in_a_prefix_of_its_own(sq, tiles_per_sm, tai
     poisoned(sq, t, [(5, 99), (5, 60), (9, t.kv_lens[9] - 1)])
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("q", [[1, 3], [2, 40]])
+@pytest.mark.parametrize("spread,keys", [(2e-5, 2e4), (1e7, 1e-6), (3e-30, 1.0), (0.0, 1.0)])
+def test_large_and_small_queries(sq, spread, keys, q, dtype):
+    """Queries far from the range of the cache's type, keys that make logits of
+    order one or ten of them."""
+    t = Batch(q, [200, 333], 8, 2, 128, 32, dtype, seed=41, spread=spread)
+    # (4.5 deviations of 2e4 pass fp16's largest number, and infinite keys have no logits)
+    t.k = (t.k.float() * keys).clamp(-65504.0, 65504.0).to(dtype)
+    verify(sq, t.cuda())
+
+
 def test_many_sequences(sq):
     q = [1 + (i % 3 == 0) for i in range(300)]
     kv = [(37 * i) % 200 for i in range(300)]
