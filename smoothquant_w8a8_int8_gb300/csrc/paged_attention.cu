@@ -56,9 +56,10 @@ bool few_rows(int64_t tokens, int G) { return std::max<int64_t>(1, tokens) * G <
 // sequences fill two row tiles each and more, the prefix in front costs less than
 // its state's way through memory whatever its length (bf16, 64 sequences of 1 to
 // 257 tokens behind 1000 positions: 944 and 782 us, behind 8000: 2838 and 2792).
-bool prefix_in_front(const PagedArgs &a, int64_t max_q, int sms) {
+// tokens: what T, B and max_q leave possible (a padded batch has fewer than T).
+bool prefix_in_front(const PagedArgs &a, int64_t max_q, int64_t tokens, int sms) {
     const bool few = few_rows(max_q, a.G);
-    if (!few && (int64_t)a.T * a.G >= 256 * (int64_t)a.B) return true;
+    if (!few && tokens * a.G >= 256 * (int64_t)a.B) return true;
     const int64_t tiles = (int64_t)std::min(a.B, a.T) * a.Hkv * ((a.prefix_len + 127) / 128);
     return tiles <= (few ? 40 : 20) * (int64_t)sms;
 }
@@ -122,10 +123,12 @@ sq_status launch_paged_attention(const PagedCall &c, cudaStream_t st) {
     a.scale = std::max(fabsf(c.scale) * 1.4426950408889634f, 1e-30f);
     a.sign = c.scale < 0.0f ? -1.0f : 1.0f;
     const bool bf16 = c.cache_type == SQ_CACHE_BF16;
-    const bool front = c.prefix_len > 0 && prefix_in_front(a, std::min(c.max_q, c.T), di.sms);
+    const int64_t max_q = std::min(c.max_q, c.T), tokens = std::min(c.T, max_q * c.B);
+    const bool front = c.prefix_len > 0 && prefix_in_front(a, max_q, tokens, di.sms);
     for (int phase = c.prefix_len > 0 && !front ? 1 : 0; phase >= 0; --phase) {
         a.prefix_phase = phase;
-        const int64_t most = phase ? c.T : std::min(c.max_q, c.T);
+        a.after_prefix = !phase && c.prefix_len > 0 && !front;
+        const int64_t most = phase ? tokens : max_q;
         const bool few = few_rows(most, a.G);
         const int r = few ? (std::max<int64_t>(1, most) * a.G <= 8 ? 8 : 16) : 128;
         const int kt = few ? 16 : 128;

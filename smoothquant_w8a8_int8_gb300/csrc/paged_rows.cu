@@ -130,8 +130,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     __shared__ Share shares[kWarps];
     __shared__ Piece pieces[kWarps][kPieces];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    pdl_launch_dependents();
-    pdl_wait();  // every global-memory access below follows the previous kernel
+    begin_paged(a);
     find_shares<kKT, kPad, kWarps * 32, kWarps>(a, kMinSteps, shares);
     const Share &share = shares[warp];
     const int worker = warp * gridDim.x + blockIdx.x;
@@ -210,6 +209,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     };
 #pragma unroll 1
     for (int i = 0; i < ST - 1; ++i) copy_step();
+    end_of_prefix(a);
     __syncwarp();
 
     const int g = lane >> 2, t = lane & 3;  // fragment row and column pair
