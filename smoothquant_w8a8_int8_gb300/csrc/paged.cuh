@@ -83,20 +83,6 @@ __device__ __forceinline__ float widen16(uint32_t low) {
     return BF ? __uint_as_float(low << 16) : __half2float(__ushort_as_half((uint16_t)low));
 }
 
-// The order of launches.  The prefix's launch lets the next one start only when the
-// kernels before it are complete, so that the launch behind it need not wait for
-// them, but for the prefix's state and the workspace alone (end_of_prefix: called
-// before the first access to either, by the threads that make them); its first
-// copies are on their way meanwhile.
-__device__ __forceinline__ void begin_paged(const PagedArgs &a) {
-    if (!a.prefix_phase) pdl_launch_dependents();
-    if (!a.after_prefix) pdl_wait();  // the accesses below follow the previous kernel
-    if (a.prefix_phase) pdl_launch_dependents();
-}
-__device__ __forceinline__ void end_of_prefix(const PagedArgs &a) {
-    if (a.after_prefix) pdl_wait();
-}
-
 // The line's length and the shares of this block's W workers (worker w of block
 // c is number w gridDim.x + c, so that neighbours on the line are on different
 // SMs), by all NT threads: each sums a run of sequences, a scan over the

@@ -127,11 +127,11 @@ sq_status launch_paged_attention(const PagedCall &c, cudaStream_t st) {
     const bool front = c.prefix_len > 0 && prefix_in_front(a, max_q, tokens, di.sms);
     for (int phase = c.prefix_len > 0 && !front ? 1 : 0; phase >= 0; --phase) {
         a.prefix_phase = phase;
-        a.after_prefix = !phase && c.prefix_len > 0 && !front;
         const int64_t most = phase ? tokens : max_q;
         const bool few = few_rows(most, a.G);
         const int r = few ? (std::max<int64_t>(1, most) * a.G <= 8 ? 8 : 16) : 128;
         const int kt = few ? 16 : 128;
+        a.after_prefix = few && !phase && c.prefix_len > 0 && !front;
         a.tpt = r / a.G;
         a.kstart = phase ? 0 : a.prefix_len / kt * kt;
         a.front_tiles = front ? (a.prefix_len + kt - 1) / kt : 0;

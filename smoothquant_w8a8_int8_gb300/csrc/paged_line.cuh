@@ -50,7 +50,7 @@ struct PagedArgs {
     float scale;         // |scale| log2 e; the sign is folded into the queries
     float sign;
     int prefix_phase;    // 1: every token over the prefix, into prefix_o / prefix_ml
-    int after_prefix;    // 1: the launch behind that one (see begin_paged)
+    int after_prefix;    // 1: the few rows' launch behind that one (see begin_rows)
 };
 
 namespace {

@@ -301,7 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_before();
     __syncthreads();
     tc_after();
-    begin_paged(a);
+    pdl_wait();  // every global-memory access below follows the previous kernel
+    pdl_launch_dependents();  // (after it: see begin_rows)
     find_shares<kKT, C::kPad, kThreads, 1>(a, kMinTiles, &B.share);
     const uint32_t tmem = B.tmem;
 
@@ -752,7 +753,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         // -------------------------------------------------------- the output
-        end_of_prefix(a);
         const int w = warp & 3;
         const int row = 32 * w + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16) + C::kPV0;
