@@ -5,8 +5,9 @@ import torch
 
 U32 = 2.0 ** -24                                            # half a step of fp32
 HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}  # eps / 2, relative
-# what a number keeps as a pair of the type's numbers: two roundings in a row
-SPLIT = {torch.bfloat16: 2.0 ** -18, torch.float16: 2.0 ** -22}
+# what a number loses as a sum of the type's numbers: two roundings in a row for
+# fp16; three bf16 numbers hold an fp32 number's 24 bits
+SPLIT = {torch.bfloat16: 0.0, torch.float16: 2.0 ** -22}
 
 
 class Batch:
@@ -70,10 +71,10 @@ def attention_ref(t: Batch, scale):
 
     The bound, per output: a logit is off by at most
       d = |scale| sum |q k| (SPLIT + 2^-20) + 2^-22 |logit|
-    (the pair that stands for q; products summed in fp32 in at most a dozen
+    (the numbers that stand for q; products summed in fp32 in at most a dozen
     steps of a tensor-core instruction, each within 2^-23 of the partial sum;
     the product with log2 e), so a probability by a factor 1 + 2 d (its own and
-    the largest's), to which the exponential adds 2^-22 and its own pair SPLIT.
+    the largest's), to which the exponential adds 2^-22 and its own SPLIT.
     Numerator and denominator are sums over L keys in at most L / 16 + 32 steps
     (tiles, warps, pieces), each within 2^-23 of sum p |v| <= max |v| sum p."""
     O = torch.full((t.T, t.Hq, t.D), float("nan"), dtype=torch.float64)
