@@ -277,10 +277,10 @@ sq_status sq_kv_append(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv, int
  * kernel only, results do not depend on it but for rounding.
  * Queries and probabilities enter the tensor cores as sums of 16-bit numbers of
  * the cache's type, three for bf16 (exact) and two for fp16 (within 2^-22, or
- * 2^-32 of the row's largest element), and products are summed in fp32, as are the
- * softmax's maxima and sums: O agrees with the exact attention over the stored rows
- * as far as fp32 logits and sums do, to a few 2^-21 of max |V| where logits are of
- * order one.
+ * 2^-32 of the row's largest element, or 2^-65), and products are summed in fp32,
+ * as are the softmax's maxima and sums: O agrees with the exact attention over the
+ * stored rows as far as fp32 logits and sums do, to a few 2^-21 of max |V| where
+ * logits are of order one.
  * Results are the same bits from call to call.
  * workspace (16-byte aligned, zero-filled once before its first use): at least
  * sq_paged_attention_workspace_bytes bytes; it serves one call at a time, on

@@ -24,8 +24,9 @@ __device__ __forceinline__ float max_factor(float a, float b) {
 // 2^e, e in [-126, 127]
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 // The multiple of 8 that scales numbers whose largest has the exponent e into
-// fp16's range, the largest into [2^8, 2^16); tiny and zero rows as if e = -32.
-__device__ __forceinline__ int shift_of(int e) { return (max(e, -32) - 8) & ~7; }
+// fp16's range, the largest into [2^7, 2^15) (fp16 ends at 65504, so the octave
+// below 2^16 would round to infinity at its end); tiny and zero rows as if e = -32.
+__device__ __forceinline__ int shift_of(int e) { return (max(e, -32) - 7) & ~7; }
 
 // N pairs of 16-bit numbers of the cache's type that sum to (a, b), a in the
 // low half.  Three bf16 numbers hold an fp32 number exactly: each takes the
