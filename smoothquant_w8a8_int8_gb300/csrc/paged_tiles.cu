@@ -636,11 +636,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  : "memory");
                     float mul = a.sign;
                     if (!BF) {
-                        // (the rows of a step have one factor)
+                        // (over the row's own lanes: a step may hold two rows, and what
+                        // one of them holds must not cost the other its bits)
                         const float top = fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)),
                                                 fmaxf(fabsf(q.z), fabsf(q.w)));
+                        const unsigned row_lanes =
+                            LPR == 32 ? 0xffffffffu : 0xffffu << (lane & 16);
                         const unsigned e =
-                            __reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23;
+                            __reduce_max_sync(row_lanes, __float_as_uint(top)) >> 23;
                         const int sh = shift_of((int)e - 127);
                         mul *= pow2(-sh);
                         if (c4 == 0) B.qmul[n & 1][16 * warp + i + sub] = pow2(sh);

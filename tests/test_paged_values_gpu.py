@@ -5,8 +5,8 @@ pagedlib.attention_ref's where no other is derived."""
 import pytest
 import torch
 
-from pagedlib import Batch
-from test_paged_attention_gpu import verify
+from pagedlib import Batch, attention_ref
+from test_paged_attention_gpu import call, many_behind, verify
 
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float16
@@ -36,4 +36,60 @@ def test_largest_element_at_an_octaves_end(sq, top, q, D, dtype):
     rows[at, at % D] = torch.where(at % 2 == 0, 1.0, -1.0) * (1 - 2.0 ** -24)
     rows.mul_(top)
     t.k = (t.k.float() * (3 / top)).clamp(-65504.0, 65504.0).to(dtype)
+    verify(sq, t.cuda())
+
+
+def uneven(t, factors):
+    """Multiplies the rows (tokens x heads of a group) by `factors` in turn.  Rows of
+    2^-13, and keys that make their logits of order one: `factors` of 1 lose their
+    bits if a larger row's range is taken for theirs."""
+    tok, head = torch.meshgrid(torch.arange(t.T), torch.arange(t.Hq), indexing="ij")
+    f = torch.tensor(factors)[(tok * t.G + head % t.G) % len(factors)] * 2.0 ** -13
+    t.Q.view(t.T, t.Hq, t.D).mul_(f[..., None])
+    t.k = (t.k.float() * 2.0 ** 13).clamp(-65504.0, 65504.0).to(t.dtype)
+    return t
+
+
+@pytest.mark.parametrize("D,dtype", [(64, FP), (128, FP), (64, BF)])
+@pytest.mark.parametrize("q,Hq,Hkv", [([1, 3], 8, 2), ([1, 1], 4, 4), ([2, 40], 8, 2),
+                                      ([60, 21], 4, 4)])
+@pytest.mark.parametrize("factor", [2.0 ** 12, 2.0 ** 20])
+def test_rows_of_different_size_side_by_side(sq, factor, q, Hq, Hkv, D, dtype):
+    verify(sq, uneven(Batch(q, [150, 333], Hq, Hkv, D, 32, dtype, seed=sum(q)),
+                      [1.0, factor, factor, 1.0, 1.0]).cuda())
+
+
+def beside(sq, t, value):
+    """Every third row's queries hold `value` where the keys hold zeros; the others'
+    outputs are those of the definition."""
+    t.k[..., 7] = 0
+    ref, bound = attention_ref(t, t.D ** -0.5)
+    rows = t.Q.view(t.T, t.Hq, t.D)
+    tok, head = torch.meshgrid(torch.arange(t.T), torch.arange(t.Hq), indexing="ij")
+    bad = (tok * t.G + head % t.G) % 3 == 1
+    rows[..., 7][bad] = value
+    t.cuda()
+    got = call(sq, t).double().cpu().view(t.T, t.Hq, t.D)
+    assert sq.device_status() == sq.SQ_OK
+    ref, bound = ref.view_as(got), bound.view_as(got)
+    good = ~bad[..., None] & ~torch.isnan(ref)
+    assert good.any() and torch.isfinite(got[good]).all()
+    assert float(((got - ref).abs() - bound)[good].max()) <= 0
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan"), 2.0 ** 40])
+@pytest.mark.parametrize("D,dtype", [(64, FP), (128, FP), (64, BF)])
+@pytest.mark.parametrize("q,Hq,Hkv", [([1, 3], 8, 2), ([2, 40], 8, 2), ([60, 21], 4, 4)])
+def test_a_query_beyond_the_others_stays_in_its_row(sq, q, Hq, Hkv, D, dtype, value):
+    beside(sq, Batch(q, [150, 333], Hq, Hkv, D, 32, dtype, seed=sum(q)), value)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 2.0 ** 40])
+@pytest.mark.parametrize("D,dtype", [(64, FP), (128, FP)])
+def test_sequences_behind_one_prefix_keep_their_queries(sq, D, dtype, value):
+    """The rows of a tile of the prefix's own launch are those of many sequences."""
+    kw = dict(Hq=4, D=D, page=64, dtype=dtype, seed=9)
+    beside(sq, many_behind(3000, 40, 4, [], **kw), value)
+    kw["seed"] = 10
+    t = uneven(many_behind(3000, 40, 4, [], **kw), [1.0, 2.0 ** 20, 1.0, 1.0])
     verify(sq, t.cuda())
