@@ -640,10 +640,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // one of them holds must not cost the other its bits)
                         const float top = fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)),
                                                 fmaxf(fabsf(q.z), fabsf(q.w)));
-                        const unsigned row_lanes =
-                            LPR == 32 ? 0xffffffffu : 0xffffu << (lane & 16);
-                        const unsigned e =
-                            __reduce_max_sync(row_lanes, __float_as_uint(top)) >> 23;
+                        unsigned e = __float_as_uint(top);
+                        if (LPR == 32) {
+                            e = __reduce_max_sync(0xffffffffu, e);
+                        } else {
+#pragma unroll
+                            for (int o = LPR / 2; o > 0; o >>= 1)
+                                e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
+                        }
+                        e >>= 23;
                         const int sh = shift_of((int)e - 127);
                         mul *= pow2(-sh);
                         if (c4 == 0) B.qmul[n & 1][16 * warp + i + sub] = pow2(sh);
