@@ -27,7 +27,10 @@
 //
 // Precision: keys and values enter as stored.  The fp32 queries and
 // probabilities are split over several 16-bit numbers (split16): two for fp16
-// (within 2^-22 of a row's largest), three for bf16 (exact).
+// (within 2^-22, or 2^-32 of a row's largest), three for bf16 (exact).  Fp16's
+// probabilities carry a factor 2^12: its smallest step is 2^-24, and without it a
+// key of less than 2^-25 of the largest's weight would count in the sum alone (8192
+// of 2^-25 behind one of 1: 2.3e-4 of the output, all of what they say).
 // Up to 8 rows, two of the parts share an instruction's 16 rows (the first in
 // rows 0-7, the second in rows 8-15) and the two halves are added in fp32.
 #include "paged.cuh"
@@ -49,6 +52,8 @@ constexpr int kMinSteps = 4;
 // for one key/value head's 100,000 keys
 constexpr int kJoin = 16;
 constexpr int kPieces = 8;    // more than the steps that the copies are ahead
+
+constexpr float kUp = 4096.0f;  // fp16 probabilities' factor
 
 template <int D>
 struct RowsCfg {
@@ -437,8 +442,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 float y[R][2];
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    y[r][0] = x[r][2 * h];
-                    y[r][1] = x[r][2 * h + 1];
+                    y[r][0] = BF ? x[r][2 * h] : x[r][2 * h] * kUp;
+                    y[r][1] = BF ? x[r][2 * h + 1] : x[r][2 * h + 1] * kUp;
                 }
                 F::fill(y, 2 * h, pf);
             }
@@ -461,11 +466,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
+                            constexpr float kDown = BF ? 1.0f : 1.0f / kUp;
+                            float &o0 = o[2 * i + j][q], &o1 = o[2 * i + j][2 * R - 2 + q];
                             if (R == 1) {
-                                o[2 * i + j][q] += c[j][q] + c[j][2 + q];
+                                o0 = fmaf(c[j][q] + c[j][2 + q], kDown, o0);
                             } else {
-                                o[2 * i + j][q] += c[j][q];
-                                o[2 * i + j][2 * R - 2 + q] += c[j][2 + q];
+                                o0 = fmaf(c[j][q], kDown, o0);
+                                o1 = fmaf(c[j][2 + q], kDown, o1);
                             }
                         }
                 }

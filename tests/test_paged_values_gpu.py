@@ -5,7 +5,7 @@ pagedlib.attention_ref's where no other is derived."""
 import pytest
 import torch
 
-from pagedlib import Batch, attention_ref
+from pagedlib import SPLIT, Batch, attention_ref
 from test_paged_attention_gpu import call, many_behind, verify
 
 pytestmark = pytest.mark.gpu
@@ -93,3 +93,72 @@ def test_sequences_behind_one_prefix_keep_their_queries(sq, D, dtype, value):
     kw["seed"] = 10
     t = uneven(many_behind(3000, 40, 4, [], **kw), [1.0, 2.0 ** 20, 1.0, 1.0])
     verify(sq, t.cuda())
+
+
+def sink_batch(q, L, Hq, Hkv, D, dtype, logit, sink, prefix=0, seqs=1):
+    """`seqs` sequences of L cached tokens (the first `prefix` shared) and q new
+    tokens each.  Position `sink` has the logit `logit` in every row, every other
+    position 0; values are of one sign, and the sink's are 0 in the first half of
+    the columns."""
+    page = 64
+    g = torch.Generator().manual_seed(L + q)
+    first, pages = prefix // page, -(-L // page)
+    own = pages - first
+    shared = -(-prefix // page)
+    n = shared + seqs * own
+    k = torch.zeros(n, Hkv, page, D).to(dtype)
+    v = torch.rand(n, Hkv, page, D, generator=g).to(dtype)
+    table = torch.full((seqs, pages), -1, dtype=torch.int32)
+    for b in range(seqs):
+        table[b, first:] = shared + b * own + torch.arange(own)
+    where = [(sink // page if sink < prefix else int(table[b, sink // page])) for b in range(seqs)]
+    for e in set(where):
+        k[e, :, sink % page, 3] = 1.0
+        v[e, :, sink % page, :D // 2] = 0.0
+    Q = torch.zeros(seqs * q, Hq, D)
+    Q[..., 3] = logit
+    ints = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    return dict(Q=Q.view(seqs * q, -1).cuda(), k_cache=k.cuda(), v_cache=v.cuda(),
+                block_table=table.cuda(), q_start=ints([q * b for b in range(seqs + 1)]),
+                kv_len=ints([L] * seqs), max_q=q,
+                prefix_pages=torch.arange(shared, dtype=torch.int32).cuda(), prefix_len=prefix)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q,L,prefix,seqs", [
+    (1, 8192, 0, 1), (1, 100000, 0, 1), (4, 3000, 0, 2),     # few rows
+    (40, 8192, 0, 1), (40, 50000, 0, 1),                     # many rows
+    (1, 9000, 8192, 2), (40, 3000, 2000, 2),                 # the prefix in front
+    (1, 40200, 40000, 12), (1, 100200, 100000, 4),           # and in a launch of its own
+])
+@pytest.mark.parametrize("logit", [16.0, 17.4])
+@pytest.mark.parametrize("late", [False, True])
+def test_one_key_of_most_weight(sq, q, L, prefix, seqs, D, dtype, logit, late):
+    """The others' weights are 2^-23 to 2^-25 of its own, and count together.
+    All terms are of one sign, so the error is relative: a weight by 2 d, d =
+    2^-22 |logit| (attention_ref's, products exact), by 2^-22 for the exponential
+    and by SPLIT; numerator and denominator in L / 16 + 32 steps of 2^-23; and
+    2^-37 of the largest weight for each key, half of fp16's smallest step under
+    the factor 2^12 that the probabilities carry."""
+    Hq, Hkv = 8, 2
+    sink = L - q if late else 5
+    c = sink_batch(q, L, Hq, Hkv, D, dtype, logit, sink, prefix, seqs)
+    got = sq.paged_attention(scale=1.0, **c).double().cpu().view(seqs, q, Hq, D)
+    assert sq.device_status() == sq.SQ_OK
+    w = torch.ones(L, dtype=torch.float64)
+    w[sink] = torch.tensor(logit, dtype=torch.float32).double().exp()
+    rel = 2 * (2 * 2.0 ** -22 * logit + 2.0 ** -22 + SPLIT[dtype] + (L / 16 + 32) * 2.0 ** -23)
+    table = c["block_table"].cpu().long()
+    table[:, :prefix // 64] = torch.arange(prefix // 64)
+    pos = torch.arange(L)
+    for b in range(seqs):
+        pages = table[b, pos // 64]
+        pages[pos < prefix] = pos[pos < prefix] // 64
+        v = c["v_cache"].cpu()[pages, :, pos % 64].double()      # [L, Hkv, D]
+        for i in range(q):
+            n = L - q + i + 1
+            total = torch.einsum("k,khd->hd", w[:n], v[:n]) / w[:n].sum()
+            want = total.repeat_interleave(Hq // Hkv, 0)
+            floor = 0.0 if dtype == BF else n * 2.0 ** -37
+            assert ((got[b, i] - want).abs() <= want * rel + floor).all()
