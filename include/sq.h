@@ -210,7 +210,8 @@ sq_status sq_rmsnorm_quant(const float *H, const float *residual, const float *g
  * and for a batch of B sequences (device arrays, int32, 4-byte aligned):
  *   q_start [B + 1]    sequence b's tokens are rows q_start[b] .. q_start[b+1]-1
  *                      of this call's T rows (non-decreasing; rows outside every
- *                      sequence are neither read nor written),
+ *                      sequence are neither read nor written; what the rows hold
+ *                      where it decreases is not specified),
  *   kv_len [B]         its cached tokens, this call's included, so that its
  *                      i-th token stands at position kv_len[b] - q_len[b] + i,
  *   block_table [B][max_pages]  the page of positions page_size n ..

@@ -14,7 +14,8 @@
 // unnormalised output) per worker in the workspace; the one that arrives last
 // (a counter) joins them in the order of the line, so that the result does not
 // depend on who is last.  The line is shorter than 2^31 pairs (checked on the
-// host for the longest that the sizes allow).
+// host for the longest that the sizes allow), but for sequences that overlap: see
+// add_pairs.
 #pragma once
 #include <cuda_runtime.h>
 #include <cmath>
@@ -70,8 +71,8 @@ SQ_HD int at_least(int a, int b) { return a > b ? a : b; }
 struct Seq {
     int q0, qlen, kv;  // first token, tokens, keys after the append
 };
-// The device arrays are taken as they come: offsets clamped into [0, T] and
-// made non-decreasing, lengths into [0, cap].
+// The device arrays are taken as they come: offsets clamped into [0, T], a
+// sequence's end to its start at least, lengths into [0, cap].
 SQ_HD Seq load_seq(const PagedArgs &a, int b) {
     Seq s;
     const int e = a.prefix_phase ? a.B : b + 1;
@@ -133,6 +134,18 @@ SQ_HD int pairs_before(const PagedArgs &a, const Seq &s, int J) {
     if (J > whole && J > 0) sum += key_tiles<KT>(a, s, J - 1);
     return sum;
 }
+
+// The line's length is summed with this.  Where q_start is non-decreasing the
+// sequences hold T tokens in all, and the host has checked the longest line of
+// theirs.  Where it is not, they overlap, B of them with T tokens each at most: one
+// sequence's pairs still fit, but the sum may be anything, so it stops at
+// kTooLong, and such a line is not worked on.  (x and y are not negative.)
+constexpr int kTooLong = 0x7fffffff;
+SQ_HD int add_pairs(int x, int y) {
+    const uint32_t sum = (uint32_t)x + (uint32_t)y;
+    return sum < (uint32_t)kTooLong ? (int)sum : kTooLong;
+}
+SQ_HD int line_length(int sum) { return sum == kTooLong ? 0 : sum; }
 
 // Where a worker's share starts.
 struct Share {
