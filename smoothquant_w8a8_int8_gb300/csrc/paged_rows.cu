@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 float mx = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = mx == -INFINITY ? m[r] : fmaxf(m[r], mx * scale[r]);
+                const float mn =
+                    mx == -INFINITY ? m[r] : fmaxf(m[r], __fmul_rn(mx, scale[r]));
                 any = any || mn > m[r];
                 grow[r] = mn > m[r] ? max_factor(m[r], mn) : 1.0f;
                 m[r] = mn;
@@ -430,11 +431,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 }
             }
             uint32_t pf[S][4];
+            // (far from zero, what is subtracted from the maximum is rounded as it is)
+            const bool far = __any_sync(0xffffffffu, is_far(m[0]) || is_far(m[R - 1]));
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[r][i] = x[r][i] == -INFINITY ? 0.0f : ex2(fmaf(x[r][i], scale[r], -m[r]));
+                    float e = fmaf(x[r][i], scale[r], -m[r]);
+                    if (far) e = __fsub_rn(__fmul_rn(x[r][i], scale[r]), m[r]);
+                    x[r][i] = x[r][i] == -INFINITY ? 0.0f : ex2(e);
                     l[r] += x[r][i];
                 }
 #pragma unroll

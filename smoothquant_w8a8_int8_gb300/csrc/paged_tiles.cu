@@ -719,8 +719,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 mx = fmaxf(mx, B.half_max[t & 1][1 - g][r]);
-                const float m = mx == -INFINITY ? 0.0f : fmaf(mx, c, -kBias);
-                const unsigned long long c2 = pk(c, c), m2 = pk(-m, -m);
+                float m = mx == -INFINITY ? 0.0f : fmaf(mx, c, -kBias);
+                float mul = c, sub = m;
+                if (is_far(m)) {
+                    // a power of two in c's place: the products are exact, and the
+                    // largest key's probability is 1
+                    mul = __uint_as_float(__float_as_uint(c) & 0xff800000u);
+                    sub = mx * mul;
+                    m = mx * c;
+                }
+                const unsigned long long c2 = pk(mul, mul), m2 = pk(-sub, -sub);
                 unsigned long long sum2 = 0;
                 // per 16 keys 8 columns of each part
 #pragma unroll

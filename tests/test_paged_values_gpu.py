@@ -162,3 +162,43 @@ def test_one_key_of_most_weight(sq, q, L, prefix, seqs, D, dtype, logit, late):
             want = total.repeat_interleave(Hq // Hkv, 0)
             floor = 0.0 if dtype == BF else n * 2.0 ** -37
             assert ((got[b, i] - want).abs() <= want * rel + floor).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q,prefix", [(FEW, 0), (MANY, 0), (FEW, 150), (MANY, 150),
+                                      ([5, 2], 0), ([6], 0)])
+@pytest.mark.parametrize("size", [2.0 ** 18, 2.0 ** 22, 2.0 ** 26, 2.0 ** 31, 2.0 ** 40, -2.0 ** 40,
+                                  2.0 ** 100])
+def test_logits_far_from_one(sq, size, q, prefix, D, dtype):
+    """One element of the queries is `size`, the keys' is one of -1, -7/8 ... 7/8:
+    logits are whole multiples of size / 64, exact in every format, so a row's
+    output is the mean of its values at the largest: within SPLIT, the exponential's
+    2^-22, the rounding of log2 e in those weights' common factor (none: they are
+    equal) and n / 16 + 32 steps of 2^-23 of the largest value, as attention_ref."""
+    kv = [200, 533, 3000][:len(q)] if len(q) > 1 else [3000]   # the last: many pieces
+    t = Batch(q, kv, 8, 2, D, 32, dtype, prefix=prefix, seed=sum(q) + D)
+    g = torch.Generator().manual_seed(1)
+    t.Q.view(t.T, t.Hq, t.D)[:] = 0
+    t.Q.view(t.T, t.Hq, t.D)[..., 5] = size
+    t.k[:] = 0
+    t.k[..., 5] = torch.randint(-8, 8, t.k.shape[:-1], generator=g).to(dtype) / 8
+    t.cuda()
+    got = call(sq, t, scale=0.125).double().cpu().view(t.T, t.Hq, t.D)
+    assert sq.device_status() == sq.SQ_OK
+    row = 0
+    for b, (n, length) in enumerate(zip(t.q_lens, t.kv_lens)):
+        where = [t.row(b, p) for p in range(length)]
+        K = torch.stack([t.k[e, :, r, 5] for e, r in where]).double()   # [length, Hkv]
+        V = torch.stack([t.v[e, :, r] for e, r in where]).double()
+        for i in range(n):
+            seen = length - n + i + 1
+            x = K[:seen] * (1 if size > 0 else -1)
+            top = (x == x.max(0).values).double()
+            want = torch.einsum("kh,khd->hd", top, V[:seen]) / top.sum(0)[:, None]
+            want = want.repeat_interleave(t.G, 0)
+            bound = V[:seen].abs().max() * (2 * SPLIT[dtype] + 2.0 ** -20
+                                            + 2 * (seen / 16 + 32) * 2.0 ** -23)
+            assert torch.isfinite(got[row]).all()
+            assert ((got[row] - want).abs() <= bound).all()
+            row += 1
