@@ -449,7 +449,7 @@ sq_status sq_paged_attention(const float *Q, int64_t ldq, int64_t T, int64_t Hq,
     sq_status rc = check_paged_shape(T, Hq, Hkv, D, cache_type, num_pages, page_size, B,
                                      max_pages, ldq);
     if (rc != SQ_OK) return rc;
-    if (!(scale == scale) || !(fabsf(scale) <= 3.4028234663852886e38f)) return SQ_ERR_INVALID_ARG;
+    if (!(fabsf(scale) <= 0x1p127f)) return SQ_ERR_INVALID_ARG;  // (times log2 e it is finite)
     if (max_q < 0 || prefix_len < 0) return SQ_ERR_INVALID_ARG;
     if (prefix_len > (int64_t)1 << 30) return SQ_ERR_UNSUPPORTED;
     if (T == 0 || B == 0) return SQ_OK;

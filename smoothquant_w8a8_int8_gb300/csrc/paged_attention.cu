@@ -119,9 +119,11 @@ sq_status launch_paged_attention(const PagedCall &c, cudaStream_t st) {
                    : c.page_size == 128 ? 7 : 8;
     a.prefix_len = (int)c.prefix_len;
     a.cap = (int)(c.max_pages * c.page_size);
-    // (not zero: a masked logit's -inf stays -inf under it)
-    a.scale = std::max(fabsf(c.scale) * 1.4426950408889634f, 1e-30f);
-    a.sign = c.scale < 0.0f ? -1.0f : 1.0f;
+    // Not zero, so that a masked logit's -inf stays -inf under it, and large enough for
+    // the factors of fp16 rows.  A scale below that is zero: no query counts.
+    const float scale = fabsf(c.scale) * 1.4426950408889634f;
+    a.scale = std::max(scale, 0x1p-100f);
+    a.sign = scale < 0x1p-100f ? 0.0f : c.scale < 0.0f ? -1.0f : 1.0f;
     const bool bf16 = c.cache_type == SQ_CACHE_BF16;
     const int64_t max_q = std::min(c.max_q, c.T), tokens = std::min(c.T, max_q * c.B);
     const bool front = c.prefix_len > 0 && prefix_in_front(a, max_q, tokens, di.sms);

@@ -202,3 +202,19 @@ def test_logits_far_from_one(sq, size, q, prefix, D, dtype):
             assert torch.isfinite(got[row]).all()
             assert ((got[row] - want).abs() <= bound).all()
             row += 1
+
+
+@pytest.mark.parametrize("q", [FEW, MANY])
+@pytest.mark.parametrize("dtype,scale,size,keys", [
+    (BF, 0.0, 2.0 ** 60, 2.0 ** 50), (FP, 0.0, 2.0 ** 100, 2.0 ** 12),   # equal weights
+    (BF, 2.0 ** -110, 2.0 ** 30, 2.0 ** 30), (FP, -2.0 ** -140, 2.0 ** 40, 2.0 ** 10),
+    (BF, 2.0 ** 90, 2.0 ** -45, 2.0 ** -45), (BF, -2.0 ** 127, 0.0, 1.0),
+    (FP, 2.0 ** 30, 2.0 ** -20, 2.0 ** -12), (FP, 2.0 ** 127, 0.0, 1.0),
+    (BF, 2.0 ** -90, 2.0 ** 50, 2.0 ** 38), (FP, 2.0 ** -90, 2.0 ** 80, 2.0 ** 8),
+])
+def test_scales_of_any_size(sq, dtype, scale, size, keys, q):
+    """Queries and keys so that the logits are of order one, or zero."""
+    t = Batch(q, [200, 333], 8, 2, 128, 32, dtype, seed=43, spread=size)
+    t.k = (t.k.float() * keys).clamp(-2.0 ** 127 if dtype == BF else -65504.0,
+                                     2.0 ** 127 if dtype == BF else 65504.0).to(dtype)
+    verify(sq, t.cuda(), scale=scale)
