@@ -453,7 +453,9 @@ def kv_append(QKV: torch.Tensor, Hq: int, k_cache: torch.Tensor, v_cache: torch.
     """Rotates the queries and keys of the fused projection's output QKV
     [T, (Hq + 2 Hkv) * D] and appends keys and values to the paged cache;
     returns the rotated queries [T, Hq * D].  rope: rope_table's [positions, n,
-    2], None for no rotation.  q_out may be the view QKV[:, :Hq * D] (in place)."""
+    2], None for no rotation.  q_out may be the view QKV[:, :Hq * D] (in place).
+    With q_out, rows of no sequence are left as they are; without it they are
+    zeros."""
     (ctype, pages, Hkv, page_size, D, B, width), (k, v, table, starts, lens) = _need_paged(
         k_cache, v_cache, block_table, q_start, kv_len)
     dev, f32 = k_cache.device, torch.float32
@@ -470,7 +472,7 @@ def kv_append(QKV: torch.Tensor, Hq: int, k_cache: torch.Tensor, v_cache: torch.
         positions, rot = rope.shape[0], 2 * rope.shape[1]
     with _on(QKV, stream) as st:
         if q_out is None:
-            q_out = torch.empty(T, Hq * D, dtype=f32, device=dev)
+            q_out = torch.zeros(T, Hq * D, dtype=f32, device=dev)
         ldq = _rows_of(q_out, Hq * D, "q_out", dev, T)
         _check((_lib or load()).sq_kv_append(qkv, T, Hq, Hkv, D, rope_at, positions, rot,
                                    1 if interleaved else 0, starts, lens, B, table, width, k, v,
