@@ -272,7 +272,9 @@ sq_status sq_kv_append(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv, int
  * than kv_len[b]) gets zeros.  Keys whose page entry is outside [0, num_pages)
  * are left out, as if masked; kv_len is taken as at most max_pages * page_size,
  * and cache rows at or behind kv_len are not used, whatever they hold; nor do keys
- * and values of positions behind a token's own reach its row, finite or not.
+ * and values of positions behind a token's own reach its row, finite or not.  A value
+ * that is not finite leaves its column of the rows that see it not finite; an
+ * infinity may come out as NaN (its product with a probability's smaller parts).
  * scale: of either sign, 2^127 at most; below 2^-101 it counts as 0 (each key that a
  * row sees has the same weight).
  * Q fp32, rows of ldq floats (ldq >= Hq D, a multiple of 4); O fp32 [T][Hq D],

@@ -430,7 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // A masked key's probability is zero, but its value need not be
                 // finite, and zero times that is NaN: in tiles of which a row does not
                 // see every key such values are taken out here (each thread its own
-                // copies) and left to the item's end.
+                // copies) and left to the item's end.  (In the other tiles they stay in
+                // the product: every row sees them, and none of its sum is finite.)
                 for (uint32_t d = done; d < seq - (all ? 0 : 1); ++d) {
                     const int s4 = 4 * (d % NS);
                     const uint32_t who = scan >> s4 & 15u;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from pagedlib import SPLIT, Batch, attention_ref
-from test_paged_attention_gpu import call, many_behind, verify
+from test_paged_attention_gpu import call, many_behind, poisoned, verify
 
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float16
@@ -218,3 +218,13 @@ def test_scales_of_any_size(sq, dtype, scale, size, keys, q):
     t.k = (t.k.float() * keys).clamp(-2.0 ** 127 if dtype == BF else -65504.0,
                                      2.0 ** 127 if dtype == BF else 65504.0).to(dtype)
     verify(sq, t.cuda(), scale=scale)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, BF), (128, FP)])
+@pytest.mark.parametrize("q,kv,prefix,places", [
+    ([1, 3], [900, 700], 0, [(0, 3), (1, 40)]), ([40, 9], [900, 700], 0, [(0, 3), (1, 200)]),
+    ([1, 1], [900, 700], 300, [(0, 2), (1, 400)]), ([40, 9], [900, 700], 300, [(0, 2), (1, 400)]),
+])
+def test_values_that_are_not_finite_and_seen_by_every_row(sq, q, kv, prefix, places, D, dtype):
+    """Tiles without a mask: every row that sees them is not finite in their columns."""
+    poisoned(sq, Batch(q, kv, 8, 2, D, 32, dtype, prefix=prefix, seed=51), places)
