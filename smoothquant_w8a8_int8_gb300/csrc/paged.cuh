@@ -21,12 +21,12 @@ __device__ __forceinline__ float max_factor(float a, float b) {
     return a == -INFINITY ? 0.0f : ex2(a - b);
 }
 
-// Whether a row maximum m = RN(x c) (log2 units) is so large that its own rounding
-// counts in x c - m: at most 2 below 2^26, then 4 and more, with which the largest
-// key's probability 2^(x c - m), under the factor 2^12, would leave fp16's range, and
-// from 2^32 on that of fp32.  Two logits of such a row that are not equal differ by
-// 2 at least, so its probabilities may be formed otherwise: see the kernels.
-__device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= 0x1p26f; }
+// The smaller one; NaN if either is
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
 
 // 2^e, e in [-126, 127]
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }

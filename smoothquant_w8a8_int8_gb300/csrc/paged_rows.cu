@@ -365,8 +365,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 float mx = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                // rounded down: see below
                 const float mn =
-                    mx == -INFINITY ? m[r] : fmaxf(m[r], __fmul_rn(mx, scale[r]));
+                    mx == -INFINITY ? m[r] : fmaxf(m[r], __fmul_rd(mx, scale[r]));
                 any = any || mn > m[r];
                 grow[r] = mn > m[r] ? max_factor(m[r], mn) : 1.0f;
                 m[r] = mn;
@@ -431,17 +432,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 }
             }
             uint32_t pf[S][4];
-            // (far from zero, what is subtracted from the maximum is rounded as it is)
-            const bool far = __any_sync(0xffffffffu, is_far(m[0]) || is_far(m[R - 1]));
+            // The exponents are formed with one rounding; the largest logit's is what
+            // its maximum lost in its own: nothing that counts below 2^23, and no more
+            // than 1 here above that, where the logits themselves are as coarse.
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+            for (int r = 0; r < R; ++r) {
+                const float from = m[r] == -INFINITY ? 0.0f : -m[r];  // (no key yet)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float e = fmaf(x[r][i], scale[r], -m[r]);
-                    if (far) e = __fsub_rn(__fmul_rn(x[r][i], scale[r]), m[r]);
-                    x[r][i] = x[r][i] == -INFINITY ? 0.0f : ex2(e);
+                    x[r][i] = ex2(min_nan(fmaf(x[r][i], scale[r], from), 1.0f));
                     l[r] += x[r][i];
                 }
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float y[R][2];

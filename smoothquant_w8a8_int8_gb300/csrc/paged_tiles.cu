@@ -131,6 +131,13 @@ constexpr int kJoin = 6;
 constexpr int kMinTiles = 4;
 constexpr float kBias = 12.0f;  // log2 of the probabilities' factor
 
+// Whether a row maximum m of x c (log2 units) is so large that its own rounding
+// counts in x c - m: at most 2 below 2^26, then 4 and more, with which the largest
+// key's probability 2^(x c - m), under its factor, would leave fp16's range, and
+// from 2^32 on that of fp32.  Two logits of such a row that are not equal differ by
+// 2 at least.
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= 0x1p26f; }
+
 template <int D, bool BF>
 struct TilesCfg {
     static constexpr int kParts = BF ? 3 : 2;
@@ -727,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // largest key's probability is 1
                     mul = __uint_as_float(__float_as_uint(c) & 0xff800000u);
                     sub = mx * mul;
-                    m = mx * c;
+                    m = __fmul_rd(mx, c);  // (as the kernel for few rows has it)
                 }
                 const unsigned long long c2 = pk(mul, mul), m2 = pk(-sub, -sub);
                 unsigned long long sum2 = 0;
