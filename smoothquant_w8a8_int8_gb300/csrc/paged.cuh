@@ -103,6 +103,7 @@ __device__ __forceinline__ void find_shares(const PagedArgs &a, int min_pairs, S
     const int b0 = min(nb, (int)threadIdx.x * run);
     int b1 = min(nb, b0 + run);
     int mine = 0, before = 0;
+    bool overlap = false;  // (the sums may wrap around then, and are not used)
     // first every thread's run is summed, then the shares that begin in it are
     // found, walking through it again
 #pragma unroll 1
@@ -113,7 +114,8 @@ __device__ __forceinline__ void find_shares(const PagedArgs &a, int min_pairs, S
             const Seq s = load_seq(a, b);
             const int n = a.Hkv * pairs_before<KT, PAD>(a, s, row_tiles(a, s));
             if (pass == 0) {
-                mine = add_pairs(mine, n);
+                mine += n;
+                overlap = overlap || !in_order(a, b);
                 continue;
             }
 #pragma unroll 1
@@ -129,22 +131,23 @@ __device__ __forceinline__ void find_shares(const PagedArgs &a, int min_pairs, S
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if ((threadIdx.x & 31) >= o) incl = add_pairs(incl, v);
+            if ((threadIdx.x & 31) >= o) incl += v;
         }
         if ((threadIdx.x & 31) == 31) warp_sum[threadIdx.x >> 5] = incl;
-        __syncthreads();
+        const bool none = __syncthreads_or(overlap) != 0;
         int total = 0;
 #pragma unroll 1
         for (int w = 0; w < NT / 32; ++w) {
-            if (w < (int)(threadIdx.x >> 5)) before = add_pairs(before, warp_sum[w]);
-            total = add_pairs(total, warp_sum[w]);
+            if (w < (int)(threadIdx.x >> 5)) before += warp_sum[w];
+            total += warp_sum[w];
         }
-        total = line_length(total);
-        if (total == 0) b1 = b0;     // (a line that is too long has no places)
-        else before += incl - mine;  // pairs of the runs before this thread's
+        if (none) {
+            total = 0;
+            b1 = b0;  // no share has a place
+        }
+        before += incl - mine;  // pairs of the runs before this thread's
         if (threadIdx.x < W) {
-            int workers = min(total / min_pairs + (total % min_pairs != 0 ? 1 : 0),
-                              W * (int)gridDim.x);
+            int workers = min((total + min_pairs - 1) / min_pairs, W * (int)gridDim.x);
             if (a.prefix_phase && total > 0) {
                 // items of one length: whole numbers of workers for each, where
                 // there are enough, so that no worker has parts of two

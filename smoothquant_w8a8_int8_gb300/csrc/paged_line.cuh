@@ -15,7 +15,7 @@
 // (a counter) joins them in the order of the line, so that the result does not
 // depend on who is last.  The line is shorter than 2^31 pairs (checked on the
 // host for the longest that the sizes allow), but for sequences that overlap: see
-// add_pairs.
+// in_order.
 #pragma once
 #include <cuda_runtime.h>
 #include <cmath>
@@ -135,17 +135,14 @@ SQ_HD int pairs_before(const PagedArgs &a, const Seq &s, int J) {
     return sum;
 }
 
-// The line's length is summed with this.  Where q_start is non-decreasing the
-// sequences hold T tokens in all, and the host has checked the longest line of
-// theirs.  Where it is not, they overlap, B of them with T tokens each at most: one
-// sequence's pairs still fit, but the sum may be anything, so it stops at
-// kTooLong, and such a line is not worked on.  (x and y are not negative.)
-constexpr int kTooLong = 0x7fffffff;
-SQ_HD int add_pairs(int x, int y) {
-    const uint32_t sum = (uint32_t)x + (uint32_t)y;
-    return sum < (uint32_t)kTooLong ? (int)sum : kTooLong;
+// Whether sequence b ends where it starts or behind it.  Where all do, they hold at
+// most T tokens in all, and the host has checked the longest line of those.  Where one
+// does not, sequences overlap, B of them with T tokens each at most: one sequence's
+// pairs still fit, but their sum may wrap around, and nothing is worked on (see
+// find_shares).
+SQ_HD bool in_order(const PagedArgs &a, int b) {
+    return a.prefix_phase || load_int(a.q_start + b) <= load_int(a.q_start + b + 1);
 }
-SQ_HD int line_length(int sum) { return sum == kTooLong ? 0 : sum; }
 
 // Where a worker's share starts.
 struct Share {

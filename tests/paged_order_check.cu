@@ -2,57 +2,41 @@
 // paged_line_check.cu leaves out, run on the CPU by tests/test_paged_order.py:
 //  - row tiles of 128, 16 and 8 rows with every number of heads to a group up to
 //    them, as the launches have them;
-//  - q_start that decreases.  Its sequences overlap, so that their pairs can pass
-//    2^31 although the host's check of the sizes holds: the length that the shares
-//    are cut from is then 0, and no worker takes a piece.
+//  - any q_start: where every sequence is in order, the pairs of all stay within what
+//    the host's check of the sizes has counted.  Where one is not, they overlap and can
+//    pass 2^31 although that check holds: the shares are cut from a length of 0 then,
+//    and no worker takes a piece.
 #define main line_main
 #include "paged_line_check.cu"
 #undef main
 
-// The shares as find_shares cuts them: `threads` runs of sequences, their sums
-// scanned; returns the line's length.
-template <int KT, int PAD>
-static int length_by_runs(const PagedArgs &a, int threads) {
-    const int nb = a.prefix_phase ? 1 : a.B, run = (nb + threads - 1) / threads;
-    int total = 0;
-    for (int t = 0; t < threads; ++t) {
-        int mine = 0;
-        for (int b = std::min(nb, t * run); b < std::min(nb, (t + 1) * run); ++b) {
-            const Seq s = load_seq(a, b);
-            mine = add_pairs(mine, a.Hkv * pairs_before<KT, PAD>(a, s, row_tiles(a, s)));
-        }
-        total = add_pairs(total, mine);
-    }
-    return line_length(total);
-}
+#include <algorithm>
 
 template <int KT, int PAD>
-static bool decreasing(const PagedArgs &a) {
+static bool any_order(const PagedArgs &a) {
     // the host's check, as launch_paged_attention makes it
-    const int64_t tiles = (a.T + a.tpt - 1) / a.tpt + (a.prefix_phase ? 0 : a.B);
-    const int64_t keys = ((a.prefix_phase ? 0 : a.cap) + (int64_t)a.prefix_len) / KT + 16;
+    const int64_t tiles = (a.T + a.tpt - 1) / a.tpt + a.B;
+    const int64_t keys = (a.cap + (int64_t)a.prefix_len) / KT + 16;
     if (tiles * a.Hkv > ((int64_t)1 << 31) / keys) return false;
-    int64_t want = 0;
-    for (int b = 0; b < (a.prefix_phase ? 1 : a.B); ++b) {
+    int64_t total = 0;
+    bool ordered = true;
+    for (int b = 0; b < a.B; ++b) {
         const Seq s = load_seq(a, b);
         CHECK(s.q0 >= 0 && s.qlen >= 0 && s.q0 + s.qlen <= a.T && s.kv >= 0 && s.kv <= a.cap);
         const int64_t n = (int64_t)a.Hkv * pairs_before<KT, PAD>(a, s, row_tiles(a, s));
-        CHECK(n >= 0 && n < kTooLong);  // one sequence's pairs fit
-        want += n;
+        CHECK(n >= 0 && n < ((int64_t)1 << 31));  // one sequence's pairs fit
+        total += n;
+        ordered = ordered && in_order(a, b);
     }
-    const bool fits = want < kTooLong;
-    for (int threads : {256, 640}) {
-        const int total = length_by_runs<KT, PAD>(a, threads);
-        CHECK(total == (fits ? want : 0));
-        if (fits) continue;
-        Share sh;
-        sh.seq = sh.seq_begin = 0x55555555;  // never looked at
-        set_shares(sh, total, 0, threads % 7);
-        Walk<KT, PAD> w;
-        w.start(a, sh);
-        Piece p;
-        CHECK(!w.next(a, sh, p));
-    }
+    const bool fits = total < ((int64_t)1 << 31);
+    CHECK(!ordered || (fits && total <= tiles * a.Hkv * keys));
+    Share sh;
+    sh.seq = sh.seq_begin = 0x55555555;  // never looked at
+    set_shares(sh, 0, 0, a.B % 7);
+    Walk<KT, PAD> w;
+    w.start(a, sh);
+    Piece p;
+    CHECK(!w.next(a, sh, p));
     return !fits;
 }
 
@@ -106,11 +90,12 @@ int main() {
         std::vector<int> q(a.B + 1), kv(a.B);
         for (int b = 0; b <= a.B; ++b)
             q[b] = trial % 5 == 0 ? (int)rng() : b % 2 ? a.T : 0;  // 0, T, 0, T, ...
+        if (trial % 3 == 1) std::sort(q.begin(), q.end());
         for (int b = 0; b < a.B; ++b) kv[b] = trial % 7 == 0 ? (int)rng() : a.cap;
         a.q_start = q.data();
         a.kv_len = kv.data();
         a.kstart = a.prefix_len / KT * KT;
-        too_long += KT == 16 ? decreasing<16, 2>(a) : decreasing<128, 4>(a);
+        too_long += KT == 16 ? any_order<16, 2>(a) : any_order<128, 4>(a);
     }
     CHECK(too_long > 20);
     std::printf("%lld checks, %lld failures, %d lines too long\n", g_checked, g_fail, too_long);
