@@ -275,17 +275,17 @@ sq_status sq_kv_append(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv, int
  * and values of positions behind a token's own reach its row, finite or not.  A value
  * that is not finite leaves its column of the rows that see it not finite; an
  * infinity may come out as NaN (its product with a probability's smaller parts).
- * scale: of either sign, 2^127 at most; below 2^-101 it counts as 0 (each key that a
- * row sees has the same weight).
+ * scale: of either sign, 2^127 at most; below 2^-100 it may count as 0 (each key that
+ * a row sees has the same weight).
  * Q fp32, rows of ldq floats (ldq >= Hq D, a multiple of 4); O fp32 [T][Hq D],
  * overlapping nothing.  max_q: the most tokens of a sequence; it chooses the
  * kernel only, results do not depend on it but for rounding.
- * Queries and probabilities enter the tensor cores as sums of 16-bit numbers of
- * the cache's type, three for bf16 (exact) and two for fp16 (within 2^-22, or
- * 2^-32 of the row's largest element, or 2^-65), and products are summed in fp32,
- * as are the softmax's maxima and sums: O agrees with the exact attention over the
- * stored rows as far as fp32 logits and sums do, to a few 2^-21 of max |V| where
- * logits are of order one.
+ * Queries (times the significand of scale log2 e, one rounding to fp32) and
+ * probabilities enter the tensor cores as sums of 16-bit numbers of the cache's type,
+ * three for bf16 (exact) and two for fp16 (within 2^-22, or 2^-32 of the row's largest
+ * element, or 2^-65), and products are summed in fp32, as are the softmax's maxima
+ * and sums: O agrees with the exact attention over the stored rows as far as fp32
+ * logits and sums do, to a few 2^-21 of max |V| where logits are of order one.
  * Results are the same bits from call to call.
  * workspace (16-byte aligned, zero-filled once before its first use): at least
  * sq_paged_attention_workspace_bytes bytes; it serves one call at a time, on

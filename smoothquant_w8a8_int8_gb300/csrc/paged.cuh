@@ -21,13 +21,6 @@ __device__ __forceinline__ float max_factor(float a, float b) {
     return a == -INFINITY ? 0.0f : ex2(a - b);
 }
 
-// The smaller one; NaN if either is
-__device__ __forceinline__ float min_nan(float a, float b) {
-    float d;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
-
 // 2^e, e in [-126, 127]
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 // The multiple of 8 that scales numbers whose largest has the exponent e into

@@ -119,11 +119,17 @@ sq_status launch_paged_attention(const PagedCall &c, cudaStream_t st) {
                    : c.page_size == 128 ? 7 : 8;
     a.prefix_len = (int)c.prefix_len;
     a.cap = (int)(c.max_pages * c.page_size);
+    // A power of two, so that a logit's product with it is exact: however large a row's
+    // maximum is, the largest key's exponent is as formed for the maximum, and its
+    // probability what it should be.  The rest is the queries' (one rounding each, 2^-24).
     // Not zero, so that a masked logit's -inf stays -inf under it, and large enough for
-    // the factors of fp16 rows.  A scale below that is zero: no query counts.
+    // the factors of fp16 rows; a scale below that is zero: no query counts.
     const float scale = fabsf(c.scale) * 1.4426950408889634f;
-    a.scale = std::max(scale, 0x1p-100f);
-    a.sign = scale < 0x1p-100f ? 0.0f : c.scale < 0.0f ? -1.0f : 1.0f;
+    int exponent = 0;
+    (void)frexpf(std::max(scale, 0x1p-100f), &exponent);
+    exponent = std::min(exponent, 127);
+    a.scale = ldexpf(1.0f, exponent);
+    a.q_factor = scale < 0x1p-100f ? 0.0f : copysignf(ldexpf(scale, -exponent), c.scale);
     const bool bf16 = c.cache_type == SQ_CACHE_BF16;
     const int64_t max_q = std::min(c.max_q, c.T), tokens = std::min(c.T, max_q * c.B);
     const bool front = c.prefix_len > 0 && prefix_in_front(a, max_q, tokens, di.sms);

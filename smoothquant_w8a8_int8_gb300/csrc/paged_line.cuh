@@ -48,8 +48,8 @@ struct PagedArgs {
                          // where the prefix is a launch of its own
     int front_shift;     // front_tiles KT - kstart: 0, or KT for a prefix that ends in a tile
     int cap;             // keys a row of the page table can name
-    float scale;         // |scale| log2 e; the sign is folded into the queries
-    float sign;          // 1, -1, or 0 for a scale of zero
+    float scale;         // a power of two; times q_factor the call's scale times log2 e
+    float q_factor;      // what the queries are multiplied by, 0 for a scale of zero
     int prefix_phase;    // 1: every token over the prefix, into prefix_o / prefix_ml
     int after_prefix;    // 1: the few rows' launch behind that one (see begin_rows)
 };

@@ -30,7 +30,9 @@
 // (within 2^-22, or 2^-32 of a row's largest), three for bf16 (exact).  Fp16's
 // probabilities carry a factor 2^12: its smallest step is 2^-24, and without it a
 // key of less than 2^-25 of the largest's weight would count in the sum alone (8192
-// of 2^-25 behind one of 1: 2.3e-4 of the output, all of what they say).
+// of 2^-25 behind one of 1: 2.3e-4 of the output, all of what they say).  The queries
+// carry the scale's significand, so that logits are multiplied by a power of two:
+// the largest key's exponent is 0 however large its logit is.
 // Up to 8 rows, two of the parts share an instruction's 16 rows (the first in
 // rows 0-7, the second in rows 8-15) and the two halves are added in fp32.
 #include "paged.cuh"
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         float mul[R], scale[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            mul[r] = a.sign;
+            mul[r] = a.q_factor;
             scale[r] = a.scale;
             if (BF) continue;
             float top = 0.0f;
@@ -268,6 +270,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            top *= fabsf(a.q_factor);
             const int sh = shift_of((int)(__float_as_uint(top) >> 23) - 127);
             mul[r] *= pow2(-sh);
             scale[r] *= pow2(sh);
@@ -365,9 +368,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 float mx = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                // rounded down: see below
-                const float mn =
-                    mx == -INFINITY ? m[r] : fmaxf(m[r], __fmul_rd(mx, scale[r]));
+                const float mn = mx == -INFINITY ? m[r] : fmaxf(m[r], mx * scale[r]);
                 any = any || mn > m[r];
                 grow[r] = mn > m[r] ? max_factor(m[r], mn) : 1.0f;
                 m[r] = mn;
@@ -432,15 +433,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 }
             }
             uint32_t pf[S][4];
-            // The exponents are formed with one rounding; the largest logit's is what
-            // its maximum lost in its own: nothing that counts below 2^23, and no more
-            // than 1 here above that, where the logits themselves are as coarse.
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const float from = m[r] == -INFINITY ? 0.0f : -m[r];  // (no key yet)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[r][i] = ex2(min_nan(fmaf(x[r][i], scale[r], from), 1.0f));
+                    x[r][i] = ex2(fmaf(x[r][i], scale[r], from));
                     l[r] += x[r][i];
                 }
             }

@@ -19,7 +19,9 @@
 // are split in 16-bit numbers of their type, one instruction per part: two for
 // fp16 (within 2^-22), three for bf16 (exact; two would leave 2^-17).
 // The probabilities of a tile carry a factor 2^12, and fp16 queries are scaled
-// row by row by a power of two, so that no part falls below fp16's range.
+// row by row by a power of two, so that no part falls below fp16's range.  The
+// queries carry the scale's significand, so that logits are multiplied by a power
+// of two: the exponents of a row whose logits are far from one are exact too.
 //
 // Bound: the products, at twice (fp16) or three times (bf16) the instructions
 // of the plain operands' attention, for long items (152 of 16,384 keys, bf16:
@@ -130,13 +132,6 @@ constexpr int kJoin = 6;
 // (30,000 keys, 1 item)
 constexpr int kMinTiles = 4;
 constexpr float kBias = 12.0f;  // log2 of the probabilities' factor
-
-// Whether a row maximum m of x c (log2 units) is so large that its own rounding
-// counts in x c - m: at most 2 below 2^26, then 4 and more, with which the largest
-// key's probability 2^(x c - m), under its factor, would leave fp16's range, and
-// from 2^32 on that of fp32.  Two logits of such a row that are not equal differ by
-// 2 at least.
-__device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= 0x1p26f; }
 
 template <int D, bool BF>
 struct TilesCfg {
@@ -642,12 +637,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
                                  : "r"(raw + i * 128 + (((in4 & 7) ^ ((i + sub) & 7)) << 4))
                                  : "memory");
-                    float mul = a.sign;
+                    float mul = a.q_factor;
                     if (!BF) {
                         // (over the row's own lanes: a step may hold two rows, and what
                         // one of them holds must not cost the other its bits)
-                        const float top = fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)),
-                                                fmaxf(fabsf(q.z), fabsf(q.w)));
+                        const float top =
+                            fabsf(mul) * fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)),
+                                               fmaxf(fabsf(q.z), fabsf(q.w)));
                         unsigned e = __float_as_uint(top);
                         if (LPR == 32) {
                             e = __reduce_max_sync(0xffffffffu, e);
@@ -727,16 +723,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 mx = fmaxf(mx, B.half_max[t & 1][1 - g][r]);
-                float m = mx == -INFINITY ? 0.0f : fmaf(mx, c, -kBias);
-                float mul = c, sub = m;
-                if (is_far(m)) {
-                    // a power of two in c's place: the products are exact, and the
-                    // largest key's probability is 1
-                    mul = __uint_as_float(__float_as_uint(c) & 0xff800000u);
-                    sub = mx * mul;
-                    m = __fmul_rd(mx, c);  // (as the kernel for few rows has it)
-                }
-                const unsigned long long c2 = pk(mul, mul), m2 = pk(-sub, -sub);
+                // (rounded up: mx c is exact, so the largest exponent is 12 at most, and
+                // at least 0 where 12 is less than the maximum's last place)
+                const float m = mx == -INFINITY ? 0.0f : __fmaf_ru(mx, c, -kBias);
+                const unsigned long long c2 = pk(c, c), m2 = pk(-m, -m);
                 unsigned long long sum2 = 0;
                 // per 16 keys 8 columns of each part
 #pragma unroll

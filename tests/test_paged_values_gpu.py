@@ -26,9 +26,11 @@ def sq():
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("q", [FEW, MANY])
 @pytest.mark.parametrize("top", [2.0 ** -33, 2.0 ** -16, 2.0 ** -8, 1.0, 2.0, 256.0, 2.0 ** 16])
-def test_largest_element_at_an_octaves_end(sq, top, q, D, dtype):
+@pytest.mark.parametrize("scale", [0.6931471805599453 / 8, 0.1])
+def test_largest_element_at_an_octaves_end(sq, scale, top, q, D, dtype):
     """Every row's largest element is the largest float below `top`, whose
-    rounding to fewer bits is `top`; keys that make logits of order one."""
+    rounding to fewer bits is `top`, also times the first scale's log2 e; keys that
+    make logits of order one."""
     t = Batch(q, [200, 333], 8, 2, D, 32, dtype, seed=D + sum(q))
     rows = t.Q.view(t.T * t.Hq, D)
     rows.mul_(0.3).clamp_(-0.9, 0.9)
@@ -36,7 +38,7 @@ def test_largest_element_at_an_octaves_end(sq, top, q, D, dtype):
     rows[at, at % D] = torch.where(at % 2 == 0, 1.0, -1.0) * (1 - 2.0 ** -24)
     rows.mul_(top)
     t.k = (t.k.float() * (3 / top)).clamp(-65504.0, 65504.0).to(dtype)
-    verify(sq, t.cuda())
+    verify(sq, t.cuda(), scale=scale)
 
 
 def uneven(t, factors):
