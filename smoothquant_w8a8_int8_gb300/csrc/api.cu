@@ -467,7 +467,7 @@ sq_status sq_paged_attention(const float *Q, int64_t ldq, int64_t T, int64_t Hq,
     const PagedCall c = {Q,         ldq,         T,         Hq,      Hkv,          D,
                          k_cache,   v_cache,     cache_type, num_pages, page_size,  block_table,
                          max_pages, q_start,     kv_len,    B,       max_q,        prefix_pages,
-                         prefix_len, scale,      O,         workspace, workspace_bytes};
+                         prefix_len, scale,      O,         workspace};
     return launch_paged_attention(c, as_stream(stream));
 }
 

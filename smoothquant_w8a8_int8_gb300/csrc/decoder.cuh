@@ -39,7 +39,6 @@ struct PagedCall {
     float scale;
     float *O;
     void *workspace;
-    size_t workspace_bytes;
 };
 sq_status launch_paged_attention(const PagedCall &c, cudaStream_t st);
 

@@ -197,7 +197,7 @@ __device__ __forceinline__ float *row_target(const PagedArgs &a) {
 // The kernel for at most 16 rows per item (paged_rows.cu): rows = 8 or 16.
 sq_status launch_paged_rows(const PagedArgs &a, const void *k_cache, const void *v_cache, int D,
                             bool bf16, int rows, int sms, cudaStream_t st);
-// The kernel for up to 256 rows per item (paged_tiles.cu).
+// The kernel for up to 128 rows per item (paged_tiles.cu).
 sq_status launch_paged_tiles(const PagedArgs &a, const void *k_cache, const void *v_cache, int D,
                              bool bf16, int sms, cudaStream_t st);
 
