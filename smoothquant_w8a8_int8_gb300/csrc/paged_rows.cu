@@ -21,7 +21,7 @@
 // each per SM quarter): 16 rows are too few for tensor memory's 128.
 //
 // Measured (32 / 8 heads of 128, bf16): a step of 64 sequences of up to 8192 keys
-// 160 us, 6.5 TB/s, 96 % of the measured copy rate; one token behind 300 keys 13
+// 161 us, 6.5 TB/s, 96 % of the measured copy rate; one token behind 300 keys 14
 // us, behind 4000 21, behind 100,000 83 (4.8 TB/s): those are bound by latency, the
 // start's chain of dependent loads and the pieces' join.
 //
