@@ -167,8 +167,8 @@ sq_status launch_kv_append(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv,
     sq_status rc = device_info(&di);
     if (rc != SQ_OK) return rc;
     // a few tokens: a unit per thread; many: a block per token (32 / 8 heads of 128,
-    // that layout alone, cold L2, launch included: 64 tokens 7.8 and 9.9 us, 256: 8.6 and 9.7, 512: 11.9
-    // and 12.5, 1024: 16.7 and 16.0, 2048: 24.8 and 22.9)
+    // that layout alone, cold L2, launch included: 64 tokens 7.8 and 9.9 us, 256: 8.6
+    // and 9.7, 512: 11.9 and 12.5, 1024: 16.7 and 16.0, 2048: 24.8 and 22.9)
     const int64_t units = (Hq + 2 * Hkv) * D / 8;
     const int64_t gy = T <= 2 * di.sms ? (units + kAppendThreads - 1) / kAppendThreads : 1;
     const int64_t grid = std::min<int64_t>(T, (int64_t)di.sms * 64);

@@ -33,8 +33,9 @@
 // another 5 us where an item is split and joined.
 // Measured: two prompts of about 4000 tokens, 32 / 8 heads of 128, bf16: 717 us
 // (the same in fp16 532); 16 drafts of 2 to 5 tokens behind 4096 to 16,384 keys,
-// 24 / 4 heads, fp16: 94 us, 57 % of the measured copy rate.  TMA boxes of one 16-row page each
-// measured 3.0 TB/s (104 ns of its unit's time a box); cp.async 7 TB/s.
+// 24 / 4 heads, fp16: 94 us, 57 % of the measured copy rate.  TMA boxes of one
+// 16-row page each measured 3.0 TB/s (104 ns of its unit's time a box); cp.async
+// 7 TB/s.
 //
 // Roles (640 threads, one persistent CTA per SM):
 //   warps 0-3, 4-7   queries and softmax, 64 keys of a tile each;
