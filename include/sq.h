@@ -322,6 +322,48 @@ sq_status sq_linear_i8(const void *Xop, const float *x_scale, const int32_t *x_r
                        const float *bias, const float *residual, int64_t M, int64_t N, int64_t K,
                        int mode, void *Y, void *stream);
 
+/* ---- Gated feed-forward block ---------------------------------------------- */
+
+/* Both projections of a decoder's gated feed-forward block, the gate's activation
+ * and the product, in one GEMM:
+ *   Y[m][f] = act(g) u,  g = d_gate[m][f] + bias_gate[f],  u = d_up[m][f] + bias_up[f],
+ * d = acc * x_scale * w_scale of the two weight matrices as in sq_linear_i8 (acc
+ * exact in int32).  Y fp32 [M][F] is the down projection's input (sq_quantize_act
+ * and its kin). */
+typedef enum {
+    SQ_GATE_SILU = 0,     /* act(t) = t / (1 + exp(-t)) */
+    SQ_GATE_GELU = 1,     /* 0.5 t (1 + erf(t / sqrt 2)) */
+    SQ_GATE_GELU_TANH = 2 /* 0.5 t (1 + tanh(sqrt(2 / pi) (t + 0.044715 t^3))) */
+} sq_gate;
+
+/* Rows of the packed operand of two F x K weights: 64 ceil(F / 32).  Rows 64 b ..
+ * 64 b + 31 are the gate's rows 32 b .., rows 64 b + 32 .. 64 b + 63 the other
+ * projection's; rows of no f >= F are codes of zero with scale 1.  0 for F < 0
+ * or F > 2^24. */
+int64_t sq_gated_rows(int64_t F);
+
+/* Packs the two weights (offline), row by row as sq_pack_weight: W_gate and W_up
+ * fp32 [F][K], s fp32 [K] their common input's smoothing factor.  R =
+ * sq_gated_rows(F): Wop GEMM operand of sq_operand_bytes(R, K) bytes, w_scale fp32
+ * [R] (4-byte aligned), w_row_l1 int32 [R] (nullable).  F <= 2^24. */
+sq_status sq_pack_gated_weight(const float *W_gate, const float *W_up, const float *s, int64_t F,
+                               int64_t K, float *w_scale, void *Wop, int32_t *w_row_l1,
+                               void *stream);
+
+/* Xop, x_scale, x_row_l1 as in sq_linear_i8; Wop, w_scale, w_row_l1 from
+ * sq_pack_gated_weight; bias_gate and bias_up fp32 [F] (4-byte aligned), each
+ * nullable; act: sq_gate; Y fp32 [M][F], overlapping nothing.  Rows of F a
+ * multiple of 4 take bulk stores.  workspace (nullable): splits K over several SMs
+ * for small launches, on the rules of sq_linear_i8_ws, sized by
+ * sq_gated_workspace_bytes (0: not split); Y is the same bits with and without
+ * it.  K <= 133144, F <= 2^24 (SQ_ERR_UNSUPPORTED beyond). */
+sq_status sq_gated_workspace_bytes(int64_t M, int64_t F, int64_t K, size_t *bytes);
+sq_status sq_linear_i8_gated(const void *Xop, const float *x_scale, const int32_t *x_row_l1,
+                             const void *Wop, const float *w_scale, const int32_t *w_row_l1,
+                             const float *bias_gate, const float *bias_up, int64_t M, int64_t F,
+                             int64_t K, int act, float *Y, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
 /* sq_linear_i8 on the int8 activation codes Xq [M][K] (as sq_quantize_act
  * writes them) instead of the GEMM-operand buffer: the per-token x per-channel
  * INT8 recipe's own input format.  sm_103a's tensor cores take no int8

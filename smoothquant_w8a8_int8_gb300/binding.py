@@ -33,6 +33,8 @@ EXPORTS = ("sq_status_string", "sq_version", "sq_operand_bytes", "sq_packed_weig
            "sq_linear_block_host",
            "sq_rmsnorm_quant", "sq_rope_table", "sq_kv_append",
            "sq_paged_attention_workspace_bytes", "sq_paged_attention",
+           "sq_gated_rows", "sq_pack_gated_weight", "sq_gated_workspace_bytes",
+           "sq_linear_i8_gated",
            "sq_check_division", "sq_device_status", "sq_get_device_status")
 
 class LinearLayerC(ctypes.Structure):
@@ -89,6 +91,12 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                 "sq_paged_attention": ([vp, i64, i64, i64, i64, i64, vp, vp, i32, i64, i64, vp,
                                         i64, vp, vp, i64, i64, vp, i64, f32, vp, vp,
                                         ctypes.c_size_t, vp], i32),
+                "sq_gated_rows": ([i64], i64),
+                "sq_pack_gated_weight": ([vp, vp, vp, i64, i64, vp, vp, vp, vp], i32),
+                "sq_gated_workspace_bytes": ([i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)],
+                                             i32),
+                "sq_linear_i8_gated": ([vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp,
+                                        vp, ctypes.c_size_t, vp], i32),
                 "sq_linear_i8": ([vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, vp],
                                  i32),
                 "sq_linear_i8_requant": ([vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp,
@@ -556,6 +564,77 @@ def linear_i8(Xop, x_scale, Wop, w_scale, bias=None, residual=None, mode=EPI_BIA
     _check(load().sq_linear_i8(_p(Xop), _p(x_scale), _p(x_l1), _p(Wop), _p(w_scale), _p(w_l1),
                                _p(bias), _p(residual), M, N, K, int(mode), _p(out),
                                _stream(stream)), "sq_linear_i8")
+    return out
+
+
+GATE_SILU, GATE_GELU, GATE_GELU_TANH = range(3)
+
+
+def gated_rows(F: int) -> int:
+    """Rows of the packed operand of a gated block's two F x K weights."""
+    return int(load().sq_gated_rows(F))
+
+
+def pack_gated_weight(W_gate: torch.Tensor, W_up: torch.Tensor, s: torch.Tensor,
+                      want_l1: bool = False, stream=None):
+    """Packs the two projections of a gated block, [F, K] each, into one operand for
+    linear_i8_gated; s: their common input's smoothing factor.  Returns (w_scale
+    [gated_rows(F)], Wop [gated_rows(F), K]), plus the rows' code L1 norms (int32)
+    as a third item when want_l1."""
+    _need(W_gate, torch.float32, "W_gate")
+    if W_gate.dim() != 2:
+        raise ValueError("W_gate must have shape (F, K)")
+    F, K = W_gate.shape
+    dev, f32 = W_gate.device, torch.float32
+    up, sp = _arg(W_up, f32, "W_up", (F, K), dev), _arg(s, f32, "s", (K,), dev)
+    with _on(W_gate, stream) as st:
+        rows = gated_rows(F)
+        sw = torch.empty(rows, dtype=f32, device=dev)
+        Wop = empty_operand(rows, K, dev)
+        l1 = torch.empty(rows, dtype=torch.int32, device=dev) if want_l1 else None
+        _check(load().sq_pack_gated_weight(W_gate.data_ptr(), up, sp, F, K, sw.data_ptr(),
+                                           Wop.data_ptr(), _p(l1), st), "sq_pack_gated_weight")
+    return (sw, Wop, l1) if want_l1 else (sw, Wop)
+
+
+def gated_workspace_bytes(M: int, F: int, K: int) -> int:
+    """Bytes of linear_i8_gated's split-K workspace (0: none needed) on the current
+    device."""
+    n = ctypes.c_size_t(0)
+    _check(load().sq_gated_workspace_bytes(M, F, K, ctypes.byref(n)), "sq_gated_workspace_bytes")
+    return int(n.value)
+
+
+def linear_i8_gated(Xop: torch.Tensor, x_scale: torch.Tensor, Wop: torch.Tensor,
+                    w_scale: torch.Tensor, F: int, act: int = GATE_SILU, bias_gate=None,
+                    bias_up=None, out: Optional[torch.Tensor] = None, x_l1=None, w_l1=None,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gated feed-forward block's two projections, the gate's activation and the
+    product in one GEMM: act(gate) * up, fp32 [M, F].  Wop and w_scale come from
+    pack_gated_weight; workspace: empty_workspace(gated_workspace_bytes(M, F, K)), None
+    for no split over K (the same bits either way)."""
+    _need(Xop, torch.bfloat16, "Xop")
+    if Xop.dim() != 2:
+        raise ValueError("Xop must have shape (M, K)")
+    M, K = Xop.shape
+    rows = gated_rows(F)
+    dev, f32, i32 = Xop.device, torch.float32, torch.int32
+
+    def at(t, dtype, name, shape):
+        return None if t is None else _arg(t, dtype, name, shape, dev)
+
+    with _on(Xop, stream) as st:
+        if out is None:
+            out = torch.empty(M, F, dtype=f32, device=dev)
+        _check((_lib or load()).sq_linear_i8_gated(
+            Xop.data_ptr(), _arg(x_scale, f32, "x_scale", (M,), dev),
+            at(x_l1, i32, "x_l1", (M,)), _arg(Wop, torch.bfloat16, "Wop", (rows, K), dev),
+            _arg(w_scale, f32, "w_scale", (rows,), dev), at(w_l1, i32, "w_l1", (rows,)),
+            at(bias_gate, f32, "bias_gate", (F,)), at(bias_up, f32, "bias_up", (F,)), M, F, K,
+            int(act), _arg(out, f32, "out", (M, F), dev),
+            None if workspace is None else _arg(workspace, torch.uint8, "workspace",
+                                                workspace.shape, dev),
+            0 if workspace is None else workspace.numel(), st), "sq_linear_i8_gated")
     return out
 
 

@@ -1,6 +1,7 @@
 // C-ABI boundary: argument checks, then one launch per call on the caller's
 // stream.  Declarations and the contract of every entry point are in sq.h.
 #include "decoder.cuh"
+#include "gated.cuh"
 
 #include <cmath>
 #include <mutex>
@@ -46,6 +47,7 @@ sq_status require_sm103() {
 }
 
 constexpr int64_t kMaxK = 133144;  // K * 127^2 < 2^31
+constexpr int64_t kMaxGated = (int64_t)1 << 24;  // outputs of a gated block: rows fit a grid
 
 sq_status check_linear_args(const void *X, const float *sx, const void *W, const float *sw,
                             const float *bias, const float *residual, int64_t M, int64_t N,
@@ -530,6 +532,62 @@ sq_status sq_linear_i8_codes(const int8_t *Xq, const float *x_scale, const int32
     if ((rc = launch_widen_codes(Xq, op, M * K, as_stream(stream))) != SQ_OK) return rc;
     return linear_impl(op, x_scale, x_row_l1, Wop, w_scale, w_row_l1, bias, residual, M, N, K,
                        mode, Y, nullptr, 0, stream);
+}
+
+int64_t sq_gated_rows(int64_t F) {
+    return F < 0 || F > kMaxGated ? 0 : gated_rows(F);
+}
+
+sq_status sq_pack_gated_weight(const float *W_gate, const float *W_up, const float *s, int64_t F,
+                               int64_t K, float *w_scale, void *Wop, int32_t *w_row_l1,
+                               void *stream) {
+    sq_status rc = check_quant_args(W_gate, s, F, K, nullptr, w_scale, Wop);
+    if (rc != SQ_OK) return rc;
+    if (F > kMaxGated) return SQ_ERR_UNSUPPORTED;
+    if (F == 0) return SQ_OK;
+    if (!W_up) return SQ_ERR_INVALID_ARG;
+    if (!aligned16(W_up) || (w_row_l1 && !aligned4(w_row_l1))) return SQ_ERR_ALIGNMENT;
+    if ((rc = require_sm103()) != SQ_OK) return rc;
+    return launch_pack_gated(W_gate, W_up, s, F, K, w_scale, static_cast<__nv_bfloat16 *>(Wop),
+                             w_row_l1, as_stream(stream));
+}
+
+sq_status sq_gated_workspace_bytes(int64_t M, int64_t F, int64_t K, size_t *bytes) {
+    if (!bytes) return SQ_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (M < 0 || F < 0 || K <= 0) return SQ_ERR_INVALID_ARG;
+    if (F > kMaxGated || K > kMaxK) return SQ_ERR_UNSUPPORTED;
+    if (M == 0 || F == 0) return SQ_OK;
+    return gemm_tc_workspace_bytes(M, gated_rows(F), K, bytes);
+}
+
+sq_status sq_linear_i8_gated(const void *Xop, const float *x_scale, const int32_t *x_row_l1,
+                             const void *Wop, const float *w_scale, const int32_t *w_row_l1,
+                             const float *bias_gate, const float *bias_up, int64_t M, int64_t F,
+                             int64_t K, int act, float *Y, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+    if (act < SQ_GATE_SILU || act > SQ_GATE_GELU_TANH) return SQ_ERR_INVALID_ARG;
+    sq_status rc = check_linear_args(Xop, x_scale, Wop, w_scale, nullptr, nullptr, M, F, K,
+                                     SQ_EPI_NONE, Y);
+    if (rc != SQ_OK) return rc;
+    if (F > kMaxGated) return SQ_ERR_UNSUPPORTED;
+    if (M == 0 || F == 0) return SQ_OK;
+    if ((bias_gate && !aligned4(bias_gate)) || (bias_up && !aligned4(bias_up)) ||
+        (x_row_l1 && !aligned4(x_row_l1)) || (w_row_l1 && !aligned4(w_row_l1)) ||
+        (workspace && !aligned16(workspace)))
+        return SQ_ERR_ALIGNMENT;
+    if ((rc = require_sm103()) != SQ_OK) return rc;
+    constexpr float kLog2e = 1.4426950408889634f;
+    GatedOut g = {bias_gate, bias_up, (int)F, act, -kLog2e, 0.0f};
+    if (act == SQ_GATE_GELU_TANH) {
+        const double two_root = 1.5957691216057308;  // 2 sqrt(2 / pi)
+        g.c1 = (float)(-two_root * 1.4426950408889634);
+        g.c3 = (float)(-two_root * 1.4426950408889634 * 0.044715);
+    }
+    return launch_gemm_tc(static_cast<const __nv_bfloat16 *>(Xop), x_scale, x_row_l1,
+                          static_cast<const __nv_bfloat16 *>(Wop), w_scale, w_row_l1, nullptr,
+                          nullptr, M, gated_rows(F), K, SQ_EPI_NONE, Y, nullptr, workspace,
+                          workspace_bytes, as_stream(stream), nullptr, nullptr, &g);
 }
 
 sq_status sq_linear_i8_requant(const void *Xop, const float *x_scale, const int32_t *x_row_l1,

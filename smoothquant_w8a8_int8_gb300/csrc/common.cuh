@@ -180,12 +180,16 @@ sq_status launch_gemm_mma_sync(const int8_t *Xq, const float *sx, const int8_t *
 // rm_pairs / row_amax (both non-NULL, rq NULL): Y as usual, and each row's
 // maximum of |fl(Y / s_next)| merged into row_amax (pairs: the division table
 // of s_next, see sq_division_table).
+// gated (mode SQ_EPI_NONE, the others NULL): N packed columns become Y [M][F]
+// (gated.cuh).
+struct GatedOut;
 sq_status launch_gemm_tc(const __nv_bfloat16 *Xop, const float *sx, const int32_t *x_l1,
                          const __nv_bfloat16 *Wop, const float *sw, const int32_t *w_l1,
                          const float *bias, const float *residual, int64_t M, int64_t N,
                          int64_t K, int mode, void *Y, const RequantOut *rq, void *workspace,
                          size_t workspace_bytes, cudaStream_t st,
-                         const float *rm_pairs = nullptr, float *row_amax = nullptr);
+                         const float *rm_pairs = nullptr, float *row_amax = nullptr,
+                         const GatedOut *gated = nullptr);
 // Bytes of the split-K workspace of an M x N x K launch on the current device (0: none used).
 sq_status gemm_tc_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes);
 // Read and clear the device error words of the tcgen05 GEMM and of the

@@ -50,6 +50,7 @@
 // records SQ_ERR_TIMEOUT in a device word, lets its issued copies and MMAs
 // drain, frees its tensor memory and returns.
 #include "common.cuh"
+#include "gated.cuh"
 #include "schedule.cuh"
 
 #include <cuda.h>
@@ -332,6 +333,7 @@ struct EpiArgs {
     // two columns per float4; and the [M] running maxima they merge into
     const float4 *rm_pairs;
     float *row_amax;
+    GatedOut gt;    // the gated epilogue's activation, biases and width (kOutGated kernels)
     int rq_vec;     // 1: rows of the code arrays are 16-byte multiples (N % 16 == 0)
     int rq_fast;    // 1: scale >= 2^-70, so the reciprocal division may be used
     Schedule sched;     // work units (made on the host)
@@ -343,8 +345,9 @@ struct EpiArgs {
 // What the epilogue hands out: fp32 (or int32) Y; the next linear's
 // Smooth-Static codes instead of Y; or Y plus each row's maximum of
 // |fl(Y / s_next)| (the next linear's dynamic statistic, merged across the
-// row's tiles by an integer atomicMax on the bit pattern).
-constexpr int kOutPlain = 0, kOutRequant = 1, kOutRowMax = 2;
+// row's tiles by an integer atomicMax on the bit pattern); or, of a gated
+// block's two projections (gated.cuh), the activated gate times the other.
+constexpr int kOutPlain = 0, kOutRequant = 1, kOutRowMax = 2, kOutGated = 3;
 
 // Largest row L1 norm of int8 codes for which 127 * L1 < 2^24: then every
 // partial sum of that row's products with any codes stays below 2^24 in
@@ -391,6 +394,28 @@ __device__ __forceinline__ unsigned long long gelu2(unsigned long long t2) {
     return fma2(h2, pk(copysignf(r0, u0), copysignf(r1, u1)), h2);
 }
 
+// t times the logistic function of t (c1 + c3 t^2), on a pair: SiLU (c1 = 1, c3 = 0)
+// and GELU's tanh form, t (1 + tanh(z / 2)) / 2 = t / (1 + exp(-z)).  exp(-z) may
+// overflow to infinity, whose reciprocal is zero.  The hardware's approximations of
+// 2^x and 1 / x are within 2^-22 and 2^-23.
+__device__ __forceinline__ unsigned long long sigmoid_gate2(unsigned long long t2,
+                                                            const GatedOut &g) {
+    const unsigned long long c1 = pk(g.c1, g.c1);
+    // (not 0 t^2: that is NaN where t^2 overflows)
+    const unsigned long long c = g.c3 == 0.0f ? c1 : fma2(mul2(t2, t2), pk(g.c3, g.c3), c1);
+    const unsigned long long z2 = mul2(t2, c);  // times -log2 e
+    float z0, z1;
+    upk(z2, z0, z1);
+    return mul2(t2, pk(rcp_approx(1.0f + ex2_approx(z0)), rcp_approx(1.0f + ex2_approx(z1))));
+}
+
+// The bias of column n of the packed operand (gated.cuh): the gate's or the other's.
+__device__ __forceinline__ float gated_bias(const GatedOut &g, int n) {
+    const float *bias = n & kGatedBlock ? g.bias_up : g.bias_gate;
+    const int f = n / (2 * kGatedBlock) * kGatedBlock + n % kGatedBlock;
+    return bias && f < g.F ? __ldg(bias + f) : 0.f;
+}
+
 // Per-column epilogue operands of one tile half, spread over the warp: lane j
 // holds column (nb + 32 s + j) for slice s; a slice broadcasts them with
 // shuffles.  Loaded before the accumulator wait, so their latency hides.
@@ -409,6 +434,7 @@ __device__ __forceinline__ void load_col_params(ColParams &cp, const EpiArgs &a,
         const bool ok = n < a.N;
         cp.w[s] = (MODE != SQ_EPI_RAW_I32 && ok) ? __ldg(a.sw + n) : 0.f;
         cp.b[s] = (MODE != SQ_EPI_RAW_I32 && MODE != SQ_EPI_NONE && ok) ? __ldg(a.bias + n) : 0.f;
+        if (OUT == kOutGated) cp.b[s] = gated_bias(a.gt, n);
         if (OUT == kOutRowMax) {
             // column n's pair alone (a float2: the table holds exactly N of them)
             const float2 c = ok ? __ldg(reinterpret_cast<const float2 *>(a.rm_pairs) + n)
@@ -763,6 +789,57 @@ __device__ __forceinline__ void epilogue_slice(uint32_t (&v)[32], int64_t m, int
     }
 }
 
+// The gated epilogue of two neighbouring slices: `v` holds the gate's sums of 32
+// outputs and `u` the other projection's (the packed weights alternate in blocks of
+// as many rows), n is the gate's first column; Y's 32 columns from n / 2 are stored as
+// epilogue_slice stores its.
+template <bool INT_IN>
+__device__ __forceinline__ void gated_slices(uint32_t (&v)[32], const uint32_t (&u)[32], int64_t m,
+                                             int n, int row0, int lane, const EpiArgs &a,
+                                             float xs, float wv, float wu, float bv, float bu,
+                                             const CUtensorMap *tmY, uint8_t *stg) {
+    const int f = n / 2;
+    if (f >= a.gt.F || row0 >= a.M) return;  // wholly outside Y
+    const unsigned long long xs2 = pk(xs, xs);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        auto value = [&](const uint32_t (&x)[32], float w, float b) {
+            const unsigned long long w2 =
+                pk(__shfl_sync(0xffffffffu, w, j), __shfl_sync(0xffffffffu, w, j + 1));
+            const unsigned long long b2 =
+                pk(__shfl_sync(0xffffffffu, b, j), __shfl_sync(0xffffffffu, b, j + 1));
+            const unsigned long long x2 =
+                INT_IN ? pk(__int2float_rn((int32_t)x[j]), __int2float_rn((int32_t)x[j + 1]))
+                       : pk(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+            return fma2(x2, mul2(xs2, w2), b2);
+        };
+        const unsigned long long g2 = value(v, wv, bv), u2 = value(u, wu, bu);
+        float y0, y1;
+        upk(mul2(a.gt.act == SQ_GATE_GELU ? gelu2(g2) : sigmoid_gate2(g2, a.gt), u2), y0, y1);
+        v[j] = __float_as_uint(y0);
+        v[j + 1] = __float_as_uint(y1);
+    }
+    if (a.tma_io) {
+        if (lane == 0) bulk_wait_read0();
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4 *>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(tmY, smem_u32(stg), f, row0);
+            bulk_commit();
+        }
+    } else if (m < a.M) {
+        uint32_t *y = static_cast<uint32_t *>(a.Y) + m * a.gt.F;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (f + j < a.gt.F) y[f + j] = v[j];
+    }
+}
+
 // The first `nsl` slices of this warp's part of a tile (all four for a full
 // tile, fewer for a column slice of one), reading tensor memory at `taddr`
 // (fp32 sums, or int32 with INT_IN).
@@ -771,6 +848,18 @@ __device__ __forceinline__ void epilogue_tile(uint32_t taddr, int64_t m, int nb,
                                               int lane, const EpiArgs &a, float xs,
                                               const ColParams &cp, float4 (&rnext)[8],
                                               const CUtensorMap *tmY, uint8_t *stg, int nsl) {
+    if (OUT == kOutGated) {
+#pragma unroll 1
+        for (int s = 0; s < nsl; s += 2) {  // (a unit's columns come in multiples of 64)
+            uint32_t v[32], u[32];
+            tmem_ld32(taddr + s * SLICE, v);
+            tmem_ld32(taddr + (s + 1) * SLICE, u);
+            gated_slices<INT_IN>(v, u, m, nb + s * SLICE, row0, lane, a, xs,
+                                 s == 0 ? cp.w[0] : cp.w[2], s == 0 ? cp.w[1] : cp.w[3],
+                                 s == 0 ? cp.b[0] : cp.b[2], s == 0 ? cp.b[1] : cp.b[3], tmY, stg);
+        }
+        return;
+    }
     float rmax = 0.0f;  // kOutRowMax: this row's maximum over the tile's columns
 #pragma unroll 1
     for (int s = 0; s < nsl; ++s) {
@@ -1634,8 +1723,10 @@ sq_status launch_gemm_tc(const __nv_bfloat16 *Xop, const float *sx, const int32_
                          const float *bias, const float *residual, int64_t M, int64_t N,
                          int64_t K, int mode, void *Y, const RequantOut *rq, void *workspace,
                          size_t workspace_bytes, cudaStream_t st, const float *rm_pairs,
-                         float *row_amax) {
+                         float *row_amax, const GatedOut *gated) {
     if (!shape_ok(M, N, K)) return SQ_ERR_UNSUPPORTED;
+    if (gated && (rq || row_amax || mode != SQ_EPI_NONE)) return SQ_ERR_INVALID_ARG;
+    const int64_t width = gated ? gated->F : N;  // of Y's rows
     if ((rq || row_amax) && mode == SQ_EPI_RAW_I32) return SQ_ERR_INVALID_ARG;
     if (rq && row_amax) return SQ_ERR_INVALID_ARG;
     sq_status rc = get_encoder();
@@ -1654,7 +1745,7 @@ sq_status launch_gemm_tc(const __nv_bfloat16 *Xop, const float *sx, const int32_
     args.N = (int)N;
     // TMA staging for Y (and the residual) needs 16-byte rows and aligned bases;
     // the vector loads of the scales and bias need them aligned too
-    args.tma_io = (N % 4 == 0) && (rq || aligned16(Y)) &&
+    args.tma_io = (width % 4 == 0) && (rq || aligned16(Y)) &&
                   (mode == SQ_EPI_RAW_I32 || aligned16(sw)) &&
                   (bias == nullptr || aligned16(bias)) &&
                   (residual == nullptr || aligned16(residual));
@@ -1662,6 +1753,7 @@ sq_status launch_gemm_tc(const __nv_bfloat16 *Xop, const float *sx, const int32_
     args.rq_vec = rq && N % 16 == 0 && (!rq->Yq || aligned16(rq->Yq)) &&
                   (!rq->Yop || aligned16(rq->Yop));
     args.rq_fast = rq && rq->scale >= 0x1p-70f;
+    args.gt = gated ? *gated : GatedOut{};
     args.rm_pairs = reinterpret_cast<const float4 *>(rm_pairs);
     args.row_amax = row_amax;
     CUtensorMap ta, tb, tbs, ty;
@@ -1691,7 +1783,7 @@ sq_status launch_gemm_tc(const __nv_bfloat16 *Xop, const float *sx, const int32_
     if (args.tma_io && !rq) {
         const CUtensorMapDataType yt = mode == SQ_EPI_RAW_I32 ? CU_TENSOR_MAP_DATA_TYPE_INT32
                                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-        if ((rc = make_map(&ty, yt, 4, Y, M, N, SLICE, SLICE)) != SQ_OK) return rc;
+        if ((rc = make_map(&ty, yt, 4, Y, M, width, SLICE, SLICE)) != SQ_OK) return rc;
     }
     const int q = rq ? kOutRequant : row_amax ? kOutRowMax : kOutPlain;
     const int k = (int)K, dev = di.device;
@@ -1707,6 +1799,8 @@ sq_status launch_gemm_tc(const __nv_bfloat16 *Xop, const float *sx, const int32_
         // the pair schedule counts its tiles (and twice that in halves) in int
         if (((M + 2 * BM - 1) / (2 * BM)) * ((N + BN - 1) / BN) > 0x3fffffff)
             return SQ_ERR_UNSUPPORTED;
+        if (gated)
+            return launch_pair_kernel<SQ_EPI_NONE, kOutGated>(ta, tbp, tbq, ty, args, k, dev, st);
         switch (mode) {
         case SQ_EPI_NONE:
             return launch_pair_mode<SQ_EPI_NONE>(ta, tbp, tbq, ty, args, k, dev, q, st);
@@ -1721,6 +1815,8 @@ sq_status launch_gemm_tc(const __nv_bfloat16 *Xop, const float *sx, const int32_
                                                                  st);
         }
     }
+    if (gated)
+        return launch_kernel<SQ_EPI_NONE, kOutGated>(ta, tb, tbs, ty, args, k, grid, dev, st);
     switch (mode) {
     case SQ_EPI_NONE: return launch_mode<SQ_EPI_NONE>(ta, tb, tbs, ty, args, k, grid, dev, q, st);
     case SQ_EPI_BIAS: return launch_mode<SQ_EPI_BIAS>(ta, tb, tbs, ty, args, k, grid, dev, q, st);
