@@ -301,6 +301,50 @@ sq_status sq_paged_attention(const float *Q, int64_t ldq, int64_t T, int64_t Hq,
                              int64_t prefix_len, float scale, float *O, void *workspace,
                              size_t workspace_bytes, void *stream);
 
+/* ---- Paged key/value cache in 8 bits ----------------------------------------- */
+
+/* The same cache with symmetric int8 rows: k_cache and v_cache int8 [num_pages][Hkv]
+ * [page_size][D], and a scale for each row, k_scale and v_scale fp32 [num_pages][Hkv]
+ * [page_size]: row r reads back as scale[r] code[r][d].  Half the bytes of a 16-bit
+ * cache (and 4 / D more for the scales).  Limits, tables and lengths as above; all four
+ * arrays 16-byte aligned. */
+
+/* sq_kv_append into it: the rotation and the queries as there (each product and sum
+ * of the rotation rounded by itself), and for a rotated key or value row x of one token
+ * and head
+ *   scale   = max_d |x[d]| / 127          (IEEE fp32 division; 1 where that is 0)
+ *   code[d] = clamp(round_half_even(x[d] / scale), -127, 127).
+ * A row with an element that is not finite is stored as codes of 0 with scale NaN.
+ * Two tokens of one call with the same page and row leave one of the two's codes in
+ * each group of 4 codes, and one of their scales. */
+sq_status sq_kv_append_i8(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                          const float *rope, int64_t rope_positions, int64_t rot, int interleaved,
+                          const int32_t *q_start, const int32_t *kv_len, int64_t B,
+                          const int32_t *block_table, int64_t max_pages, int8_t *k_cache,
+                          int8_t *v_cache, float *k_scale, float *v_scale, int64_t num_pages,
+                          int64_t page_size, float *Q, int64_t ldq, void *stream);
+
+/* sq_paged_attention over it: the attention over the rows that the cache reads back as.
+ * Everything said there holds, with these differences.  Codes enter the tensor cores as
+ * they are (as fp16 numbers, exactly), fp32 queries and the products of probabilities
+ * and value scales as two fp16 numbers each, a row's largest scaled near the top of
+ * fp16's range: within 2^-22, or 2^-32 of the row's largest (or 2^-130), and so O agrees
+ * with the exact attention over the rows as sq_paged_attention's does for an fp16 cache,
+ * whatever the scales' range within a row's keys is (weights below 2^-100 of the largest
+ * may count as 0).  Key scales are 2^96 at most, larger ones may leave the rows that see
+ * them not finite.  Keys and values that a row does not see do not reach it, whatever their
+ * codes and scales are; a key or value row that it sees whose scale is not finite leaves
+ * the whole row not finite (a key's infinite scale may count as no weight).
+ * workspace: as for sq_paged_attention, of sq_paged_attention_workspace_bytes. */
+sq_status sq_paged_attention_i8(const float *Q, int64_t ldq, int64_t T, int64_t Hq, int64_t Hkv,
+                                int64_t D, const int8_t *k_cache, const int8_t *v_cache,
+                                const float *k_scale, const float *v_scale, int64_t num_pages,
+                                int64_t page_size, const int32_t *block_table, int64_t max_pages,
+                                const int32_t *q_start, const int32_t *kv_len, int64_t B,
+                                int64_t max_q, const int32_t *prefix_pages, int64_t prefix_len,
+                                float scale, float *O, void *workspace, size_t workspace_bytes,
+                                void *stream);
+
 /* ---- INT8 GEMM + fused dequantising epilogue ------------------------------ */
 
 /* acc[m][n] = sum_k Xq[m][k] * Wq[n][k], exact in int32, then the epilogue

@@ -33,6 +33,7 @@ EXPORTS = ("sq_status_string", "sq_version", "sq_operand_bytes", "sq_packed_weig
            "sq_linear_block_host",
            "sq_rmsnorm_quant", "sq_rope_table", "sq_kv_append",
            "sq_paged_attention_workspace_bytes", "sq_paged_attention",
+           "sq_kv_append_i8", "sq_paged_attention_i8",
            "sq_gated_rows", "sq_pack_gated_weight", "sq_gated_workspace_bytes",
            "sq_linear_i8_gated",
            "sq_check_division", "sq_device_status", "sq_get_device_status")
@@ -91,6 +92,11 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                 "sq_paged_attention": ([vp, i64, i64, i64, i64, i64, vp, vp, i32, i64, i64, vp,
                                         i64, vp, vp, i64, i64, vp, i64, f32, vp, vp,
                                         ctypes.c_size_t, vp], i32),
+                "sq_kv_append_i8": ([vp, i64, i64, i64, i64, vp, i64, i64, i32, vp, vp, i64, vp,
+                                     i64, vp, vp, vp, vp, i64, i64, vp, i64, vp], i32),
+                "sq_paged_attention_i8": ([vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, i64, i64,
+                                           vp, i64, vp, vp, i64, i64, vp, i64, f32, vp, vp,
+                                           ctypes.c_size_t, vp], i32),
                 "sq_gated_rows": ([i64], i64),
                 "sq_pack_gated_weight": ([vp, vp, vp, i64, i64, vp, vp, vp, vp], i32),
                 "sq_gated_workspace_bytes": ([i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)],
@@ -405,13 +411,22 @@ def rope_table(inv_freq: torch.Tensor, positions: int, out=None, stream=None) ->
 
 
 CACHE_BF16, CACHE_F16 = 0, 1
-_CACHE_TYPES = {torch.bfloat16: CACHE_BF16, torch.float16: CACHE_F16}
+_CACHE_I8 = 2  # (not a type of the C interface: its int8 calls are functions of their own)
+_CACHE_TYPES = {torch.bfloat16: CACHE_BF16, torch.float16: CACHE_F16, torch.int8: _CACHE_I8}
 
 
 def empty_kv_cache(num_pages: int, kv_heads: int, page_size: int, D: int,
                    dtype=torch.bfloat16, device="cuda"):
-    """(k_cache, v_cache) of one layer, [num_pages, kv_heads, page_size, D]."""
+    """(k_cache, v_cache) of one layer, [num_pages, kv_heads, page_size, D]; an int8 cache
+    goes with empty_kv_scales of the same sizes."""
     return tuple(torch.empty(num_pages, kv_heads, page_size, D, dtype=dtype, device=device)
+                 for _ in range(2))
+
+
+def empty_kv_scales(num_pages: int, kv_heads: int, page_size: int, device="cuda"):
+    """(k_scale, v_scale) of an int8 cache, a scale for each row: [num_pages, kv_heads,
+    page_size] fp32."""
+    return tuple(torch.empty(num_pages, kv_heads, page_size, dtype=torch.float32, device=device)
                  for _ in range(2))
 
 
@@ -431,12 +446,14 @@ def _rows_of(t: torch.Tensor, cols: int, name: str, dev, rows: Optional[int] = N
     return apart
 
 
-def _need_paged(k_cache, v_cache, block_table, q_start, kv_len):
-    """Checks the cache and the batch's tables; returns (type, pages, Hkv, page size, D, B,
-    table width) and the five addresses."""
+def _need_paged(k_cache, v_cache, block_table, q_start, kv_len, k_scale, v_scale):
+    """Checks the cache, its scales and the batch's tables; returns (type, pages, Hkv, page
+    size, D, B, table width), the five addresses, and the scales' two (none for 16 bits)."""
     ctype = _CACHE_TYPES.get(k_cache.dtype)
     if ctype is None:
-        raise ValueError(f"k_cache must be bfloat16 or float16, got {k_cache.dtype}")
+        raise ValueError(f"k_cache must be bfloat16, float16 or int8, got {k_cache.dtype}")
+    if (k_scale is None) != (ctype != _CACHE_I8) or (v_scale is None) != (ctype != _CACHE_I8):
+        raise ValueError("k_scale and v_scale go with an int8 cache, and it with both")
     if k_cache.dim() != 4:
         raise ValueError("k_cache must have shape (num_pages, kv_heads, page_size, D)")
     if kv_len.dim() != 1:
@@ -448,7 +465,11 @@ def _need_paged(k_cache, v_cache, block_table, q_start, kv_len):
     dev, i32, shape = k_cache.device, torch.int32, k_cache.shape
     pages, Hkv, page_size, D = shape
     width = block_table.shape[1]
-    return (ctype, pages, Hkv, page_size, D, B, width), (
+    scales = ()
+    if k_scale is not None:
+        scales = tuple(_arg(t, torch.float32, n, shape[:3], dev)
+                       for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")))
+    return (ctype, pages, Hkv, page_size, D, B, width), scales, (
         k_cache.data_ptr(), _arg(v_cache, k_cache.dtype, "v_cache", shape, dev),
         _arg(block_table, i32, "block_table", (B, width), dev),
         _arg(q_start, i32, "q_start", (B + 1,), dev), _arg(kv_len, i32, "kv_len", (B,), dev))
@@ -457,15 +478,18 @@ def _need_paged(k_cache, v_cache, block_table, q_start, kv_len):
 def kv_append(QKV: torch.Tensor, Hq: int, k_cache: torch.Tensor, v_cache: torch.Tensor,
               block_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
               rope: Optional[torch.Tensor] = None, interleaved: bool = False,
-              q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+              q_out: Optional[torch.Tensor] = None, stream=None,
+              k_scale: Optional[torch.Tensor] = None,
+              v_scale: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Rotates the queries and keys of the fused projection's output QKV
     [T, (Hq + 2 Hkv) * D] and appends keys and values to the paged cache;
     returns the rotated queries [T, Hq * D].  rope: rope_table's [positions, n,
     2], None for no rotation.  q_out may be the view QKV[:, :Hq * D] (in place).
     With q_out, rows of no sequence are left as they are; without it they are
-    zeros."""
-    (ctype, pages, Hkv, page_size, D, B, width), (k, v, table, starts, lens) = _need_paged(
-        k_cache, v_cache, block_table, q_start, kv_len)
+    zeros.  An int8 cache is written as codes, with its rows' scales to k_scale and
+    v_scale (empty_kv_scales)."""
+    (ctype, pages, Hkv, page_size, D, B, width), scales, (k, v, table, starts, lens) = _need_paged(
+        k_cache, v_cache, block_table, q_start, kv_len, k_scale, v_scale)
     dev, f32 = k_cache.device, torch.float32
     if QKV.dim() != 2:
         raise ValueError(f"QKV must have shape (T, {(Hq + 2 * Hkv) * D})")
@@ -482,10 +506,13 @@ def kv_append(QKV: torch.Tensor, Hq: int, k_cache: torch.Tensor, v_cache: torch.
         if q_out is None:
             q_out = torch.zeros(T, Hq * D, dtype=f32, device=dev)
         ldq = _rows_of(q_out, Hq * D, "q_out", dev, T)
-        _check((_lib or load()).sq_kv_append(qkv, T, Hq, Hkv, D, rope_at, positions, rot,
-                                   1 if interleaved else 0, starts, lens, B, table, width, k, v,
-                                   ctype, pages, page_size, q_out.data_ptr(), ldq, st),
-               "sq_kv_append")
+        front = (qkv, T, Hq, Hkv, D, rope_at, positions, rot, 1 if interleaved else 0, starts,
+                 lens, B, table, width, k, v)
+        back = (pages, page_size, q_out.data_ptr(), ldq, st)
+        if scales:
+            _check((_lib or load()).sq_kv_append_i8(*front, *scales, *back), "sq_kv_append_i8")
+        else:
+            _check((_lib or load()).sq_kv_append(*front, ctype, *back), "sq_kv_append")
     return q_out
 
 
@@ -504,16 +531,18 @@ def paged_attention(Q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                     max_q: Optional[int] = None, prefix_pages: Optional[torch.Tensor] = None,
                     prefix_len: int = 0, scale: Optional[float] = None,
                     workspace: Optional[torch.Tensor] = None,
-                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                    out: Optional[torch.Tensor] = None, stream=None,
+                    k_scale: Optional[torch.Tensor] = None,
+                    v_scale: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Causal attention of the rows Q [T, Hq * D] (kv_append's queries; rows may
     lie apart) over the paged cache -> [T, Hq * D].  Positions below prefix_len
     come from prefix_pages for every sequence.  max_q: the most tokens of a
     sequence (T if not given).  workspace: a zero-filled uint8 tensor that one
     call at a time uses (empty_workspace(paged_attention_workspace_bytes(...)));
     a fresh one is made if None.  With `out`, rows of no sequence are left as
-    they are; without it they are zeros."""
-    (ctype, pages, Hkv, page_size, D, B, width), (k, v, table, starts, lens) = _need_paged(
-        k_cache, v_cache, block_table, q_start, kv_len)
+    they are; without it they are zeros.  An int8 cache goes with its rows' scales."""
+    (ctype, pages, Hkv, page_size, D, B, width), scales, (k, v, table, starts, lens) = _need_paged(
+        k_cache, v_cache, block_table, q_start, kv_len, k_scale, v_scale)
     dev = k_cache.device
     if Q.dim() != 2 or Q.shape[1] % D != 0 or Q.shape[1] == 0:
         raise ValueError(f"Q must have shape (T, heads * {D}), got {tuple(Q.shape)}")
@@ -534,12 +563,18 @@ def paged_attention(Q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         if workspace is None:
             workspace = empty_workspace(
                 paged_attention_workspace_bytes(T, Hq, Hkv, D, prefix_len), dev)
-        _check((_lib or load()).sq_paged_attention(
-            Q.data_ptr(), ldq, T, Hq, Hkv, D, k, v, ctype, pages, page_size, table, width, starts,
-            lens, B, T if max_q is None else int(max_q), pages_at, int(prefix_len), float(scale),
-            _arg(out, torch.float32, "out", (T, Hq * D), dev),
-            _arg(workspace, torch.uint8, "workspace", workspace.shape, dev), workspace.numel(),
-            st), "sq_paged_attention")
+        front = (Q.data_ptr(), ldq, T, Hq, Hkv, D, k, v)
+        back = (pages, page_size, table, width, starts, lens, B,
+                T if max_q is None else int(max_q), pages_at, int(prefix_len), float(scale),
+                _arg(out, torch.float32, "out", (T, Hq * D), dev),
+                _arg(workspace, torch.uint8, "workspace", workspace.shape, dev),
+                workspace.numel(), st)
+        if scales:
+            _check((_lib or load()).sq_paged_attention_i8(*front, *scales, *back),
+                   "sq_paged_attention_i8")
+        else:
+            _check((_lib or load()).sq_paged_attention(*front, ctype, *back),
+                   "sq_paged_attention")
     return out
 
 

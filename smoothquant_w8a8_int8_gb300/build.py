@@ -23,7 +23,7 @@ OBJ_DIR = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "quantize.cu", "gemm_mma.cu", "gemm_tc.cu", "selfcheck.cu", "static_ws.cu",
            "attention.cu", "host_pipeline.cu", "rmsnorm.cu", "kv_cache.cu", "paged_attention.cu",
-           "paged_rows.cu", "paged_tiles.cu", "gated.cu"]
+           "paged_rows.cu", "paged_tiles.cu", "gated.cu", "kv_cache_i8.cu", "paged_rows_i8.cu"]
 
 
 def nvcc() -> str:

@@ -128,6 +128,54 @@ sq_status require_gb300() { return require_sm103(); }
 
 namespace {
 
+// The appends' arguments apart from the shape; *empty: a valid call without work.
+sq_status check_append(const float *QKV, int64_t T, int64_t D, const float *rope,
+                       int64_t rope_positions, int64_t rot, const int32_t *q_start,
+                       const int32_t *kv_len, int64_t B, const int32_t *block_table,
+                       const void *k_cache, const void *v_cache, int64_t num_pages,
+                       const float *Q, bool *empty) {
+    if (rot < 0 || rot > D || rope_positions < 0) return SQ_ERR_INVALID_ARG;
+    if (rot % 8 != 0) return SQ_ERR_ALIGNMENT;
+    *empty = T == 0 || B == 0;
+    if (*empty) return SQ_OK;
+    if (num_pages == 0 || !QKV || !q_start || !kv_len || !block_table || !k_cache || !v_cache || !Q ||
+        (rot > 0 && !rope))
+        return SQ_ERR_INVALID_ARG;
+    if (!aligned16(QKV) || !aligned16(Q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        (rot > 0 && !aligned16(rope)) || !aligned4(q_start) || !aligned4(kv_len) ||
+        !aligned4(block_table))
+        return SQ_ERR_ALIGNMENT;
+    return SQ_OK;
+}
+
+// The scales of an int8 cache (read 16 bytes at a time).
+sq_status check_cache_scales(const float *k_scale, const float *v_scale) {
+    if (!k_scale || !v_scale) return SQ_ERR_INVALID_ARG;
+    return aligned16(k_scale) && aligned16(v_scale) ? SQ_OK : SQ_ERR_ALIGNMENT;
+}
+
+// The attentions' other checks, and the call.
+sq_status attention_impl(const PagedCall &c, size_t workspace_bytes, void *stream) {
+    if (!(fabsf(c.scale) <= 0x1p127f)) return SQ_ERR_INVALID_ARG;  // (times log2 e it is finite)
+    if (c.max_q < 0 || c.prefix_len < 0) return SQ_ERR_INVALID_ARG;
+    if (c.prefix_len > (int64_t)1 << 30) return SQ_ERR_UNSUPPORTED;
+    if (c.T == 0 || c.B == 0) return SQ_OK;
+    if (c.num_pages == 0 || !c.Q || !c.q_start || !c.kv_len || !c.block_table || !c.k_cache ||
+        !c.v_cache || !c.O || !c.workspace || (c.prefix_len > 0 && !c.prefix_pages))
+        return SQ_ERR_INVALID_ARG;
+    if (!aligned16(c.Q) || !aligned16(c.O) || !aligned16(c.k_cache) || !aligned16(c.v_cache) ||
+        !aligned16(c.workspace) || !aligned4(c.q_start) || !aligned4(c.kv_len) ||
+        !aligned4(c.block_table) || (c.prefix_len > 0 && !aligned4(c.prefix_pages)))
+        return SQ_ERR_ALIGNMENT;
+    sq_status rc = c.cache_type == kCacheI8 ? check_cache_scales(c.k_scale, c.v_scale) : SQ_OK;
+    if (rc != SQ_OK) return rc;
+    if ((rc = require_sm103()) != SQ_OK) return rc;
+    size_t need = 0;
+    if ((rc = paged_workspace_bytes(c.T, c.Hq, c.D, c.prefix_len, &need)) != SQ_OK) return rc;
+    if (workspace_bytes < need) return SQ_ERR_INVALID_ARG;
+    return launch_paged_attention(c, as_stream(stream));
+}
+
 sq_status linear_impl(const void *Xop, const float *x_scale, const int32_t *x_row_l1,
                       const void *Wop, const float *w_scale, const int32_t *w_row_l1,
                       const float *bias, const float *residual, int64_t M, int64_t N, int64_t K,
@@ -414,20 +462,34 @@ sq_status sq_kv_append(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv, int
     sq_status rc = check_paged_shape(T, Hq, Hkv, D, cache_type, num_pages, page_size, B,
                                      max_pages, ldq);
     if (rc != SQ_OK) return rc;
-    if (rot < 0 || rot > D || rope_positions < 0) return SQ_ERR_INVALID_ARG;
-    if (rot % 8 != 0) return SQ_ERR_ALIGNMENT;
-    if (T == 0 || B == 0) return SQ_OK;
-    if (num_pages == 0 || !QKV || !q_start || !kv_len || !block_table || !k_cache || !v_cache || !Q ||
-        (rot > 0 && !rope))
-        return SQ_ERR_INVALID_ARG;
-    if (!aligned16(QKV) || !aligned16(Q) || !aligned16(k_cache) || !aligned16(v_cache) ||
-        (rot > 0 && !aligned16(rope)) || !aligned4(q_start) || !aligned4(kv_len) ||
-        !aligned4(block_table))
-        return SQ_ERR_ALIGNMENT;
+    bool empty = false;
+    rc = check_append(QKV, T, D, rope, rope_positions, rot, q_start, kv_len, B, block_table, k_cache,
+                      v_cache, num_pages, Q, &empty);
+    if (rc != SQ_OK || empty) return rc;
     if ((rc = require_sm103()) != SQ_OK) return rc;
     return launch_kv_append(QKV, T, Hq, Hkv, D, rope, rope_positions, rot, interleaved ? 1 : 0,
                             q_start, kv_len, B, block_table, max_pages, k_cache, v_cache,
                             cache_type, num_pages, page_size, Q, ldq, as_stream(stream));
+}
+
+sq_status sq_kv_append_i8(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                          const float *rope, int64_t rope_positions, int64_t rot, int interleaved,
+                          const int32_t *q_start, const int32_t *kv_len, int64_t B,
+                          const int32_t *block_table, int64_t max_pages, int8_t *k_cache,
+                          int8_t *v_cache, float *k_scale, float *v_scale, int64_t num_pages,
+                          int64_t page_size, float *Q, int64_t ldq, void *stream) {
+    sq_status rc = check_paged_shape(T, Hq, Hkv, D, SQ_CACHE_BF16, num_pages, page_size, B,
+                                     max_pages, ldq);
+    if (rc != SQ_OK) return rc;
+    bool empty = false;
+    rc = check_append(QKV, T, D, rope, rope_positions, rot, q_start, kv_len, B, block_table, k_cache,
+                      v_cache, num_pages, Q, &empty);
+    if (rc != SQ_OK || empty) return rc;
+    if ((rc = check_cache_scales(k_scale, v_scale)) != SQ_OK) return rc;
+    if ((rc = require_sm103()) != SQ_OK) return rc;
+    return launch_kv_append_i8(QKV, T, Hq, Hkv, D, rope, rope_positions, rot, interleaved ? 1 : 0,
+                               q_start, kv_len, B, block_table, max_pages, k_cache, v_cache,
+                               k_scale, v_scale, num_pages, page_size, Q, ldq, as_stream(stream));
 }
 
 sq_status sq_paged_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
@@ -451,26 +513,29 @@ sq_status sq_paged_attention(const float *Q, int64_t ldq, int64_t T, int64_t Hq,
     sq_status rc = check_paged_shape(T, Hq, Hkv, D, cache_type, num_pages, page_size, B,
                                      max_pages, ldq);
     if (rc != SQ_OK) return rc;
-    if (!(fabsf(scale) <= 0x1p127f)) return SQ_ERR_INVALID_ARG;  // (times log2 e it is finite)
-    if (max_q < 0 || prefix_len < 0) return SQ_ERR_INVALID_ARG;
-    if (prefix_len > (int64_t)1 << 30) return SQ_ERR_UNSUPPORTED;
-    if (T == 0 || B == 0) return SQ_OK;
-    if (num_pages == 0 || !Q || !q_start || !kv_len || !block_table || !k_cache || !v_cache || !O || !workspace ||
-        (prefix_len > 0 && !prefix_pages))
-        return SQ_ERR_INVALID_ARG;
-    if (!aligned16(Q) || !aligned16(O) || !aligned16(k_cache) || !aligned16(v_cache) ||
-        !aligned16(workspace) || !aligned4(q_start) || !aligned4(kv_len) ||
-        !aligned4(block_table) || (prefix_len > 0 && !aligned4(prefix_pages)))
-        return SQ_ERR_ALIGNMENT;
-    if ((rc = require_sm103()) != SQ_OK) return rc;
-    size_t need = 0;
-    if ((rc = paged_workspace_bytes(T, Hq, D, prefix_len, &need)) != SQ_OK) return rc;
-    if (workspace_bytes < need) return SQ_ERR_INVALID_ARG;
     const PagedCall c = {Q,         ldq,         T,         Hq,      Hkv,          D,
                          k_cache,   v_cache,     cache_type, num_pages, page_size,  block_table,
                          max_pages, q_start,     kv_len,    B,       max_q,        prefix_pages,
-                         prefix_len, scale,      O,         workspace};
-    return launch_paged_attention(c, as_stream(stream));
+                         prefix_len, scale,      O,         workspace, nullptr,     nullptr};
+    return attention_impl(c, workspace_bytes, stream);
+}
+
+sq_status sq_paged_attention_i8(const float *Q, int64_t ldq, int64_t T, int64_t Hq, int64_t Hkv,
+                                int64_t D, const int8_t *k_cache, const int8_t *v_cache,
+                                const float *k_scale, const float *v_scale, int64_t num_pages,
+                                int64_t page_size, const int32_t *block_table, int64_t max_pages,
+                                const int32_t *q_start, const int32_t *kv_len, int64_t B,
+                                int64_t max_q, const int32_t *prefix_pages, int64_t prefix_len,
+                                float scale, float *O, void *workspace, size_t workspace_bytes,
+                                void *stream) {
+    sq_status rc = check_paged_shape(T, Hq, Hkv, D, SQ_CACHE_BF16, num_pages, page_size, B,
+                                     max_pages, ldq);
+    if (rc != SQ_OK) return rc;
+    const PagedCall c = {Q,         ldq,         T,         Hq,      Hkv,          D,
+                         k_cache,   v_cache,     kCacheI8,  num_pages, page_size,  block_table,
+                         max_pages, q_start,     kv_len,    B,       max_q,        prefix_pages,
+                         prefix_len, scale,      O,         workspace, k_scale,    v_scale};
+    return attention_impl(c, workspace_bytes, stream);
 }
 
 sq_status sq_linear_i8(const void *Xop, const float *x_scale, const int32_t *x_row_l1,

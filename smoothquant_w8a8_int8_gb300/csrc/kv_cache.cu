@@ -12,7 +12,7 @@
 // Memory-bound: every projected element is read once and written once.  Measured:
 // 7976 tokens of 32 / 8 heads of 128, bf16: 54 us, 6.8 TB/s, the measured copy
 // rate; 64 tokens 5 us, latency.
-#include "decoder.cuh"
+#include "kv_tokens.cuh"
 
 #include <cuda_fp16.h>
 
@@ -35,24 +35,6 @@ __global__ void rope_table_kernel(const float *__restrict__ inv_freq, int64_t to
         sincos((double)(i / half) * (double)inv_freq[i % half], &sn, &cs);
         table[i] = make_float2((float)cs, (float)sn);
     }
-}
-
-// The number of e in [1, B] with q_start[e] <= t: the sequence that token t
-// belongs to (B: behind the last one).  Called by whole warps with one t.
-__device__ __forceinline__ int token_sequence(const int *__restrict__ q_start, int B, int t,
-                                              int lane) {
-    int lo = 0, n = B;  // the answer lies in [lo, lo + n]
-    while (n > 0) {
-        const int step = (n + 31) / 32;
-        const int e = lo + min(n, (lane + 1) * step);  // probes q_start[e], non-decreasing
-        const unsigned below = __ballot_sync(0xffffffffu, __ldg(q_start + e) <= t);
-        const int c = __popc(below);
-        // probes 0..c-1 are <= t
-        const int at = c ? min(n, c * step) : 0;
-        lo += at;
-        n = c == 32 ? 0 : min(n - at, step - 1);
-    }
-    return lo;
 }
 
 template <bool BF>

@@ -27,6 +27,12 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // fp16's range, the largest into [2^7, 2^15) (fp16 ends at 65504, so the octave
 // below 2^16 would round to infinity at its end); tiny and zero rows as if e = -32.
 __device__ __forceinline__ int shift_of(int e) { return (max(e, -32) - 7) & ~7; }
+// The same for queries of an int8 cache, whose keys are as large as their scales:
+// down to e = -100, as long as `scale` (a power of two) times the factor stays normal.
+__device__ __forceinline__ int shift_of_wide(int e, float scale) {
+    const int least = 1 - (int)(__float_as_uint(scale) >> 23);  // of a normal product
+    return max((max(e, -100) - 7) & ~7, (least + 7) & ~7);
+}
 
 // N pairs of 16-bit numbers of the cache's type that sum to (a, b), a in the
 // low half.  Three bf16 numbers hold an fp32 number exactly: each takes the
@@ -52,6 +58,18 @@ __device__ __forceinline__ void split16(float a, float b, uint32_t (&w)[N]) {
             b -= __high2float(h);
         }
     }
+}
+
+// Codes as fp16 numbers, exactly: code + 128 in the low byte of 0x6400 is 1024 + code +
+// 128, from which 1152 is taken away, two at a time.  bytes: codes + 128 (each code's
+// highest bit turned); select: the bytes that are taken, in turn with 0x64.
+constexpr uint32_t kCodesLow = 0x4140, kCodesHigh = 0x4342, kCodeBias = 0x80808080u;
+__device__ __forceinline__ uint32_t fp16_codes(uint32_t bytes, uint32_t select) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;"
+        : "=r"(r)
+        : "r"(__byte_perm(bytes, 0x64646464u, select)), "r"(0x64806480u));
+    return r;
 }
 
 // 16 bytes of global memory into shared memory, asynchronously, or zeros
@@ -194,11 +212,14 @@ __device__ __forceinline__ float *row_target(const PagedArgs &a) {
 
 }  // namespace
 
-// The kernel for at most 16 rows per item (paged_rows.cu): rows = 8 or 16.
+// The kernels for at most 16 rows per item (paged_rows_i8.cu, paged_rows.cu): rows = 8
+// or 16.
+sq_status launch_paged_rows_i8(const PagedArgs &a, const void *k_cache, const void *v_cache, int D,
+                               int rows, int sms, cudaStream_t st);
 sq_status launch_paged_rows(const PagedArgs &a, const void *k_cache, const void *v_cache, int D,
                             bool bf16, int rows, int sms, cudaStream_t st);
 // The kernel for up to 128 rows per item (paged_tiles.cu).
 sq_status launch_paged_tiles(const PagedArgs &a, const void *k_cache, const void *v_cache, int D,
-                             bool bf16, int sms, cudaStream_t st);
+                             int cache_type, int sms, cudaStream_t st);
 
 }  // namespace sq

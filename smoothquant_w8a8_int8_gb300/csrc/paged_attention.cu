@@ -130,7 +130,9 @@ sq_status launch_paged_attention(const PagedCall &c, cudaStream_t st) {
     exponent = std::min(exponent, 127);
     a.scale = ldexpf(1.0f, exponent);
     a.q_factor = scale < 0x1p-100f ? 0.0f : copysignf(ldexpf(scale, -exponent), c.scale);
-    const bool bf16 = c.cache_type == SQ_CACHE_BF16;
+    a.k_scale = c.k_scale;
+    a.v_scale = c.v_scale;
+    const bool bf16 = c.cache_type == SQ_CACHE_BF16, i8 = c.cache_type == kCacheI8;
     const int64_t max_q = std::min(c.max_q, c.T), tokens = std::min(c.T, max_q * c.B);
     const bool front = c.prefix_len > 0 && prefix_in_front(a, max_q, tokens, di.sms);
     for (int phase = c.prefix_len > 0 && !front ? 1 : 0; phase >= 0; --phase) {
@@ -149,8 +151,9 @@ sq_status launch_paged_attention(const PagedCall &c, cudaStream_t st) {
         const int64_t tiles = (c.T + a.tpt - 1) / a.tpt + (phase ? 0 : c.B);
         const int64_t keys = ((phase ? 0 : c.max_pages * c.page_size) + c.prefix_len) / kt + 16;
         if (tiles * c.Hkv > ((int64_t)1 << 31) / keys) return SQ_ERR_UNSUPPORTED;
-        rc = few ? launch_paged_rows(a, c.k_cache, c.v_cache, (int)c.D, bf16, r, di.sms, st)
-                 : launch_paged_tiles(a, c.k_cache, c.v_cache, (int)c.D, bf16, di.sms, st);
+        rc = !few ? launch_paged_tiles(a, c.k_cache, c.v_cache, (int)c.D, c.cache_type, di.sms, st)
+             : i8 ? launch_paged_rows_i8(a, c.k_cache, c.v_cache, (int)c.D, r, di.sms, st)
+                  : launch_paged_rows(a, c.k_cache, c.v_cache, (int)c.D, bf16, r, di.sms, st);
         if (rc != SQ_OK) return rc;
     }
     return SQ_OK;

@@ -51,6 +51,7 @@ struct PagedArgs {
     float scale;         // a power of two; times q_factor the call's scale times log2 e
     float q_factor;      // what the queries are multiplied by, 0 for a scale of zero
     int prefix_phase;    // 1: every token over the prefix, into prefix_o / prefix_ml
+    const float *k_scale, *v_scale;  // an int8 cache's: [cache rows]
     int after_prefix;    // 1: the few rows' launch behind that one (see begin_rows)
 };
 

@@ -1,0 +1,514 @@
+// Attention over the paged int8 cache for few query rows per key/value head: the
+// single tokens and short drafts of a decoding step.
+//
+// A cached key row is k_scale codes, a value row v_scale codes, so with y = Q . codes
+//   logit = y k_scale,  p = 2^(logit - m),  l += p,  O += (p v_scale) codes:
+// the scales stand at the logits and the probabilities, the codes enter the products
+// as they are.  The rest is paged_rows.cu's: a worker is a warp with a ring of its own,
+// filled with cp.async by steps of 16 keys, products on the warp-level tensor
+// instructions (m16n8k16), the running maximum, the pieces' join.
+//
+// Half the cache's bytes per key leave half the time for each, so the codes' way into
+// the instruction's operands is kept short.  Which element of the contraction stands
+// where in an operand is free, as long as both operands agree:
+//   keys: thread t of a row's four takes the 16 bytes of chunk t (and t + 4) with one
+//     load, four elements of them per instruction; the queries lie to match;
+//   values: column n of an instruction's result is element D/8 n + i in its i-th
+//     instruction, so that a thread's columns of all of them are 16 (8) bytes in a row.
+// Codes become fp16 numbers exactly: a byte code + 128 in the low half of 0x6400 is
+// 1024 + code + 128, from which 1152 is taken away, two codes at a time.
+//
+// Precision: codes are exact in fp16; fp32 queries and weights p v_scale are sums of two
+// fp16 numbers, each row scaled by a power of two so that its largest is within
+// [2^7, 2^15) (queries) and [2^14, 2^15) (a step's weights), and what is 2^-37 of the
+// row's largest weight still counts.  Logits are multiplied by a power of two as in
+// paged_rows.cu.
+#include "paged_rows.cuh"
+
+#include <algorithm>
+#include <mutex>
+
+namespace sq {
+namespace {
+
+constexpr int kKT = 16;  // keys per step
+constexpr int kWarps = 8;
+constexpr int kPad = 2;       // an item's start and end, in steps
+constexpr int kMinSteps = 4;  // steps of a worker's share at least
+constexpr int kJoin = 16;     // pieces of an item that are joined in one go
+constexpr int kPieces = 16;   // more than the steps that the copies are ahead
+
+template <int D>
+struct RowsI8Cfg {
+    static constexpr int kCodes = kKT * D;                       // bytes of the keys or values
+    static constexpr int kStepBytes = 2 * kCodes + 2 * kKT * 4;  // and both scales
+    static constexpr int kStages = D == 128 ? 6 : 10;
+    static constexpr int kSmem = kWarps * kStages * kStepBytes;
+    static_assert(kStages < kPieces, "a piece per step in flight and the one being worked on");
+};
+
+// Byte offset of 16-byte chunk `ch` of row r: the reads below (four chunks of two
+// neighbouring rows; two chunks of four rows of one parity) meet every bank once.
+template <int D>
+__device__ __forceinline__ int place(int r, int ch) {
+    if (D == 128) return r * 128 + ((ch ^ ((r >> 1 & 3) << 1) ^ ((r & 1) << 2)) << 4);
+    const int line = r >> 1;
+    return line * 128 + ((((r & 1) << 2 | ch) ^ ((line & 3) << 1)) << 4);
+}
+
+__device__ __forceinline__ float2 lds_f2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    paged_rows_i8_kernel(const __grid_constant__ PagedArgs a, const int8_t *__restrict__ k_cache,
+                         const int8_t *__restrict__ v_cache) {
+    using C = RowsI8Cfg<D>;
+    using F = Parts<false, ROWS>;
+    constexpr int ST = C::kStages, R = F::kRows, S = F::kSets;
+    constexpr int NT = D / 8;  // a thread's columns of each of its two column groups
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Share shares[kWarps];
+    __shared__ Piece pieces[kWarps][kPieces];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    begin_rows(a);
+    find_shares<kKT, kPad, kWarps * 32, kWarps>(a, kMinSteps, shares);
+    const Share &share = shares[warp];
+    const int worker = warp * gridDim.x + blockIdx.x;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * ST * C::kStepBytes;
+
+    // ---- the copies: one step of the share per call, or nothing at its end
+    Walk<kKT, kPad> walk;
+    walk.start(a, share);
+    int npieces = 0, left = 0, key = 0, held = -1, entry = -1;
+    int buf = 0;  // the ring's buffer that is filled next
+    int64_t head_row = 0;  // the piece's head, in cache rows of a page
+    int keys = 0;
+    unsigned holes = 0;    // bit i: the page of the step in buffer i is missing
+    const int *table = nullptr;
+    auto copy_step = [&]() {
+        if (left == 0) {
+            Piece p;
+            if (walk.next(a, share, p)) {
+                if (lane == 0) pieces[warp][npieces % kPieces] = p;
+                ++npieces;
+                left = p.ntiles;
+                key = p.key0;
+                keys = p.keys;
+                head_row = (int64_t)p.head << a.page_shift;
+                table = a.block_table + (int64_t)p.seq * a.max_pages;
+                held = -1;
+            }
+        }
+        if (left > 0) {
+            // lane i holds the page-table entry 32 held + i
+            const KeyRange kr = key_range(a, key, keys);
+            const int idx = kr.key >> a.page_shift;
+            if (idx >> 5 != held || key == a.kstart) {
+                held = idx >> 5;
+                const int at = (held << 5) + lane;
+                entry = (int64_t)at << a.page_shift < kr.hi
+                            ? __ldg((kr.front ? a.prefix_pages : table) + at)
+                            : -1;
+            }
+            const int e = __shfl_sync(0xffffffffu, entry, idx & 31);
+            const bool there = e >= 0 && e < a.num_pages;
+            holes = (holes & ~(1u << buf)) | (there ? 0u : 1u << buf);
+            const int64_t row0 = (there ? (((int64_t)e * a.Hkv) << a.page_shift) + head_row : 0) +
+                                 (kr.key & ((1 << a.page_shift) - 1));
+            // lane: chunk lane % kLanes of row lane / kLanes of every kStride rows; the
+            // step's 16 rows are contiguous in the cache.  (Rows of no key are masked
+            // whatever they hold: codes are finite.)
+            constexpr int kLanes = D / 16, kCopies = C::kCodes / 512, kStride = 32 / kLanes;
+            const int r0 = lane / kLanes, ch = lane % kLanes;
+            const uint32_t dst = ring + buf * C::kStepBytes;
+            const int8_t *ks = k_cache + row0 * D + lane * 16, *vs = v_cache + row0 * D + lane * 16;
+#pragma unroll
+            for (int j = 0; j < kCopies; ++j) {
+                const uint32_t d = dst + place<D>(r0 + j * kStride, ch);
+                copy16(d, ks + j * 512, there);
+                copy16(d + C::kCodes, vs + j * 512, there);
+            }
+            if (lane < 2 * kKT / 4)
+                copy16(dst + 2 * C::kCodes + lane * 16,
+                       (lane < kKT / 4 ? a.k_scale : a.v_scale) + row0 + lane % (kKT / 4) * 4,
+                       there);
+            key += kKT;
+            --left;
+        }
+        if (++buf == ST) buf = 0;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < ST - 1; ++i) copy_step();
+    end_of_prefix(a);
+    __syncwarp();
+
+    const int g = lane >> 2, t = lane & 3;  // fragment row and column pair
+    int cur = 0;  // the ring's buffer of the step
+    for (int n = 0; n < npieces; ++n) {
+        const Piece p = pieces[warp][n % kPieces];
+        // this thread's rows of the item: g and, of 16, g + 8
+        int tok[R], limit[R];
+        bool live[R];
+        const float *qrow[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int row = g + 8 * i;
+            tok[i] = row / a.G;
+            live[i] = tok[i] < p.ntok;
+            limit[i] = live[i] ? row_limit(a, p, tok[i]) : p.keys;
+            qrow[i] = a.Q + (int64_t)(p.tok0 + tok[i]) * a.ldq +
+                      (p.head * a.G + row % a.G) * D + 16 * t;
+        }
+        auto out_row = [&](int r) {
+            return (int64_t)(p.tok0 + tok[r]) * a.Hq + p.head * a.G + (g + 8 * r) % a.G;
+        };
+        // elements 64 c + 16 t + 4 i .. + 3 of row r's query
+        auto query = [&](int r, int c, int i) {
+            return live[r] ? *reinterpret_cast<const float4 *>(qrow[r] + 64 * c + 4 * i)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        float mul[R], scale[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const float4 q = query(r, i / 4, i % 4);
+                top = fmaxf(top, fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w))));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            top *= fabsf(a.q_factor);
+            const int sh = shift_of_wide((int)(__float_as_uint(top) >> 23) - 127, a.scale);
+            mul[r] = a.q_factor * pow2(-sh);
+            scale[r] = a.scale * pow2(sh);
+        }
+        uint32_t qf[D / 16][S][4];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            float x[2][R][2];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float4 q = query(r, i / 4, i % 4);
+                x[0][r][0] = q.x * mul[r];
+                x[0][r][1] = q.y * mul[r];
+                x[1][r][0] = q.z * mul[r];
+                x[1][r][1] = q.w * mul[r];
+            }
+            F::fill(x[0], 0, qf[i]);
+            F::fill(x[1], 2, qf[i]);
+        }
+        // o[i][2 r + q]: row r's element NT (2 t + q) + i
+        float o[NT][2 * R], m[R], l[R];
+        auto each_column = [&](auto &&f) {  // f(i of four columns, q, their first)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < NT; i += 4) f(i, q, NT * (2 * t + q) + i);
+        };
+#pragma unroll
+        for (int i = 0; i < NT * 2 * R; ++i) o[i / (2 * R)][i % (2 * R)] = 0.0f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.0f;
+            if (live[r] && starts_with_prefix(a, p)) {
+                const int64_t row = out_row(r);
+                const float2 f = __ldcg(a.prefix_ml + row);
+                m[r] = f.x;
+                l[r] = t == 0 ? f.y : 0.0f;  // (the row's four threads' sums are added)
+                each_column([&](int i, int q, int d) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.prefix_o + row * D + d));
+                    o[i][2 * r + q] = v.x;
+                    o[i + 1][2 * r + q] = v.y;
+                    o[i + 2][2 * r + q] = v.z;
+                    o[i + 3][2 * r + q] = v.w;
+                });
+            }
+        }
+        int key0 = p.key0;
+        for (int it = 0; it < p.ntiles; ++it, key0 += kKT) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
+            __syncwarp();
+            const uint32_t ks = ring + cur * C::kStepBytes;
+            const uint32_t vs = ks + C::kCodes, sc = ks + 2 * C::kCodes;
+            // logits of the rows x 16 keys
+            float s[2][2][4];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i >> 3][i >> 2 & 1][i & 3] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                uint32_t w[2][4];
+                lds4(w[0], ks + place<D>(g, t + 4 * c));
+                lds4(w[1], ks + place<D>(g + 8, t + 4 * c));
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t b = w[h][i] ^ kCodeBias;
+                        const uint32_t b0 = fp16_codes(b, kCodesLow), b1 = fp16_codes(b, kCodesHigh);
+#pragma unroll
+                        for (int j = 0; j < S; ++j)
+                            mma16816<false>(s[i & 1][h], qf[4 * c + i][j], b0, b1);
+                    }
+            }
+            // x[row][key]: keys 2t, 2t + 1, 2t + 8, 2t + 9 of the step
+            float x[R][4], kf[4], vf[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 k2 = lds_f2(sc + (8 * h + 2 * t) * 4);
+                const float2 v2 = lds_f2(sc + (kKT + 8 * h + 2 * t) * 4);
+                kf[2 * h] = k2.x;
+                kf[2 * h + 1] = k2.y;
+                vf[2 * h] = v2.x;
+                vf[2 * h + 1] = v2.y;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float c0 = s[0][e >> 1][e & 1] + s[1][e >> 1][e & 1];
+                const float c1 = s[0][e >> 1][2 + (e & 1)] + s[1][e >> 1][2 + (e & 1)];
+                if (R == 1) x[0][e] = (c0 + c1) * kf[e];
+                else x[0][e] = c0 * kf[e], x[R - 1][e] = c1 * kf[e];
+            }
+            // keys that are masked: behind the row's own, in front of the
+            // suffix, or of a page that is missing
+            const KeyRange kr = key_range(a, key0, limit[0]);
+            const int hi1 = R == 1 ? 0 : key_range(a, key0, limit[R - 1]).hi;
+            bool cut = kr.key < kr.lo || kr.key + kKT > kr.hi ||
+                       (R > 1 && kr.key + kKT > hi1) || (holes >> cur & 1);
+            cut = __any_sync(0xffffffffu, cut);
+            if (cut) {
+                const bool missing = holes >> cur & 1;
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = kr.key + 8 * (i >> 1) + 2 * t + (i & 1);
+                        if (missing || k >= (r ? hi1 : kr.hi) || k < kr.lo) x[r][i] = -INFINITY;
+                    }
+            }
+            float grow[R];
+            bool any = false;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float mx = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float mn = mx == -INFINITY ? m[r] : fmaxf(m[r], mx * scale[r]);
+                any = any || mn > m[r];
+                grow[r] = mn > m[r] ? max_factor(m[r], mn) : 1.0f;
+                m[r] = mn;
+            }
+            if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) l[r] *= grow[r];
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        o[i][2 * r] *= grow[r];
+                        o[i][2 * r + 1] *= grow[r];
+                    }
+            }
+            uint32_t pf[S][4];
+            float down[R];
+            {
+                float w[2][R][2];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float from = m[r] == -INFINITY ? 0.0f : -m[r];  // (no key yet)
+                    float top = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float pr = ex2(fmaf(x[r][i], scale[r], from));
+                        l[r] += pr;
+                        // (a masked key's scale need not be finite)
+                        w[i >> 1][r][i & 1] = cut && x[r][i] == -INFINITY ? 0.0f : pr * vf[i];
+                        top = fmaxf(top, fabsf(w[i >> 1][r][i & 1]));
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // the row's largest weight into [2^14, 2^15)
+                    const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100) - 14;
+                    const float up = pow2(-e);
+                    down[r] = pow2(e);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i >> 1][r][i & 1] *= up;
+                }
+                F::fill(w[0], 0, pf);
+                F::fill(w[1], 2, pf);
+            }
+            // the values of this thread's keys: NT bytes of each
+            constexpr int NW = NT / 4;
+            uint32_t v[4][NW];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 8 * (i >> 1) + 2 * t + (i & 1);
+                if constexpr (D == 128) {
+                    lds4(v[i], vs + place<D>(r, g));
+                } else {
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                 : "=r"(v[i][0]), "=r"(v[i][1])
+                                 : "r"(vs + place<D>(r, g >> 1) + 8 * (g & 1))
+                                 : "memory");
+                }
+#pragma unroll
+                for (int j = 0; j < NW; ++j) v[i][j] ^= kCodeBias;
+            }
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                // byte i of keys 2t and 2t + 1, and of 2t + 8 and 2t + 9
+                const int j = i / 4;
+                const uint32_t pair = i & 2 ? 0x7362u : 0x5140u;
+                const uint32_t half = i & 1 ? kCodesHigh : kCodesLow;
+                const uint32_t b0 = fp16_codes(__byte_perm(v[0][j], v[1][j], pair), half);
+                const uint32_t b1 = fp16_codes(__byte_perm(v[2][j], v[3][j], pair), half);
+                // (the instruction's accumulator truncates: the step's products alone go
+                // through it)
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < S; ++k) mma16816<false>(c, pf[k], b0, b1);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if (R == 1) {
+                        o[i][q] = fmaf(c[q] + c[2 + q], down[0], o[i][q]);
+                    } else {
+                        o[i][q] = fmaf(c[q], down[0], o[i][q]);
+                        o[i][2 * R - 2 + q] = fmaf(c[2 + q], down[R - 1], o[i][2 * R - 2 + q]);
+                    }
+                }
+            }
+            __syncwarp();  // the step's buffer is free
+            copy_step();
+            if (++cur == ST) cur = 0;
+        }
+        __syncwarp();  // the copies' next piece is in shared memory
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        }
+        if (p.npieces > 1) {
+            // this worker's part of the item; whoever is last of a group, and then of
+            // the groups, joins them all
+            auto part_row = [&](int c) {  // piece c of the item
+                return (int64_t)(2 * (p.first + c) + (c == 0)) * ROWS + g;
+            };
+            auto put_part = [&](int64_t at) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    each_column([&](int i, int q, int d) {
+                        __stcg(reinterpret_cast<float4 *>(a.part_o + (at + 8 * r) * D + d),
+                               make_float4(o[i][2 * r + q], o[i + 1][2 * r + q],
+                                           o[i + 2][2 * r + q], o[i + 3][2 * r + q]));
+                    });
+                    if (t == 0) __stcg(a.part_ml + at + 8 * r, make_float2(m[r], l[r]));
+                }
+            };
+            const int width = join_width(p.npieces, kJoin);
+            Join join = join_of(p, worker - p.first, width);
+            bool joined = true;
+            int64_t at = part_row(worker - p.first);
+            for (;;) {
+                put_part(at);
+                __threadfence();
+                __syncwarp();
+                unsigned last = 0;
+                if (lane == 0) {
+                    last = atomicAdd(a.counters + join.counter, 1u) == (unsigned)join.n - 1;
+                    if (last) a.counters[join.counter] = 0;  // as the next launch wants it
+                }
+                if (!__shfl_sync(0xffffffffu, last, 0)) {
+                    joined = false;
+                    break;
+                }
+                __threadfence();
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    m[r] = -INFINITY;
+                    l[r] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) o[i][2 * r] = o[i][2 * r + 1] = 0.0f;
+#pragma unroll 2
+                    for (int c = 0; c < join.n; ++c) {
+                        const int64_t base = part_row(join.first + c * join.step) + 8 * r;
+                        const float2 f = __ldcg(a.part_ml + base);
+                        const float top = fmaxf(m[r], f.x);
+                        const float fo = max_factor(m[r], top), fp = max_factor(f.x, top);
+                        m[r] = top;
+                        l[r] = l[r] * fo + f.y * fp;
+                        each_column([&](int i, int q, int d) {
+                            const float4 v =
+                                __ldcg(reinterpret_cast<const float4 *>(a.part_o + base * D + d));
+                            const float u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                o[i + k][2 * r + q] = o[i + k][2 * r + q] * fo + u[k] * fp;
+                        });
+                    }
+                }
+                if (join.all) break;
+                // the group's sum in the place of its first piece
+                __syncwarp();
+                at = part_row(join.first);
+                join = join_of_groups(p, width);
+            }
+            if (!joined) continue;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (!live[r]) continue;
+            const int64_t row = out_row(r);
+            const float f = row_factor(a, row, m[r], l[r], t == 0);
+            float *dst = row_target(a) + row * D;
+            each_column([&](int i, int q, int d) {
+                *reinterpret_cast<float4 *>(dst + d) =
+                    make_float4(o[i][2 * r + q] * f, o[i + 1][2 * r + q] * f,
+                                o[i + 2][2 * r + q] * f, o[i + 3][2 * r + q] * f);
+            });
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <int D, int ROWS>
+sq_status launch_rows_i8(const PagedArgs &a, const void *k_cache, const void *v_cache, int sms,
+                         cudaStream_t st) {
+    using C = RowsI8Cfg<D>;
+    static std::mutex mu;
+    static bool done[64] = {};
+    DeviceInfo di;
+    sq_status rc = device_info(&di);
+    if (rc != SQ_OK) return rc;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!done[di.device & 63]) {
+            if (cudaFuncSetAttribute(paged_rows_i8_kernel<D, ROWS>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     C::kSmem) != cudaSuccess)
+                return SQ_ERR_CUDA;
+            done[di.device & 63] = true;
+        }
+    }
+    return launch_pdl(paged_rows_i8_kernel<D, ROWS>, dim3((unsigned)sms), dim3(kWarps * 32),
+                      C::kSmem, st, 1, a, static_cast<const int8_t *>(k_cache),
+                      static_cast<const int8_t *>(v_cache));
+}
+
+}  // namespace
+
+sq_status launch_paged_rows_i8(const PagedArgs &a, const void *k_cache, const void *v_cache, int D,
+                               int rows, int sms, cudaStream_t st) {
+    if (D == 128)
+        return rows == 8 ? launch_rows_i8<128, 8>(a, k_cache, v_cache, sms, st)
+                         : launch_rows_i8<128, 16>(a, k_cache, v_cache, sms, st);
+    return rows == 8 ? launch_rows_i8<64, 8>(a, k_cache, v_cache, sms, st)
+                     : launch_rows_i8<64, 16>(a, k_cache, v_cache, sms, st);
+}
+
+}  // namespace sq

@@ -53,6 +53,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 namespace sq {
 namespace {
@@ -125,6 +126,7 @@ constexpr int kThreads = 640;
 constexpr int kItems = 4;    // pieces the walk may be ahead
 constexpr int kStats = 4;    // tiles whose maxima and sums are kept
 constexpr int kMiss = 8;     // more than the tiles between a copy and its softmax
+constexpr int kScaleTiles = 4;  // the same for codes that have been widened
 // Pieces of an item that are joined in one go (2.3 us each; 3 to 12 measured alike;
 // all in one go: 322 against 57 us for 8 tokens of 16 heads behind 30,000 keys)
 constexpr int kJoin = 6;
@@ -134,14 +136,34 @@ constexpr int kJoin = 6;
 constexpr int kMinTiles = 4;
 constexpr float kBias = 12.0f;  // log2 of the probabilities' factor
 
-template <int D, bool BF>
+constexpr int kI8 = kCacheI8;
+
+// An int8 cache's scales of the tiles between their copy and their softmax, and which
+// tiles' value scales lie far apart.
+struct TileScales {
+    alignas(16) float k[kScaleTiles][kKT];  // (read 16 bytes at a time)
+    alignas(16) float v[kScaleTiles][kKT];  // divided by 2^exp
+    int exp[kScaleTiles];        // the largest value scale's exponent (wild: 0)
+    int wild[kScaleTiles];       // the smallest is under 2^-8 of it, or one is not finite
+    uint64_t meet;
+    unsigned range[2][4];        // a copying warp's largest exponent, and 255 - its smallest
+    float half_top[2][2][kRows];  // a wild tile's largest weights (log2) over its halves
+};
+struct NoScales {};
+
+template <int D, int CT>
 struct TilesCfg {
+    static constexpr bool BF = CT == SQ_CACHE_BF16;
     static constexpr int kParts = BF ? 3 : 2;
     static constexpr int kSlab = kKT * 128;            // 128 rows x 64 elements
     static constexpr int kSlot = kSlab * (D / 64);     // keys or values of a tile
-    static constexpr int kSlots = D == 64 ? 6 : BF ? 3 : 4;
+    static constexpr int kSlots = CT == kI8 ? (D == 64 ? 5 : 3) : D == 64 ? 6 : BF ? 3 : 4;
     static constexpr int kQPart = kRows * D * 2;       // one part of the queries
-    static constexpr int kSmem = kParts * kQPart + kSlots * kSlot + 1024;
+    // codes on their way into slots
+    static constexpr int kRaws = CT == kI8 ? 3 : 0, kRaw = kKT * D;
+    static constexpr int kSmem = kParts * kQPart + kSlots * kSlot + kRaws * kRaw + 1024;
+    using Elem = std::conditional_t<CT == kI8, int8_t, uint16_t>;
+    using Scales = std::conditional_t<CT == kI8, TileScales, NoScales>;
     // tensor memory: S and P of a tile, S's first column in it, P V
     static constexpr int kArea = 64 * kParts;
     static constexpr int kS0 = kArea - 128;
@@ -249,19 +271,40 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
         : "memory");
 }
+__device__ __forceinline__ void sts4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z,
+                                     uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z),
+                 "r"(w)
+                 : "memory");
+}
+// two fp32 numbers in 32-bit registers times (f, g)
+__device__ __forceinline__ void times2(uint32_t &x, uint32_t &y, float f, float g) {
+    float a, b;
+    upk(mul2(pk(__uint_as_float(x), __uint_as_float(y)), pk(f, g)), a, b);
+    x = __float_as_uint(a);
+    y = __float_as_uint(b);
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-template <int D, bool BF>
+template <int D, int CT>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_tiles_kernel(const __grid_constant__ PagedArgs a, const uint16_t *__restrict__ k_cache,
-                       const uint16_t *__restrict__ v_cache) {
-    using C = TilesCfg<D, BF>;
+    paged_tiles_kernel(const __grid_constant__ PagedArgs a,
+                       const typename TilesCfg<D, CT>::Elem *__restrict__ k_cache,
+                       const typename TilesCfg<D, CT>::Elem *__restrict__ v_cache) {
+    using C = TilesCfg<D, CT>;
+    constexpr bool BF = C::BF;
     constexpr int NS = C::kSlots, NP = C::kParts;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ TileBars B;
+    __shared__ typename C::Scales X;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort = &B.abort_flag;
     const uint32_t qbase = su32(smem);  // [part][slab][128 rows][128 B]
@@ -287,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_init(&B.group, 4);
         for (int i = 0; i < 4; ++i) bar_init(&B.pair[i], 2);
         bar_init(&B.mma_done, 1);
+        if constexpr (CT == kI8) bar_init(&X.meet, 4);
         for (int i = 0; i < kItems; ++i) {
             B.bad_from[i] = 0x7fffffff;
             B.bad_to[i] = -1;
@@ -421,12 +465,103 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t seq = 0, done = 0, tile = 0;  // slots begun, slots handed over, tiles begun
         bool ok = true;
         // thread: chunk ch of rows r0, r0 + kRowStep, ... of a slot
-        constexpr int kRowStep = 128 / (D / 8);
-        const int r0 = ct / (D / 8), ch = ct % (D / 8);
+        constexpr int kChunks = D * (int)sizeof(typename C::Elem) / 16;  // of a row
+        constexpr int kRowStep = 128 / kChunks;
+        const int r0 = ct / kChunks, ch = ct % kChunks;
         const uint32_t my_chunk =
             (ch >> 3) * C::kSlab + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4);
         uint32_t scan = 0;  // 4 bits per slot: 1 + the piece's slot where values are looked at
+        // int8: the thread's key's scales of the newest tile and of the one before, by
+        // the tile's parity
+        float ks0 = 0.f, ks1 = 0.f, vs0 = 0.f, vs1 = 0.f;
+        // The scales of tile t into shared memory, the values' divided by the largest's
+        // power of two.  (The four warps meet for that, bounded.)
+        auto put_scales = [&](uint32_t t) {
+            if constexpr (CT == kI8) {
+                const float ks = t & 1 ? ks1 : ks0, vs = t & 1 ? vs1 : vs0;
+                // zeros and keys that nothing attends to say nothing; one that is not finite
+                // is further from the others than any
+                const unsigned e = __float_as_uint(vs) >> 23 & 255u;
+                const unsigned top = __reduce_max_sync(0xffffffffu, e == 255u ? 0u : e);
+                const unsigned low = __reduce_max_sync(
+                    0xffffffffu, vs == 0.0f ? 0u : e == 255u ? 511u : 255u - e);
+                if (lane == 0) {
+                    X.range[t & 1][ct >> 5] = top << 16 | low;
+                    bar_arrive(&X.meet);
+                }
+                if (!warp_wait(&X.meet, t & 1u, abort, a.error)) {
+                    ok = false;
+                    return;
+                }
+                unsigned r = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r = __vmaxu2(r, X.range[t & 1][i]);
+                const int most = (int)(r >> 16), least = 255 - (int)(r & 0xffffu);
+                const bool wild = most - least > 8;
+                const int exp = wild ? 0 : min(max(most - 127, -126), 126);
+                const int at = t % kScaleTiles;
+                X.k[at][ct] = ks;
+                X.v[at][ct] = vs * pow2(-exp);
+                if (ct == 0) {
+                    X.exp[at] = exp;
+                    X.wild[at] = wild;
+                }
+            }
+        };
+        // int8: the oldest slots' codes, which this thread copied itself, into their slots
+        // as fp16 numbers
+        auto widen = [&](uint32_t upto) {
+            if constexpr (CT == kI8) {
+                while (ok && done < upto) {
+                    const uint32_t after = seq - done - 1;  // copies that may be on their way
+                    if (after == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    else if (after == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    else asm volatile("cp.async.wait_group 2;" ::: "memory");
+                    const uint32_t sl = done % NS;
+                    if (done >= NS &&
+                        !warp_wait(&B.empty[sl], (done / NS - 1) & 1u, abort, a.error)) {
+                        ok = false;
+                        break;
+                    }
+                    // keys of tile t are slot 2 t - 1 (0: 0); the last slot holds values
+                    const uint32_t kt = (done + 1) / 2;
+                    if ((done == 0 || done & 1) && kt < tile) put_scales(kt);
+                    if (!ok) break;
+                    const uint32_t from = ring + NS * C::kSlot + done % C::kRaws * C::kRaw + ct * 16;
+                    // row r0's chunks 2 ch and 2 ch + 1 of 8 numbers; half of the threads of
+                    // a row of 128 store the second first, so that every bank is met once
+                    const int c8 = 2 * ch & 7, other = D == 128 ? ch >> 2 & 1 : 0;
+                    const uint32_t slab = ring + sl * C::kSlot + (2 * ch >> 3) * C::kSlab + r0 * 128;
+                    const uint32_t to0 = slab + (((c8 + other) ^ (r0 & 7)) << 4);
+                    const uint32_t to1 = slab + (((c8 + 1 - other) ^ (r0 & 7)) << 4);
+#pragma unroll 2
+                    for (int j = 0; j < kKT / kRowStep; ++j) {
+                        uint32_t w[4], h[8];
+                        lds4(w, from + j * 2048);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t b = w[i] ^ kCodeBias;
+                            h[2 * i] = fp16_codes(b, kCodesLow);
+                            h[2 * i + 1] = fp16_codes(b, kCodesHigh);
+                        }
+                        const uint32_t d = j * kRowStep * 128;
+                        sts4(to0 + d, other ? h[4] : h[0], other ? h[5] : h[1],
+                             other ? h[6] : h[2], other ? h[7] : h[3]);
+                        sts4(to1 + d, other ? h[0] : h[4], other ? h[1] : h[5],
+                             other ? h[2] : h[6], other ? h[3] : h[7]);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&B.full[sl]);
+                    ++done;
+                }
+            }
+        };
         auto hand_over = [&](bool all) {
+            if constexpr (CT == kI8) {
+                widen(all ? seq : seq - (C::kRaws - 1));
+                return;
+            }
             if (all) asm volatile("cp.async.wait_group 0;" ::: "memory");
             else asm volatile("cp.async.wait_group 1;" ::: "memory");
             if (scan != 0) {
@@ -474,8 +609,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // 128 rows of a cache into the next slot; lane l (of 8) holds the place of
         // rows 16 l .. 16 l + 15 in the caches, in bytes
-        auto copy_slot = [&](const uint16_t *cache, int64_t place, unsigned miss, int lo, int hi,
-                             uint32_t look) {
+        auto copy_slot = [&](const typename C::Elem *cache, int64_t place, unsigned miss, int lo,
+                             int hi, uint32_t look) {
+            if constexpr (CT == kI8) {
+                // rows of no key are masked whatever they hold: codes are finite
+                const uint32_t to = ring + NS * C::kSlot + seq % C::kRaws * C::kRaw + ct * 16;
+                const char *src = reinterpret_cast<const char *>(cache) + (r0 & 15) * D + ch * 16;
+#pragma unroll
+                for (int j = 0; j < kKT / kRowStep; ++j) {
+                    const int block = (r0 + j * kRowStep) >> 4;  // of 16 rows
+                    const char *from = src + __shfl_sync(0xffffffffu, place, block);
+                    copy16(to + j * 2048, from, !(miss >> block & 1));
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                ++seq;
+                if (seq - done >= C::kRaws) hand_over(false);
+                return;
+            }
             const uint32_t sl = seq % NS;
             if (seq >= NS) {
                 const uint32_t ph = (seq / NS - 1) & 1u;
@@ -564,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int key = r.key + 16 * (lane & 7);
                 lo = r.lo - r.key;
                 hi = r.hi - r.key;
-                if (key_range(a, key0, p.pos0 + 1).hi < r.key + kKT)
+                if (CT != kI8 && key_range(a, key0, p.pos0 + 1).hi < r.key + kKT)
                     look = 1 + (n - 1) % kItems;  // (the piece's first row does not see all)
                 entry = left > 1 ? page_of(key_range(a, key0 + kKT, p.keys)) : -1;
                 const bool there = e >= 0 && e < a.num_pages;
@@ -572,8 +722,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (there)
                     place = ((((int64_t)e * a.Hkv + p.head) << a.page_shift) +
                              (key & ((1 << a.page_shift) - 1))) *
-                            (D * 2);
+                            (D * (int)sizeof(typename C::Elem));
                 if (ct == 0) B.miss[tile % kMiss] = miss;
+                if constexpr (CT == kI8) {
+                    // this thread's key's scales, on their way until its codes are widened;
+                    // zeros for keys that the item does not have
+                    const int64_t row = __shfl_sync(0xffffffffu, place, ct >> 4) / D + (ct & 15);
+                    const bool in = !(miss >> (ct >> 4) & 1) && ct >= lo && ct < hi;
+                    const float ks = in ? __ldg(a.k_scale + row) : 0.f;
+                    const float vs = in ? __ldg(a.v_scale + row) : 0.f;
+                    if (tile & 1) ks1 = ks, vs1 = vs;
+                    else ks0 = ks, vs0 = vs;
+                }
             }
 #pragma unroll 1
             for (int kv = more ? 0 : 1; kv < (tile > 0 ? 2 : 1) && ok; ++kv)
@@ -654,7 +814,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
                         }
                         e >>= 23;
-                        const int sh = shift_of((int)e - 127);
+                        const int sh = CT == kI8 ? shift_of_wide((int)e - 127, a.scale)
+                                                 : shift_of((int)e - 127);
                         mul *= pow2(-sh);
                         if (c4 == 0) B.qmul[n & 1][16 * warp + i + sub] = pow2(sh);
                     }
@@ -692,6 +853,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_wait();
                 const unsigned miss = B.miss[t % kMiss] >> (4 * g);
                 const float c = BF ? a.scale : a.scale * B.qmul[n & 1][r];
+                const int sc = t % kScaleTiles;
+                if constexpr (CT == kI8) {
+#pragma unroll
+                    for (int i = 0; i < 64; i += 4) {
+                        const float4 ks = *reinterpret_cast<const float4 *>(&X.k[sc][64 * g + i]);
+                        uint32_t (&w)[32] = v[i / 32];
+                        times2(w[i % 32], w[i % 32 + 1], ks.x, ks.y);
+                        times2(w[i % 32 + 2], w[i % 32 + 3], ks.z, ks.w);
+                    }
+                }
                 const KeyRange kr = key_range(a, key0, limit);
                 const int at = kr.key + 64 * g;  // this warp's 64 keys
                 if (__any_sync(0xffffffffu, at + 64 > kr.hi || at < kr.lo || (miss & 15u) != 0)) {
@@ -717,6 +888,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the row's maximum, with the other half's; every logit of these
                 // rows is in registers from here on
                 B.half_max[t & 1][g][r] = mx;
+                bool wild = false;  // of the tile
+                if constexpr (CT == kI8) {
+                    wild = X.wild[sc];
+                    if (wild) {
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            top = fmaxf(top, fmaf(__uint_as_float(v[i / 32][i % 32]), c,
+                                                  lg2(fabsf(X.v[sc][64 * g + i]))));
+                        X.half_top[t & 1][g][r] = top;
+                    }
+                }
                 __syncwarp();
                 if (lane == 0) bar_arrive(&B.pair[w]);
                 if (!warp_wait(&B.pair[w], t & 1u, abort, a.error)) {
@@ -729,6 +912,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float m = mx == -INFINITY ? 0.0f : __fmaf_ru(mx, c, -kBias);
                 const unsigned long long c2 = pk(c, c), m2 = pk(-m, -m);
                 unsigned long long sum2 = 0;
+                int shift = 0;  // of a wild tile's row: its largest weight is near 2^kBias
+                if constexpr (CT == kI8) {
+                    if (wild) {
+                        const float top = fmaxf(X.half_top[t & 1][0][r], X.half_top[t & 1][1][r]);
+                        shift = (int)fminf(fmaxf(kBias - ceilf(top - m), -126.0f), 126.0f);
+                    }
+                }
                 // per 16 keys 8 columns of each part
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -744,6 +934,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         x = ex2(x);
                         y = ex2(y);
                         sum2 = add2(sum2, pk(x, y));
+                        if constexpr (CT == kI8) {
+                            // the weights of the codes
+                            const float2 vs = *reinterpret_cast<const float2 *>(
+                                &X.v[sc][64 * g + 16 * q + 2 * i]);
+                            if (wild) {
+                                // (a masked key's scale need not be finite; the shift
+                                // in two steps, none of which leaves fp32's range)
+                                const uint32_t none = 0xff800000u;
+                                const float s1 = pow2(shift / 2), s2 = pow2(shift - shift / 2);
+                                x = v[q >> 1][e] == none ? 0.0f : x * s1 * vs.x * s2;
+                                y = v[q >> 1][e + 1] == none ? 0.0f : y * s1 * vs.y * s2;
+                            } else {
+                                upk(mul2(pk(x, y), pk(vs.x, vs.y)), x, y);
+                            }
+                        }
                         uint32_t z[NP];
                         split16<BF, NP>(x, y, z);
 #pragma unroll
@@ -755,7 +960,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 float sa, sb;
                 upk(sum2, sa, sb);
-                B.stat[t % kStats][g][r] = make_float2(mx == -INFINITY ? mx : m, sa + sb);
+                // (the second half's maximum is not looked at: int8 has what P V is to be
+                // multiplied by in its place)
+                const float first = mx == -INFINITY ? mx : m;
+                if constexpr (CT == kI8)
+                    B.stat[t % kStats][g][r] = make_float2(
+                        g ? pow2(X.exp[sc] - shift) : first, sa + sb);
+                else
+                    B.stat[t % kStats][g][r] = make_float2(first, sa + sb);
                 tmem_st_wait();
                 tc_before();
                 __syncwarp();
@@ -813,12 +1025,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_after();
                 float2 e = B.stat[t % kStats][0][row];
-                e.y += B.stat[t % kStats][1][row].y;
+                const float2 e1 = B.stat[t % kStats][1][row];
+                e.y += e1.y;
                 const float top = fmaxf(m, e.x);
                 const float f = max_factor(m, top), g = max_factor(e.x, top);
                 m = top;
                 l = l * f + e.y * g;
-                const unsigned long long f2 = pk(f, f), g2 = pk(g, g);
+                const float go = CT == kI8 ? g * e1.x : g;
+                const unsigned long long f2 = pk(f, f), g2 = pk(go, go);
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) {
                     uint32_t v[16];
@@ -859,7 +1073,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __stcg(reinterpret_cast<float4 *>(dst) + i, v);
                 }
             }
-            if (B.bad_to[it] >= 0) {
+            if constexpr (CT != kI8) if (B.bad_to[it] >= 0) {
                 // values that the copies took out of the tiles that not every row sees
                 // in full: added to the rows that see them
                 float *own = dst;
@@ -997,10 +1211,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, bool BF>
+template <int D, int CT>
 sq_status launch_tiles(const PagedArgs &a, const void *k_cache, const void *v_cache, int sms,
                        cudaStream_t st) {
-    using C = TilesCfg<D, BF>;
+    using C = TilesCfg<D, CT>;
+    using Elem = typename C::Elem;
     static std::mutex mu;
     static bool done[64] = {};
     DeviceInfo di;
@@ -1009,27 +1224,30 @@ sq_status launch_tiles(const PagedArgs &a, const void *k_cache, const void *v_ca
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!done[di.device & 63]) {
-            if (cudaFuncSetAttribute(paged_tiles_kernel<D, BF>,
+            if (cudaFuncSetAttribute(paged_tiles_kernel<D, CT>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      C::kSmem) != cudaSuccess)
                 return SQ_ERR_CUDA;
             done[di.device & 63] = true;
         }
     }
-    return launch_pdl(paged_tiles_kernel<D, BF>, dim3((unsigned)sms), dim3(kThreads), C::kSmem, st,
-                      1, a, static_cast<const uint16_t *>(k_cache),
-                      static_cast<const uint16_t *>(v_cache));
+    return launch_pdl(paged_tiles_kernel<D, CT>, dim3((unsigned)sms), dim3(kThreads), C::kSmem, st,
+                      1, a, static_cast<const Elem *>(k_cache), static_cast<const Elem *>(v_cache));
 }
 
 }  // namespace
 
 sq_status launch_paged_tiles(const PagedArgs &a, const void *k_cache, const void *v_cache, int D,
-                             bool bf16, int sms, cudaStream_t st) {
+                             int cache_type, int sms, cudaStream_t st) {
+    if (cache_type == kCacheI8)
+        return D == 128 ? launch_tiles<128, kCacheI8>(a, k_cache, v_cache, sms, st)
+                        : launch_tiles<64, kCacheI8>(a, k_cache, v_cache, sms, st);
+    const bool bf16 = cache_type == SQ_CACHE_BF16;
     if (D == 128)
-        return bf16 ? launch_tiles<128, true>(a, k_cache, v_cache, sms, st)
-                    : launch_tiles<128, false>(a, k_cache, v_cache, sms, st);
-    return bf16 ? launch_tiles<64, true>(a, k_cache, v_cache, sms, st)
-                : launch_tiles<64, false>(a, k_cache, v_cache, sms, st);
+        return bf16 ? launch_tiles<128, SQ_CACHE_BF16>(a, k_cache, v_cache, sms, st)
+                    : launch_tiles<128, SQ_CACHE_F16>(a, k_cache, v_cache, sms, st);
+    return bf16 ? launch_tiles<64, SQ_CACHE_BF16>(a, k_cache, v_cache, sms, st)
+                : launch_tiles<64, SQ_CACHE_F16>(a, k_cache, v_cache, sms, st);
 }
 
 }  // namespace sq
