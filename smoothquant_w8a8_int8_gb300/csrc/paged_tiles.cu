@@ -106,6 +106,20 @@ __device__ __forceinline__ bool warp_wait(const uint64_t *bar, uint32_t parity,
                                           volatile int *abort, unsigned *error) {
     return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, error)) != 0;
 }
+__device__ __forceinline__ void expect_bytes(uint64_t *bar, unsigned bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(bar)),
+                 "r"(bytes)
+                 : "memory");
+}
+// `bytes` (a multiple of 16) of global memory into shared memory, counted on `bar`
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, unsigned bytes,
+                                          uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(dst),
+        "l"(src), "r"(bytes), "r"(su32(bar))
+        : "memory");
+}
 __device__ __forceinline__ void drain_bar(const uint64_t *bar, uint32_t parity,
                                           unsigned *error) {
     const uint32_t a = su32(bar);
@@ -126,7 +140,8 @@ constexpr int kThreads = 640;
 constexpr int kItems = 4;    // pieces the walk may be ahead
 constexpr int kStats = 4;    // tiles whose maxima and sums are kept
 constexpr int kMiss = 8;     // more than the tiles between a copy and its softmax
-constexpr int kScaleTiles = 4;  // the same for codes that have been widened
+constexpr int kScaleTiles = 4;  // tiles whose scales are kept
+constexpr int kRawSlots = 3;    // keys or values of a tile as codes, on their way or landed
 // Pieces of an item that are joined in one go (2.3 us each; 3 to 12 measured alike;
 // all in one go: 322 against 57 us for 8 tokens of 16 heads behind 30,000 keys)
 constexpr int kJoin = 6;
@@ -138,18 +153,19 @@ constexpr float kBias = 12.0f;  // log2 of the probabilities' factor
 
 constexpr int kI8 = kCacheI8;
 
-// An int8 cache's scales of the tiles between their copy and their softmax, and which
-// tiles' value scales lie far apart.
-struct TileScales {
+// What an int8 cache needs beside TileBars: codes on their way into slots, and the
+// scales of the tiles between their load and their softmax.
+struct TileCodes {
     alignas(16) float k[kScaleTiles][kKT];  // (read 16 bytes at a time)
     alignas(16) float v[kScaleTiles][kKT];  // divided by 2^exp
     int exp[kScaleTiles];        // the largest value scale's exponent (wild: 0)
     int wild[kScaleTiles];       // the smallest is under 2^-8 of it, or one is not finite
-    uint64_t meet;
-    unsigned range[2][4];        // a copying warp's largest exponent, and 255 - its smallest
+    uint64_t scale_full[kScaleTiles], scale_empty[kScaleTiles];
+    uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
+    int raw_stop[kRawSlots];
     float half_top[2][2][kRows];  // a wild tile's largest weights (log2) over its halves
 };
-struct NoScales {};
+struct NoCodes {};
 
 template <int D, int CT>
 struct TilesCfg {
@@ -160,10 +176,11 @@ struct TilesCfg {
     static constexpr int kSlots = CT == kI8 ? (D == 64 ? 5 : 3) : D == 64 ? 6 : BF ? 3 : 4;
     static constexpr int kQPart = kRows * D * 2;       // one part of the queries
     // codes on their way into slots
-    static constexpr int kRaws = CT == kI8 ? 3 : 0, kRaw = kKT * D;
-    static constexpr int kSmem = kParts * kQPart + kSlots * kSlot + kRaws * kRaw + 1024;
+    static constexpr int kRaw = kKT * D;
+    static constexpr int kSmem =
+        kParts * kQPart + kSlots * kSlot + (CT == kI8 ? kRawSlots * kRaw : 0) + 1024;
     using Elem = std::conditional_t<CT == kI8, int8_t, uint16_t>;
-    using Scales = std::conditional_t<CT == kI8, TileScales, NoScales>;
+    using Codes = std::conditional_t<CT == kI8, TileCodes, NoCodes>;
     // tensor memory: S and P of a tile, S's first column in it, P V
     static constexpr int kArea = 64 * kParts;
     static constexpr int kS0 = kArea - 128;
@@ -277,12 +294,27 @@ __device__ __forceinline__ void sts4(uint32_t addr, uint32_t x, uint32_t y, uint
                  "r"(w)
                  : "memory");
 }
-// two fp32 numbers in 32-bit registers times (f, g)
-__device__ __forceinline__ void times2(uint32_t &x, uint32_t &y, float f, float g) {
-    float a, b;
-    upk(mul2(pk(__uint_as_float(x), __uint_as_float(y)), pk(f, g)), a, b);
-    x = __float_as_uint(a);
-    y = __float_as_uint(b);
+// fp32 numbers in 32-bit registers times as many of shared memory (16-byte aligned)
+template <int N>
+__device__ __forceinline__ void times_scales(uint32_t (&v)[N], const float *scales) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(scales + i);
+        float x, y;
+        upk(mul2(pk(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), pk(f.x, f.y)), x, y);
+        v[i] = __float_as_uint(x);
+        v[i + 1] = __float_as_uint(y);
+        upk(mul2(pk(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), pk(f.z, f.w)), x, y);
+        v[i + 2] = __float_as_uint(x);
+        v[i + 3] = __float_as_uint(y);
+    }
+}
+// -infinity in the places of clear bits
+template <int N>
+__device__ __forceinline__ void hide(uint32_t (&v)[N], unsigned seen) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (!(seen >> i & 1)) v[i] = 0xff800000u;
 }
 __device__ __forceinline__ float lg2(float x) {
     float y;
@@ -304,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ TileBars B;
-    __shared__ typename C::Scales X;
+    __shared__ typename C::Codes X;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort = &B.abort_flag;
     const uint32_t qbase = su32(smem);  // [part][slab][128 rows][128 B]
@@ -317,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kItems; ++i) {
             bar_init(&B.item_full[i], 1);
-            bar_init(&B.item_empty[i], 17);
+            bar_init(&B.item_empty[i], CT == kI8 ? 15 : 17);
         }
         bar_init(&B.q_full, 8);
         bar_init(&B.q_empty, 1);
@@ -330,7 +362,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_init(&B.group, 4);
         for (int i = 0; i < 4; ++i) bar_init(&B.pair[i], 2);
         bar_init(&B.mma_done, 1);
-        if constexpr (CT == kI8) bar_init(&X.meet, 4);
+        if constexpr (CT == kI8) {
+            for (int i = 0; i < kScaleTiles; ++i) {
+                bar_init(&X.scale_full[i], 1);
+                bar_init(&X.scale_empty[i], 8);
+            }
+            for (int i = 0; i < kRawSlots; ++i) {
+                bar_init(&X.raw_full[i], 1);
+                bar_init(&X.raw_empty[i], 4);
+                X.raw_stop[i] = 0;
+            }
+        }
         for (int i = 0; i < kItems; ++i) {
             B.bad_from[i] = 0x7fffffff;
             B.bad_to[i] = -1;
@@ -355,7 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // registers: 96 a thread at launch; (2 x 104 + 168 + 56 + 48) x 128 in all
     if (warp >= 16) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (CT == kI8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == 16 && lane == 0) {
             // ------------------------------------------------------ products
             // per tile t of the share: S(t + 1) is issued before P V(t)
@@ -456,112 +499,215 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (!more) break;
             }
+        } else if (CT == kI8 && warp >= 18) {
+            if constexpr (CT == kI8) {
+                // ------------------- codes (warp 18) and scales (warp 19), tile by tile
+                const bool codes = warp == 18;
+                const uint32_t raws = ring + NS * C::kSlot;
+                uint32_t seq = 0, tile = 0;  // slots begun, tiles begun
+                bool ok = true, more = true;
+                Piece p = {};
+                int left = 0, key0 = 0, entry = -1;
+                // lane l: the entry of the page of keys 16 (l % 8) .. of a tile; -1 where none
+                // is wanted
+                auto page_of = [&](const KeyRange &r) {
+                    const int *pages = r.front ? a.prefix_pages
+                                               : a.block_table + (int64_t)p.seq * a.max_pages;
+                    const int key = r.key + 16 * (lane & 7);
+                    return key < r.hi && key + 16 > r.lo ? __ldg(pages + (key >> a.page_shift)) : -1;
+                };
+                // The tile's rows of a cache into the next raw slot, by blocks of 16 (`miss`:
+                // those of no page) that lie in one page, so one after the other.  Rows of no
+                // key are masked whatever they hold: codes are finite.
+                auto fetch = [&](const int8_t *cache, int64_t row, unsigned miss) {
+                    const uint32_t sl = seq % kRawSlots;
+                    if (seq >= kRawSlots && !warp_wait(&X.raw_empty[sl], (seq / kRawSlots - 1) & 1u,
+                                                       abort, a.error)) {
+                        ok = false;
+                        return;
+                    }
+                    const int unit = min(8, 1 << (a.page_shift - 4));  // blocks of a page
+                    const int in = lane & (unit - 1);
+                    const bool first = lane < 8 && !(miss >> lane & 1) &&
+                                       (in == 0 || (miss >> (lane - 1) & 1));
+                    const int n = __ffs(miss >> (lane & 7) | 1u << (unit - in)) - 1;
+                    if (lane == 0)
+                        expect_bytes(&X.raw_full[sl], __popc(~miss & 0xffu) * 16 * D);
+                    __syncwarp();
+                    if (first)
+                        bulk_copy(raws + sl * C::kRaw + lane * 16 * D, cache + row * D, n * 16 * D,
+                                  &X.raw_full[sl]);
+                    ++seq;
+                };
+                int64_t v_row = 0;
+                unsigned v_miss = 0;
+                for (uint32_t n = 0; ok && more;) {
+                    if (left == 0) {
+                        const int it = n % kItems;
+                        if (!warp_wait(&B.item_full[it], (n / kItems) & 1u, abort, a.error)) {
+                            ok = false;
+                            break;
+                        }
+                        more = !B.stop[it];
+                        if (more) {
+                            p = B.items[it];
+                            left = p.ntiles;
+                            key0 = p.key0;
+                            entry = page_of(key_range(a, key0, p.keys));
+                            __syncwarp();
+                            if (lane == 0) bar_arrive(&B.item_empty[it]);
+                            ++n;
+                        }
+                    }
+                    int64_t row = 0;  // of the lane's block
+                    unsigned miss = 0xff;
+                    if (more) {
+                        // the next tile's entry is on its way meanwhile
+                        const int e = entry;
+                        const KeyRange r = key_range(a, key0, p.keys);
+                        const int key = r.key + 16 * (lane & 7);
+                        entry = left > 1 ? page_of(key_range(a, key0 + kKT, p.keys)) : -1;
+                        const bool there = e >= 0 && e < a.num_pages;
+                        miss = ~__ballot_sync(0xffffffffu, there) & 0xffu;
+                        if (there)
+                            row = (((int64_t)e * a.Hkv + p.head) << a.page_shift) +
+                                  (key & ((1 << a.page_shift) - 1));
+                        if (!codes) {
+                            // lane l: keys 4 l .. 4 l + 3 (zeros for keys that the item has not)
+                            const int at = tile % kScaleTiles, k0 = r.key + 4 * lane;
+                            const int64_t from =
+                                __shfl_sync(0xffffffffu, row, lane >> 2) + 4 * (lane & 3);
+                            float4 ks = make_float4(0.f, 0.f, 0.f, 0.f), vs = ks;
+                            if (!(miss >> (lane >> 2) & 1)) {
+                                ks = __ldg(reinterpret_cast<const float4 *>(a.k_scale + from));
+                                vs = __ldg(reinterpret_cast<const float4 *>(a.v_scale + from));
+                            }
+                            float *vv[4] = {&vs.x, &vs.y, &vs.z, &vs.w};
+                            unsigned top = 0, low = 0;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (k0 + i < r.lo || k0 + i >= r.hi) *vv[i] = 0.f;
+                                // zeros say nothing; one that is not finite is further from the
+                                // others than any
+                                const unsigned x = __float_as_uint(*vv[i]) >> 23 & 255u;
+                                top = max(top, x == 255u ? 0u : x);
+                                low = max(low, *vv[i] == 0.0f ? 0u : x == 255u ? 511u : 255u - x);
+                            }
+                            top = __reduce_max_sync(0xffffffffu, top);
+                            low = __reduce_max_sync(0xffffffffu, low);
+                            const bool wild = (int)top - (255 - (int)low) > 8;
+                            const int exp = wild ? 0 : min(max((int)top - 127, -126), 126);
+                            const float f = pow2(-exp);
+                            if (tile >= kScaleTiles &&
+                                !warp_wait(&X.scale_empty[at], (tile / kScaleTiles - 1) & 1u, abort,
+                                           a.error)) {
+                                ok = false;
+                                break;
+                            }
+                            *reinterpret_cast<float4 *>(&X.k[at][4 * lane]) = ks;
+                            *reinterpret_cast<float4 *>(&X.v[at][4 * lane]) =
+                                make_float4(vs.x * f, vs.y * f, vs.z * f, vs.w * f);
+                            if (lane == 0) {
+                                X.exp[at] = exp;
+                                X.wild[at] = wild;
+                                B.miss[tile % kMiss] = miss;
+                            }
+                            __syncwarp();
+                            if (lane == 0) bar_arrive(&X.scale_full[at]);
+                        }
+                    }
+                    // a turn fetches the keys of tile `tile` and the values of the one before;
+                    // the last turn the last values alone
+                    if (codes && more) fetch(k_cache, row, miss);
+                    if (codes && ok && tile > 0) fetch(v_cache, v_row, v_miss);
+                    v_row = row;
+                    v_miss = miss;
+                    if (more) {
+                        ++tile;
+                        --left;
+                        key0 += kKT;
+                    }
+                }
+                if (codes) {
+                    // the end, for those that widen; and every copy lands before the CTA's
+                    // shared memory goes away
+                    const uint32_t sl = seq % kRawSlots;
+                    if (ok && (seq < kRawSlots ||
+                               warp_wait(&X.raw_empty[sl], (seq / kRawSlots - 1) & 1u, abort,
+                                         a.error))) {
+                        if (lane == 0) {
+                            X.raw_stop[sl] = 1;
+                            bar_arrive(&X.raw_full[sl]);
+                        }
+                    }
+                    for (uint32_t d = seq < kRawSlots ? 0 : seq - kRawSlots; d < seq; ++d)
+                        if (d + kRawSlots > seq || !ok)
+                            drain_bar(&X.raw_full[d % kRawSlots], (d / kRawSlots) & 1u, a.error);
+                }
+            }
         }
         __syncwarp();
+    } else if (CT == kI8 && warp >= 12) {
+        if constexpr (CT == kI8) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+            // ------------------------------- codes into slots, as fp16 numbers
+            // Thread: 8 codes of a row at a time, number c of each half of the row (D =
+            // 64: of the row), odd rows the second half first, so that loads of 8 bytes
+            // and stores of 16 meet every bank once.
+            const int ct = threadIdx.x - 384;
+            constexpr int kRowStep = 16, kHalves = D / 64;
+            const int r0 = ct >> 3, c = ct & 7;
+            const int h0 = kHalves == 2 ? r0 & 1 : 0;
+            const uint32_t from0 = ring + NS * C::kSlot + r0 * D + 8 * c;
+            const uint32_t to0 = ring + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+            for (uint32_t d = 0;; ++d) {
+                const uint32_t rw = d % kRawSlots, sl = d % NS;
+                if (!warp_wait(&X.raw_full[rw], (d / kRawSlots) & 1u, abort, a.error)) break;
+                if (X.raw_stop[rw]) break;
+                if (d >= NS && !warp_wait(&B.empty[sl], (d / NS - 1) & 1u, abort, a.error)) break;
+                const uint32_t from = from0 + rw * C::kRaw, to = to0 + sl * C::kSlot;
+#pragma unroll
+                for (int j0 = 0; j0 < kKT / kRowStep; j0 += 4) {
+                    uint32_t w[4 * kHalves][2];
+#pragma unroll
+                    for (int j = 0; j < 4 * kHalves; ++j)
+                        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                     : "=r"(w[j][0]), "=r"(w[j][1])
+                                     : "r"(from + (j0 + j / kHalves) * kRowStep * D +
+                                           64 * (j % kHalves ^ h0))
+                                     : "memory");
+#pragma unroll
+                    for (int j = 0; j < 4 * kHalves; ++j) {
+                        const uint32_t x = w[j][0] ^ kCodeBias, y = w[j][1] ^ kCodeBias;
+                        sts4(to + (j0 + j / kHalves) * kRowStep * 128 +
+                                 (j % kHalves ^ h0) * C::kSlab,
+                             fp16_codes(x, kCodesLow), fp16_codes(x, kCodesHigh),
+                             fp16_codes(y, kCodesLow), fp16_codes(y, kCodesHigh));
+                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    bar_arrive(&X.raw_empty[rw]);
+                    bar_arrive(&B.full[sl]);
+                }
+            }
+        }
     } else if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         // ------------------------------------------------------------ copies
+        const uint16_t *k16 = reinterpret_cast<const uint16_t *>(k_cache);
+        const uint16_t *v16 = reinterpret_cast<const uint16_t *>(v_cache);
         const int ct = threadIdx.x - 384;
         uint32_t seq = 0, done = 0, tile = 0;  // slots begun, slots handed over, tiles begun
         bool ok = true;
         // thread: chunk ch of rows r0, r0 + kRowStep, ... of a slot
-        constexpr int kChunks = D * (int)sizeof(typename C::Elem) / 16;  // of a row
-        constexpr int kRowStep = 128 / kChunks;
-        const int r0 = ct / kChunks, ch = ct % kChunks;
+        constexpr int kRowStep = 128 / (D / 8);
+        const int r0 = ct / (D / 8), ch = ct % (D / 8);
         const uint32_t my_chunk =
             (ch >> 3) * C::kSlab + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4);
         uint32_t scan = 0;  // 4 bits per slot: 1 + the piece's slot where values are looked at
-        // int8: the thread's key's scales of the newest tile and of the one before, by
-        // the tile's parity
-        float ks0 = 0.f, ks1 = 0.f, vs0 = 0.f, vs1 = 0.f;
-        // The scales of tile t into shared memory, the values' divided by the largest's
-        // power of two.  (The four warps meet for that, bounded.)
-        auto put_scales = [&](uint32_t t) {
-            if constexpr (CT == kI8) {
-                const float ks = t & 1 ? ks1 : ks0, vs = t & 1 ? vs1 : vs0;
-                // zeros and keys that nothing attends to say nothing; one that is not finite
-                // is further from the others than any
-                const unsigned e = __float_as_uint(vs) >> 23 & 255u;
-                const unsigned top = __reduce_max_sync(0xffffffffu, e == 255u ? 0u : e);
-                const unsigned low = __reduce_max_sync(
-                    0xffffffffu, vs == 0.0f ? 0u : e == 255u ? 511u : 255u - e);
-                if (lane == 0) {
-                    X.range[t & 1][ct >> 5] = top << 16 | low;
-                    bar_arrive(&X.meet);
-                }
-                if (!warp_wait(&X.meet, t & 1u, abort, a.error)) {
-                    ok = false;
-                    return;
-                }
-                unsigned r = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) r = __vmaxu2(r, X.range[t & 1][i]);
-                const int most = (int)(r >> 16), least = 255 - (int)(r & 0xffffu);
-                const bool wild = most - least > 8;
-                const int exp = wild ? 0 : min(max(most - 127, -126), 126);
-                const int at = t % kScaleTiles;
-                X.k[at][ct] = ks;
-                X.v[at][ct] = vs * pow2(-exp);
-                if (ct == 0) {
-                    X.exp[at] = exp;
-                    X.wild[at] = wild;
-                }
-            }
-        };
-        // int8: the oldest slots' codes, which this thread copied itself, into their slots
-        // as fp16 numbers
-        auto widen = [&](uint32_t upto) {
-            if constexpr (CT == kI8) {
-                while (ok && done < upto) {
-                    const uint32_t after = seq - done - 1;  // copies that may be on their way
-                    if (after == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-                    else if (after == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-                    else asm volatile("cp.async.wait_group 2;" ::: "memory");
-                    const uint32_t sl = done % NS;
-                    if (done >= NS &&
-                        !warp_wait(&B.empty[sl], (done / NS - 1) & 1u, abort, a.error)) {
-                        ok = false;
-                        break;
-                    }
-                    // keys of tile t are slot 2 t - 1 (0: 0); the last slot holds values
-                    const uint32_t kt = (done + 1) / 2;
-                    if ((done == 0 || done & 1) && kt < tile) put_scales(kt);
-                    if (!ok) break;
-                    const uint32_t from = ring + NS * C::kSlot + done % C::kRaws * C::kRaw + ct * 16;
-                    // row r0's chunks 2 ch and 2 ch + 1 of 8 numbers; half of the threads of
-                    // a row of 128 store the second first, so that every bank is met once
-                    const int c8 = 2 * ch & 7, other = D == 128 ? ch >> 2 & 1 : 0;
-                    const uint32_t slab = ring + sl * C::kSlot + (2 * ch >> 3) * C::kSlab + r0 * 128;
-                    const uint32_t to0 = slab + (((c8 + other) ^ (r0 & 7)) << 4);
-                    const uint32_t to1 = slab + (((c8 + 1 - other) ^ (r0 & 7)) << 4);
-#pragma unroll 2
-                    for (int j = 0; j < kKT / kRowStep; ++j) {
-                        uint32_t w[4], h[8];
-                        lds4(w, from + j * 2048);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t b = w[i] ^ kCodeBias;
-                            h[2 * i] = fp16_codes(b, kCodesLow);
-                            h[2 * i + 1] = fp16_codes(b, kCodesHigh);
-                        }
-                        const uint32_t d = j * kRowStep * 128;
-                        sts4(to0 + d, other ? h[4] : h[0], other ? h[5] : h[1],
-                             other ? h[6] : h[2], other ? h[7] : h[3]);
-                        sts4(to1 + d, other ? h[0] : h[4], other ? h[1] : h[5],
-                             other ? h[2] : h[6], other ? h[3] : h[7]);
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(&B.full[sl]);
-                    ++done;
-                }
-            }
-        };
         auto hand_over = [&](bool all) {
-            if constexpr (CT == kI8) {
-                widen(all ? seq : seq - (C::kRaws - 1));
-                return;
-            }
             if (all) asm volatile("cp.async.wait_group 0;" ::: "memory");
             else asm volatile("cp.async.wait_group 1;" ::: "memory");
             if (scan != 0) {
@@ -609,23 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // 128 rows of a cache into the next slot; lane l (of 8) holds the place of
         // rows 16 l .. 16 l + 15 in the caches, in bytes
-        auto copy_slot = [&](const typename C::Elem *cache, int64_t place, unsigned miss, int lo,
-                             int hi, uint32_t look) {
-            if constexpr (CT == kI8) {
-                // rows of no key are masked whatever they hold: codes are finite
-                const uint32_t to = ring + NS * C::kSlot + seq % C::kRaws * C::kRaw + ct * 16;
-                const char *src = reinterpret_cast<const char *>(cache) + (r0 & 15) * D + ch * 16;
-#pragma unroll
-                for (int j = 0; j < kKT / kRowStep; ++j) {
-                    const int block = (r0 + j * kRowStep) >> 4;  // of 16 rows
-                    const char *from = src + __shfl_sync(0xffffffffu, place, block);
-                    copy16(to + j * 2048, from, !(miss >> block & 1));
-                }
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                ++seq;
-                if (seq - done >= C::kRaws) hand_over(false);
-                return;
-            }
+        auto copy_slot = [&](const uint16_t *cache, int64_t place, unsigned miss, int lo, int hi,
+                             uint32_t look) {
             const uint32_t sl = seq % NS;
             if (seq >= NS) {
                 const uint32_t ph = (seq / NS - 1) & 1u;
@@ -714,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int key = r.key + 16 * (lane & 7);
                 lo = r.lo - r.key;
                 hi = r.hi - r.key;
-                if (CT != kI8 && key_range(a, key0, p.pos0 + 1).hi < r.key + kKT)
+                if (key_range(a, key0, p.pos0 + 1).hi < r.key + kKT)
                     look = 1 + (n - 1) % kItems;  // (the piece's first row does not see all)
                 entry = left > 1 ? page_of(key_range(a, key0 + kKT, p.keys)) : -1;
                 const bool there = e >= 0 && e < a.num_pages;
@@ -722,22 +853,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (there)
                     place = ((((int64_t)e * a.Hkv + p.head) << a.page_shift) +
                              (key & ((1 << a.page_shift) - 1))) *
-                            (D * (int)sizeof(typename C::Elem));
+                            (D * 2);
                 if (ct == 0) B.miss[tile % kMiss] = miss;
-                if constexpr (CT == kI8) {
-                    // this thread's key's scales, on their way until its codes are widened;
-                    // zeros for keys that the item does not have
-                    const int64_t row = __shfl_sync(0xffffffffu, place, ct >> 4) / D + (ct & 15);
-                    const bool in = !(miss >> (ct >> 4) & 1) && ct >= lo && ct < hi;
-                    const float ks = in ? __ldg(a.k_scale + row) : 0.f;
-                    const float vs = in ? __ldg(a.v_scale + row) : 0.f;
-                    if (tile & 1) ks1 = ks, vs1 = vs;
-                    else ks0 = ks, vs0 = vs;
-                }
             }
 #pragma unroll 1
             for (int kv = more ? 0 : 1; kv < (tile > 0 ? 2 : 1) && ok; ++kv)
-                copy_slot(kv ? v_cache : k_cache, kv ? v_place : place, kv ? v_miss : miss,
+                copy_slot(kv ? v16 : k16, kv ? v_place : place, kv ? v_miss : miss,
                           kv ? v_lo : lo, kv ? v_hi : hi, kv ? v_look : 0u);
             v_place = place;
             v_miss = miss;
@@ -847,127 +968,196 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_after();
-                uint32_t v[2][32];
-                tmem_ld32(area + C::kS0 + 64 * g, v[0]);
-                tmem_ld32(area + C::kS0 + 64 * g + 32, v[1]);
-                tmem_ld_wait();
-                const unsigned miss = B.miss[t % kMiss] >> (4 * g);
-                const float c = BF ? a.scale : a.scale * B.qmul[n & 1][r];
-                const int sc = t % kScaleTiles;
                 if constexpr (CT == kI8) {
-#pragma unroll
-                    for (int i = 0; i < 64; i += 4) {
-                        const float4 ks = *reinterpret_cast<const float4 *>(&X.k[sc][64 * g + i]);
-                        uint32_t (&w)[32] = v[i / 32];
-                        times2(w[i % 32], w[i % 32 + 1], ks.x, ks.y);
-                        times2(w[i % 32 + 2], w[i % 32 + 3], ks.z, ks.w);
+                    // Twice over the logits, 32 and 16 at a time, in short loops: all roles'
+                    // code shares the instruction cache, and with the 64 logits in registers
+                    // and every loop unrolled (as for 16 bits, whose code is shorter) a tile
+                    // took 7300 cycles instead of 6150.  A chunk's weights take its place.
+                    const int sc = t % kScaleTiles;
+                    if (!warp_wait(&X.scale_full[sc], (t / kScaleTiles) & 1u, abort, a.error)) {
+                        ok = false;
+                        break;
                     }
-                }
-                const KeyRange kr = key_range(a, key0, limit);
-                const int at = kr.key + 64 * g;  // this warp's 64 keys
-                if (__any_sync(0xffffffffu, at + 64 > kr.hi || at < kr.lo || (miss & 15u) != 0)) {
-                    // keys behind the row's own, in front of the suffix or of a
-                    // missing page: bit i of `seen` is clear
+                    const unsigned miss = B.miss[t % kMiss] >> (4 * g);
+                    const float c = a.scale * B.qmul[n & 1][r];
+                    const KeyRange kr = key_range(a, key0, limit);
+                    const int at = kr.key + 64 * g;  // this warp's 64 keys
+                    const bool cut =
+                        __any_sync(0xffffffffu, at + 64 > kr.hi || at < kr.lo || (miss & 15u) != 0);
+                    const bool wild = X.wild[sc];  // of the tile
+                    // keys that this row sees of the 32 from `first` (behind its own, in front
+                    // of the suffix or of a missing page: bit clear)
+                    auto seen = [&](int first) {
+                        const int hi = kr.hi - at - first, lo = kr.lo - at - first;
+                        unsigned bits = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1;
+                        if (lo > 0) bits = lo >= 32 ? 0u : bits & (~0u << lo);
+                        if (miss >> (first >> 4) & 1) bits &= 0xffff0000u;
+                        if (miss >> ((first >> 4) + 1) & 1) bits &= 0xffffu;
+                        return bits;
+                    };
+                    const float *kscale = &X.k[sc][64 * g], *vscale = &X.v[sc][64 * g];
+                    float mx = -INFINITY, top = -INFINITY;
+#pragma unroll 1
+                    for (int q = 0; q < 64; q += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(area + C::kS0 + 64 * g + q, v);
+                        tmem_ld_wait();
+                        times_scales(v, kscale + q);
+                        if (cut) hide(v, seen(q));
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int hi = kr.hi - at - 32 * q, lo = kr.lo - at - 32 * q;
-                        unsigned seen = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1;
-                        if (lo > 0) seen = lo >= 32 ? 0u : seen & (~0u << lo);
-                        if (miss >> (2 * q) & 1) seen &= 0xffff0000u;
-                        if (miss >> (2 * q + 1) & 1) seen &= 0xffffu;
+                        for (int i = 0; i < 32; i += 2)
+                            mx = fmaxf(mx,
+                                       fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+                        if (wild) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!(seen >> i & 1)) v[q][i] = 0xff800000u;
+                            for (int i = 0; i < 32; ++i)
+                                top = fmaxf(top, fmaf(__uint_as_float(v[i]), c,
+                                                      lg2(fabsf(vscale[q + i]))));
+                        }
                     }
-                }
-                float mx = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 64; i += 2)
-                    mx = fmaxf(mx, fmaxf(__uint_as_float(v[i / 32][i % 32]),
-                                         __uint_as_float(v[i / 32][i % 32 + 1])));
-                // the row's maximum, with the other half's; every logit of these
-                // rows is in registers from here on
-                B.half_max[t & 1][g][r] = mx;
-                bool wild = false;  // of the tile
-                if constexpr (CT == kI8) {
-                    wild = X.wild[sc];
+                    // the row's maximum, with the other half's
+                    B.half_max[t & 1][g][r] = mx;
+                    if (wild) X.half_top[t & 1][g][r] = top;
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&B.pair[w]);
+                    if (!warp_wait(&B.pair[w], t & 1u, abort, a.error)) {
+                        ok = false;
+                        break;
+                    }
+                    mx = fmaxf(mx, B.half_max[t & 1][1 - g][r]);
+                    // (see below)
+                    const float m = mx == -INFINITY ? 0.0f : __fmaf_ru(mx, c, -kBias);
+                    const unsigned long long c2 = pk(c, c), m2 = pk(-m, -m);
+                    unsigned long long sum2 = 0;
+                    // of a wild tile's row: its largest weight is near 2^kBias
+                    int shift = 0;
                     if (wild) {
-                        float top = -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            top = fmaxf(top, fmaf(__uint_as_float(v[i / 32][i % 32]), c,
-                                                  lg2(fabsf(X.v[sc][64 * g + i]))));
-                        X.half_top[t & 1][g][r] = top;
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) bar_arrive(&B.pair[w]);
-                if (!warp_wait(&B.pair[w], t & 1u, abort, a.error)) {
-                    ok = false;
-                    break;
-                }
-                mx = fmaxf(mx, B.half_max[t & 1][1 - g][r]);
-                // (rounded up: mx c is exact, so the largest exponent is 12 at most, and
-                // at least 0 where 12 is less than the maximum's last place)
-                const float m = mx == -INFINITY ? 0.0f : __fmaf_ru(mx, c, -kBias);
-                const unsigned long long c2 = pk(c, c), m2 = pk(-m, -m);
-                unsigned long long sum2 = 0;
-                int shift = 0;  // of a wild tile's row: its largest weight is near 2^kBias
-                if constexpr (CT == kI8) {
-                    if (wild) {
-                        const float top = fmaxf(X.half_top[t & 1][0][r], X.half_top[t & 1][1][r]);
+                        top = fmaxf(X.half_top[t & 1][0][r], X.half_top[t & 1][1][r]);
                         shift = (int)fminf(fmaxf(kBias - ceilf(top - m), -126.0f), 126.0f);
                     }
-                }
-                // per 16 keys 8 columns of each part
+#pragma unroll 1
+                    for (int q = 0; q < 64; q += 16) {
+                        uint32_t v[16], parts[2][8];
+                        const uint32_t chunk = area + C::kS0 + 64 * g + q;
+                        tmem_ld16(chunk, v);
+                        tmem_ld_wait();
+                        times_scales(v, kscale + q);
+                        if (cut) hide(v, q & 16 ? seen(q - 16) >> 16 : seen(q));
+                        float x[16];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t parts[NP][8];
+                        for (int i = 0; i < 16; i += 2) {
+                            upk(fma2(pk(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), c2, m2),
+                                x[i], x[i + 1]);
+                            x[i] = ex2(x[i]);
+                            x[i + 1] = ex2(x[i + 1]);
+                            sum2 = add2(sum2, pk(x[i], x[i + 1]));
+                        }
+                        if (wild) {
+                            // (a masked key's scale need not be finite; the shift in two
+                            // steps, none of which leaves fp32's range)
+                            const float s1 = pow2(shift / 2), s2 = pow2(shift - shift / 2);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int e = 16 * (q & 1) + 2 * i;
-                        float x, y;
-                        upk(fma2(pk(__uint_as_float(v[q >> 1][e]),
-                                    __uint_as_float(v[q >> 1][e + 1])),
-                                 c2, m2),
-                            x, y);
-                        x = ex2(x);
-                        y = ex2(y);
-                        sum2 = add2(sum2, pk(x, y));
-                        if constexpr (CT == kI8) {
-                            // the weights of the codes
-                            const float2 vs = *reinterpret_cast<const float2 *>(
-                                &X.v[sc][64 * g + 16 * q + 2 * i]);
-                            if (wild) {
-                                // (a masked key's scale need not be finite; the shift
-                                // in two steps, none of which leaves fp32's range)
-                                const uint32_t none = 0xff800000u;
-                                const float s1 = pow2(shift / 2), s2 = pow2(shift - shift / 2);
-                                x = v[q >> 1][e] == none ? 0.0f : x * s1 * vs.x * s2;
-                                y = v[q >> 1][e + 1] == none ? 0.0f : y * s1 * vs.y * s2;
-                            } else {
-                                upk(mul2(pk(x, y), pk(vs.x, vs.y)), x, y);
+                            for (int i = 0; i < 16; ++i)
+                                x[i] = v[i] == 0xff800000u ? 0.0f : x[i] * s1 * vscale[q + i] * s2;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; i += 4) {
+                                const float4 vs = *reinterpret_cast<const float4 *>(vscale + q + i);
+                                upk(mul2(pk(x[i], x[i + 1]), pk(vs.x, vs.y)), x[i], x[i + 1]);
+                                upk(mul2(pk(x[i + 2], x[i + 3]), pk(vs.z, vs.w)), x[i + 2],
+                                    x[i + 3]);
                             }
                         }
-                        uint32_t z[NP];
-                        split16<BF, NP>(x, y, z);
 #pragma unroll
-                        for (int part = 0; part < NP; ++part) parts[part][i] = z[part];
+                        for (int i = 0; i < 8; ++i) {
+                            uint32_t z[2];
+                            split16<false, 2>(x[2 * i], x[2 * i + 1], z);
+                            parts[0][i] = z[0];
+                            parts[1][i] = z[1];
+                        }
+                        tmem_st8(chunk, parts[0]);
+                        tmem_st8(chunk + 8, parts[1]);
                     }
+                    float sa, sb;
+                    upk(sum2, sa, sb);
+                    // (the second half's maximum is not looked at: what P V is to be
+                    // multiplied by stands in its place)
+                    B.stat[t % kStats][g][r] =
+                        make_float2(g ? pow2(X.exp[sc] - shift) : mx == -INFINITY ? mx : m, sa + sb);
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&X.scale_empty[sc]);
+                } else {
+                    uint32_t v[2][32];
+                    tmem_ld32(area + C::kS0 + 64 * g, v[0]);
+                    tmem_ld32(area + C::kS0 + 64 * g + 32, v[1]);
+                    tmem_ld_wait();
+                    const unsigned miss = B.miss[t % kMiss] >> (4 * g);
+                    const float c = BF ? a.scale : a.scale * B.qmul[n & 1][r];
+                    const KeyRange kr = key_range(a, key0, limit);
+                    const int at = kr.key + 64 * g;  // this warp's 64 keys
+                    if (__any_sync(0xffffffffu, at + 64 > kr.hi || at < kr.lo || (miss & 15u) != 0)) {
+                        // keys behind the row's own, in front of the suffix or of a
+                        // missing page: bit i of `seen` is clear
 #pragma unroll
-                    for (int part = 0; part < NP; ++part)
-                        tmem_st8(area + 8 * NP * (4 * g + q) + 8 * part, parts[part]);
+                        for (int q = 0; q < 2; ++q) {
+                            const int hi = kr.hi - at - 32 * q, lo = kr.lo - at - 32 * q;
+                            unsigned seen = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1;
+                            if (lo > 0) seen = lo >= 32 ? 0u : seen & (~0u << lo);
+                            if (miss >> (2 * q) & 1) seen &= 0xffff0000u;
+                            if (miss >> (2 * q + 1) & 1) seen &= 0xffffu;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!(seen >> i & 1)) v[q][i] = 0xff800000u;
+                        }
+                    }
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2)
+                        mx = fmaxf(mx, fmaxf(__uint_as_float(v[i / 32][i % 32]),
+                                             __uint_as_float(v[i / 32][i % 32 + 1])));
+                    // the row's maximum, with the other half's; every logit of these
+                    // rows is in registers from here on
+                    B.half_max[t & 1][g][r] = mx;
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&B.pair[w]);
+                    if (!warp_wait(&B.pair[w], t & 1u, abort, a.error)) {
+                        ok = false;
+                        break;
+                    }
+                    mx = fmaxf(mx, B.half_max[t & 1][1 - g][r]);
+                    // (rounded up: mx c is exact, so the largest exponent is 12 at most, and
+                    // at least 0 where 12 is less than the maximum's last place)
+                    const float m = mx == -INFINITY ? 0.0f : __fmaf_ru(mx, c, -kBias);
+                    const unsigned long long c2 = pk(c, c), m2 = pk(-m, -m);
+                    unsigned long long sum2 = 0;
+                    // per 16 keys 8 columns of each part
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t parts[NP][8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int e = 16 * (q & 1) + 2 * i;
+                            float x, y;
+                            upk(fma2(pk(__uint_as_float(v[q >> 1][e]),
+                                        __uint_as_float(v[q >> 1][e + 1])),
+                                     c2, m2),
+                                x, y);
+                            x = ex2(x);
+                            y = ex2(y);
+                            sum2 = add2(sum2, pk(x, y));
+                            uint32_t z[NP];
+                            split16<BF, NP>(x, y, z);
+#pragma unroll
+                            for (int part = 0; part < NP; ++part) parts[part][i] = z[part];
+                        }
+#pragma unroll
+                        for (int part = 0; part < NP; ++part)
+                            tmem_st8(area + 8 * NP * (4 * g + q) + 8 * part, parts[part]);
+                    }
+                    float sa, sb;
+                    upk(sum2, sa, sb);
+                    B.stat[t % kStats][g][r] = make_float2(mx == -INFINITY ? mx : m, sa + sb);
                 }
-                float sa, sb;
-                upk(sum2, sa, sb);
-                // (the second half's maximum is not looked at: int8 has what P V is to be
-                // multiplied by in its place)
-                const float first = mx == -INFINITY ? mx : m;
-                if constexpr (CT == kI8)
-                    B.stat[t % kStats][g][r] = make_float2(
-                        g ? pow2(X.exp[sc] - shift) : first, sa + sb);
-                else
-                    B.stat[t % kStats][g][r] = make_float2(first, sa + sb);
                 tmem_st_wait();
                 tc_before();
                 __syncwarp();
