@@ -212,6 +212,7 @@ __device__ __forceinline__ float *row_target(const PagedArgs &a) {
 
 }  // namespace
 
+constexpr int kRowsI8Step = 32;  // keys per step of the int8 cache's
 // The kernels for at most 16 rows per item (paged_rows_i8.cu, paged_rows.cu): rows = 8
 // or 16.
 sq_status launch_paged_rows_i8(const PagedArgs &a, const void *k_cache, const void *v_cache, int D,

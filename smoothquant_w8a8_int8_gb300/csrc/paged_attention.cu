@@ -140,7 +140,7 @@ sq_status launch_paged_attention(const PagedCall &c, cudaStream_t st) {
         const int64_t most = phase ? tokens : max_q;
         const bool few = few_rows(most, a.G);
         const int r = few ? (std::max<int64_t>(1, most) * a.G <= 8 ? 8 : 16) : 128;
-        const int kt = few ? 16 : 128;
+        const int kt = !few ? 128 : i8 ? kRowsI8Step : 16;
         a.after_prefix = few && !phase && c.prefix_len > 0 && !front;
         a.tpt = r / a.G;
         a.kstart = phase ? 0 : a.prefix_len / kt * kt;

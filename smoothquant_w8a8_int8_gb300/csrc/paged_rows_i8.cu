@@ -5,7 +5,7 @@
 //   logit = y k_scale,  p = 2^(logit - m),  l += p,  O += (p v_scale) codes:
 // the scales stand at the logits and the probabilities, the codes enter the products
 // as they are.  The rest is paged_rows.cu's: a worker is a warp with a ring of its own,
-// filled with cp.async by steps of 16 keys, products on the warp-level tensor
+// filled with cp.async by steps of 32 keys, products on the warp-level tensor
 // instructions (m16n8k16), the running maximum, the pieces' join.
 //
 // Half the cache's bytes per key leave half the time for each, so the codes' way into
@@ -31,18 +31,18 @@
 namespace sq {
 namespace {
 
-constexpr int kKT = 16;  // keys per step
+constexpr int kKT = kRowsI8Step;  // keys per step
 constexpr int kWarps = 8;
-constexpr int kPad = 2;       // an item's start and end, in steps
-constexpr int kMinSteps = 4;  // steps of a worker's share at least
+constexpr int kPad = 1;       // an item's start and end, in steps
+constexpr int kMinSteps = 2;  // steps of a worker's share at least
 constexpr int kJoin = 16;     // pieces of an item that are joined in one go
-constexpr int kPieces = 16;   // more than the steps that the copies are ahead
+constexpr int kPieces = 8;    // more than the steps that the copies are ahead
 
 template <int D>
 struct RowsI8Cfg {
     static constexpr int kCodes = kKT * D;                       // bytes of the keys or values
     static constexpr int kStepBytes = 2 * kCodes + 2 * kKT * 4;  // and both scales
-    static constexpr int kStages = D == 128 ? 6 : 10;
+    static constexpr int kStages = D == 128 ? 3 : 6;
     static constexpr int kSmem = kWarps * kStages * kStepBytes;
     static_assert(kStages < kPieces, "a piece per step in flight and the one being worked on");
 };
@@ -114,28 +114,39 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                             ? __ldg((kr.front ? a.prefix_pages : table) + at)
                             : -1;
             }
-            const int e = __shfl_sync(0xffffffffu, entry, idx & 31);
-            const bool there = e >= 0 && e < a.num_pages;
-            holes = (holes & ~(1u << buf)) | (there ? 0u : 1u << buf);
-            const int64_t row0 = (there ? (((int64_t)e * a.Hkv) << a.page_shift) + head_row : 0) +
-                                 (kr.key & ((1 << a.page_shift) - 1));
-            // lane: chunk lane % kLanes of row lane / kLanes of every kStride rows; the
-            // step's 16 rows are contiguous in the cache.  (Rows of no key are masked
-            // whatever they hold: codes are finite.)
-            constexpr int kLanes = D / 16, kCopies = C::kCodes / 512, kStride = 32 / kLanes;
+            // the step's two blocks of 16 rows: each lies in a page, contiguous in the cache
+            const int in_page = kr.key & ((1 << a.page_shift) - 1);
+            const int second = (kr.key + 16) >> a.page_shift;
+            constexpr int kLanes = D / 16, kCopies = C::kCodes / 1024, kStride = 32 / kLanes;
             const int r0 = lane / kLanes, ch = lane % kLanes;
             const uint32_t dst = ring + buf * C::kStepBytes;
-            const int8_t *ks = k_cache + row0 * D + lane * 16, *vs = v_cache + row0 * D + lane * 16;
+            holes &= ~(3u << 2 * buf);
+            int64_t rows[2];
+            bool there[2];
 #pragma unroll
-            for (int j = 0; j < kCopies; ++j) {
-                const uint32_t d = dst + place<D>(r0 + j * kStride, ch);
-                copy16(d, ks + j * 512, there);
-                copy16(d + C::kCodes, vs + j * 512, there);
+            for (int h = 0; h < 2; ++h) {
+                // (both entries are in the lanes: a step begins at an even one or in a page)
+                const int e = __shfl_sync(0xffffffffu, entry, (h ? second : idx) & 31);
+                there[h] = e >= 0 && e < a.num_pages;
+                holes |= (there[h] ? 0u : 1u) << (2 * buf + h);
+                const int at = h && second != idx ? 0 : in_page + 16 * h;
+                rows[h] = there[h] ? (((int64_t)e * a.Hkv) << a.page_shift) + head_row + at : 0;
+                // lane: chunk lane % kLanes of row lane / kLanes of every kStride rows.  (Rows
+                // of no key are masked whatever they hold: codes are finite.)
+                const int8_t *ks = k_cache + rows[h] * D + lane * 16;
+                const int8_t *vs = v_cache + rows[h] * D + lane * 16;
+#pragma unroll
+                for (int j = 0; j < kCopies; ++j) {
+                    const uint32_t d = dst + place<D>(16 * h + r0 + j * kStride, ch);
+                    copy16(d, ks + j * 512, there[h]);
+                    copy16(d + C::kCodes, vs + j * 512, there[h]);
+                }
             }
             if (lane < 2 * kKT / 4)
                 copy16(dst + 2 * C::kCodes + lane * 16,
-                       (lane < kKT / 4 ? a.k_scale : a.v_scale) + row0 + lane % (kKT / 4) * 4,
-                       there);
+                       (lane < kKT / 4 ? a.k_scale : a.v_scale) +
+                           (lane & 4 ? rows[1] : rows[0]) + lane % 4 * 4,
+                       lane & 4 ? there[1] : there[0]);
             key += kKT;
             --left;
         }
@@ -237,66 +248,69 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             __syncwarp();
             const uint32_t ks = ring + cur * C::kStepBytes;
             const uint32_t vs = ks + C::kCodes, sc = ks + 2 * C::kCodes;
-            // logits of the rows x 16 keys
-            float s[2][2][4];
+            // logits of the rows x 32 keys
+            float s[4][4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i >> 3][i >> 2 & 1][i & 3] = 0.0f;
+            for (int i = 0; i < 16; ++i) s[i >> 2][i & 3] = 0.0f;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
-                uint32_t w[2][4];
-                lds4(w[0], ks + place<D>(g, t + 4 * c));
-                lds4(w[1], ks + place<D>(g + 8, t + 4 * c));
+                uint32_t w[4][4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) lds4(w[h], ks + place<D>(g + 8 * h, t + 4 * c));
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < 4; ++h) {
                         const uint32_t b = w[h][i] ^ kCodeBias;
                         const uint32_t b0 = fp16_codes(b, kCodesLow), b1 = fp16_codes(b, kCodesHigh);
 #pragma unroll
                         for (int j = 0; j < S; ++j)
-                            mma16816<false>(s[i & 1][h], qf[4 * c + i][j], b0, b1);
+                            mma16816<false>(s[h], qf[4 * c + i][j], b0, b1);
                     }
             }
-            // x[row][key]: keys 2t, 2t + 1, 2t + 8, 2t + 9 of the step
-            float x[R][4], kf[4], vf[4];
+            // x[row][key]: element 2 h + b is key 8 h + 2 t + b of the step
+            float x[R][8], vf[8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < 4; ++h) {
                 const float2 k2 = lds_f2(sc + (8 * h + 2 * t) * 4);
                 const float2 v2 = lds_f2(sc + (kKT + 8 * h + 2 * t) * 4);
-                kf[2 * h] = k2.x;
-                kf[2 * h + 1] = k2.y;
                 vf[2 * h] = v2.x;
                 vf[2 * h + 1] = v2.y;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float c0 = s[0][e >> 1][e & 1] + s[1][e >> 1][e & 1];
-                const float c1 = s[0][e >> 1][2 + (e & 1)] + s[1][e >> 1][2 + (e & 1)];
-                if (R == 1) x[0][e] = (c0 + c1) * kf[e];
-                else x[0][e] = c0 * kf[e], x[R - 1][e] = c1 * kf[e];
+                if (R == 1) {
+                    x[0][2 * h] = (s[h][0] + s[h][2]) * k2.x;
+                    x[0][2 * h + 1] = (s[h][1] + s[h][3]) * k2.y;
+                } else {
+                    x[0][2 * h] = s[h][0] * k2.x;
+                    x[0][2 * h + 1] = s[h][1] * k2.y;
+                    x[R - 1][2 * h] = s[h][2] * k2.x;
+                    x[R - 1][2 * h + 1] = s[h][3] * k2.y;
+                }
             }
             // keys that are masked: behind the row's own, in front of the
             // suffix, or of a page that is missing
             const KeyRange kr = key_range(a, key0, limit[0]);
             const int hi1 = R == 1 ? 0 : key_range(a, key0, limit[R - 1]).hi;
+            const unsigned missing = holes >> 2 * cur & 3u;
             bool cut = kr.key < kr.lo || kr.key + kKT > kr.hi ||
-                       (R > 1 && kr.key + kKT > hi1) || (holes >> cur & 1);
+                       (R > 1 && kr.key + kKT > hi1) || missing;
             cut = __any_sync(0xffffffffu, cut);
             if (cut) {
-                const bool missing = holes >> cur & 1;
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 8; ++i) {
                         const int k = kr.key + 8 * (i >> 1) + 2 * t + (i & 1);
-                        if (missing || k >= (r ? hi1 : kr.hi) || k < kr.lo) x[r][i] = -INFINITY;
+                        if ((missing >> (i >> 2) & 1) || k >= (r ? hi1 : kr.hi) || k < kr.lo)
+                            x[r][i] = -INFINITY;
                     }
             }
             float grow[R];
             bool any = false;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                float mx = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
+                float mx = x[r][0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[r][i]);
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 const float mn = mx == -INFINITY ? m[r] : fmaxf(m[r], mx * scale[r]);
@@ -315,16 +329,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                         o[i][2 * r + 1] *= grow[r];
                     }
             }
-            uint32_t pf[S][4];
+            uint32_t pf[2][S][4];  // of the step's two blocks of 16 keys
             float down[R];
             {
-                float w[2][R][2];
+                float w[4][R][2];
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const float from = m[r] == -INFINITY ? 0.0f : -m[r];  // (no key yet)
                     float top = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 8; ++i) {
                         const float pr = ex2(fmaf(x[r][i], scale[r], from));
                         l[r] += pr;
                         // (a masked key's scale need not be finite)
@@ -338,41 +352,49 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     const float up = pow2(-e);
                     down[r] = pow2(e);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i >> 1][r][i & 1] *= up;
+                    for (int i = 0; i < 8; ++i) w[i >> 1][r][i & 1] *= up;
                 }
-                F::fill(w[0], 0, pf);
-                F::fill(w[1], 2, pf);
-            }
-            // the values of this thread's keys: NT bytes of each
-            constexpr int NW = NT / 4;
-            uint32_t v[4][NW];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+                for (int h = 0; h < 2; ++h) {
+                    F::fill(w[2 * h], 0, pf[h]);
+                    F::fill(w[2 * h + 1], 2, pf[h]);
+                }
+            }
+            // the values of this thread's keys, NT bytes of each: v[h][i] of key 8 (2 h + i / 2)
+            // + 2 t + i % 2
+            constexpr int NW = NT / 4;
+            uint32_t v[2][4][NW];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
                 const int r = 8 * (i >> 1) + 2 * t + (i & 1);
+                uint32_t (&y)[NW] = v[i >> 2][i & 3];
                 if constexpr (D == 128) {
-                    lds4(v[i], vs + place<D>(r, g));
+                    lds4(y, vs + place<D>(r, g));
                 } else {
                     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                                 : "=r"(v[i][0]), "=r"(v[i][1])
+                                 : "=r"(y[0]), "=r"(y[1])
                                  : "r"(vs + place<D>(r, g >> 1) + 8 * (g & 1))
                                  : "memory");
                 }
 #pragma unroll
-                for (int j = 0; j < NW; ++j) v[i][j] ^= kCodeBias;
+                for (int j = 0; j < NW; ++j) y[j] ^= kCodeBias;
             }
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                // byte i of keys 2t and 2t + 1, and of 2t + 8 and 2t + 9
+                // byte i of keys 2 t and 2 t + 1, and of 2 t + 8 and 2 t + 9
                 const int j = i / 4;
                 const uint32_t pair = i & 2 ? 0x7362u : 0x5140u;
                 const uint32_t half = i & 1 ? kCodesHigh : kCodesLow;
-                const uint32_t b0 = fp16_codes(__byte_perm(v[0][j], v[1][j], pair), half);
-                const uint32_t b1 = fp16_codes(__byte_perm(v[2][j], v[3][j], pair), half);
                 // (the instruction's accumulator truncates: the step's products alone go
                 // through it)
                 float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < S; ++k) mma16816<false>(c, pf[k], b0, b1);
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t b0 = fp16_codes(__byte_perm(v[h][0][j], v[h][1][j], pair), half);
+                    const uint32_t b1 = fp16_codes(__byte_perm(v[h][2][j], v[h][3][j], pair), half);
+#pragma unroll
+                    for (int k = 0; k < S; ++k) mma16816<false>(c, pf[h][k], b0, b1);
+                }
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     if (R == 1) {

@@ -186,7 +186,7 @@ struct TilesCfg {
     static constexpr int kS0 = kArea - 128;
     // an item's start and end in key tiles (bf16: 2, 4, 6, 8 measured 755, 692,
     // 708, 735 us for two prompts of 4096 tokens; fp16: 672, 534, 506, 528)
-    static constexpr int kPad = BF ? 4 : 6;
+    static constexpr int kPad = BF || CT == kI8 ? 4 : 6;
     static constexpr int kPVs = BF ? 1 : 2;
     static constexpr int kPV0 = 2 * kArea;
 };
@@ -320,6 +320,18 @@ __device__ __forceinline__ float lg2(float x) {
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+        "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+        "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -666,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (X.raw_stop[rw]) break;
                 if (d >= NS && !warp_wait(&B.empty[sl], (d / NS - 1) & 1u, abort, a.error)) break;
                 const uint32_t from = from0 + rw * C::kRaw, to = to0 + sl * C::kSlot;
-#pragma unroll
+#pragma unroll 1
                 for (int j0 = 0; j0 < kKT / kRowStep; j0 += 4) {
                     uint32_t w[4 * kHalves][2];
 #pragma unroll
@@ -971,8 +983,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (CT == kI8) {
                     // Twice over the logits, 32 and 16 at a time, in short loops: all roles'
                     // code shares the instruction cache, and with the 64 logits in registers
-                    // and every loop unrolled (as for 16 bits, whose code is shorter) a tile
-                    // took 7300 cycles instead of 6150.  A chunk's weights take its place.
+                    // and every loop unrolled (as for 16 bits, whose code is shorter) prompts
+                    // took 897 us instead of 772.  The logits go back to tensor memory with
+                    // their scales applied and masked (702 us): a scale that every lane reads
+                    // from shared memory is a cycle of its pipe, which the products and the
+                    // widening want too.  A chunk's weights take its place.
                     const int sc = t % kScaleTiles;
                     if (!warp_wait(&X.scale_full[sc], (t / kScaleTiles) & 1u, abort, a.error)) {
                         ok = false;
@@ -996,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         return bits;
                     };
                     const float *kscale = &X.k[sc][64 * g], *vscale = &X.v[sc][64 * g];
-                    float mx = -INFINITY, top = -INFINITY;
+                    float mx = -INFINITY;
 #pragma unroll 1
                     for (int q = 0; q < 64; q += 32) {
                         uint32_t v[32];
@@ -1004,20 +1019,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld_wait();
                         times_scales(v, kscale + q);
                         if (cut) hide(v, seen(q));
+                        tmem_st32(area + C::kS0 + 64 * g + q, v);
 #pragma unroll
                         for (int i = 0; i < 32; i += 2)
                             mx = fmaxf(mx,
                                        fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
-                        if (wild) {
+                    }
+                    tmem_st_wait();
+                    // the row's maximum, with the other half's
+                    B.half_max[t & 1][g][r] = mx;
+                    if (wild) {
+                        float top = -INFINITY;
+#pragma unroll 1
+                        for (int q = 0; q < 64; q += 16) {
+                            uint32_t v[16];
+                            tmem_ld16(area + C::kS0 + 64 * g + q, v);
+                            tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
+                            for (int i = 0; i < 16; ++i)
                                 top = fmaxf(top, fmaf(__uint_as_float(v[i]), c,
                                                       lg2(fabsf(vscale[q + i]))));
                         }
+                        X.half_top[t & 1][g][r] = top;
                     }
-                    // the row's maximum, with the other half's
-                    B.half_max[t & 1][g][r] = mx;
-                    if (wild) X.half_top[t & 1][g][r] = top;
                     __syncwarp();
                     if (lane == 0) bar_arrive(&B.pair[w]);
                     if (!warp_wait(&B.pair[w], t & 1u, abort, a.error)) {
@@ -1032,7 +1056,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // of a wild tile's row: its largest weight is near 2^kBias
                     int shift = 0;
                     if (wild) {
-                        top = fmaxf(X.half_top[t & 1][0][r], X.half_top[t & 1][1][r]);
+                        const float top =
+                            fmaxf(X.half_top[t & 1][0][r], X.half_top[t & 1][1][r]);
                         shift = (int)fminf(fmaxf(kBias - ceilf(top - m), -126.0f), 126.0f);
                     }
 #pragma unroll 1
@@ -1041,8 +1066,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t chunk = area + C::kS0 + 64 * g + q;
                         tmem_ld16(chunk, v);
                         tmem_ld_wait();
-                        times_scales(v, kscale + q);
-                        if (cut) hide(v, q & 16 ? seen(q - 16) >> 16 : seen(q));
                         float x[16];
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
