@@ -20,6 +20,7 @@ struct GatedOut {
     const float *bias_gate, *bias_up;  // [F], nullable
     int F;
     int act;       // sq_gate
+    int group;     // row blocks that share a pass over the weights (grouped_item_at)
     float c1, c3;  // the logistic function's argument, times -log2 e (see sigmoid_gate2)
 };
 

@@ -1027,6 +1027,28 @@ __device__ __forceinline__ int exact_pass_kb(const EpiArgs &args, int nkb, int w
     return min(mx, mw) <= kSinglePassL1 ? nkb : KB_PER_CHUNK;
 }
 
+// The same for the gated kernels, whose weights have many rows (24,576 norms took 6 us
+// of a decoding step's 45): the other operand's norms alone decide if they can.
+__device__ __forceinline__ int exact_pass_kb_gated(const EpiArgs &args, int nkb, int warp,
+                                                   int lane, int32_t (*l1max)[2]) {
+    if (warp == 0 || nkb <= KB_PER_CHUNK) return KB_PER_CHUNK;
+    const int tid = threadIdx.x - 32;
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+        const int32_t *l1 = side ? args.w_l1 : args.x_l1;
+        if (!l1) continue;
+        const int rows = side ? args.N : args.M;
+        int32_t most = 0;
+        for (int i = tid; i < rows; i += THREADS - 32) most = max(most, __ldg(l1 + i));
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) l1max[warp - 1][side] = most;
+        asm volatile("bar.sync 1, %0;" ::"n"(THREADS - 32) : "memory");
+        for (int w = 0; w < 9; ++w) most = max(most, l1max[w][side]);
+        if (most <= kSinglePassL1) return nkb;
+    }
+    return KB_PER_CHUNK;
+}
+
 template <int MODE, int OUT>
 __global__ void __launch_bounds__(THREADS, 1)
     gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -1074,7 +1096,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     // K per exact fp32 pass: 1024, or all of K when the row L1 norms of either
     // operand bound every partial sum below 2^24.  Decided by warps 1..9 (the
     // MMA issuer and the epilogue); the producer does not need it.
-    const int chunk_kb = exact_pass_kb(args, nkb, warp, lane, S.l1max);
+    const int chunk_kb = OUT == kOutGated ? exact_pass_kb_gated(args, nkb, warp, lane, S.l1max)
+                                          : exact_pass_kb(args, nkb, warp, lane, S.l1max);
     const int nchunks = (nkb + chunk_kb - 1) / chunk_kb;
 
     if (warp == 0) {
@@ -1241,6 +1264,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 else
                     epilogue_tile<MODE, true, OUT>(T, m, nb, row0, lane, args, xs, cp, rnext,
                                                      &tmY, stg, nsl);
+            } else if (OUT == kOutGated && row0 >= M) {
+                // (no rows of Y: no sums to join)
             } else if (sk_fixup(T, nchunks == 1, t, ew, lane, args, abort_flag)) {
                 fetch();
                 epilogue_tile<MODE, true, OUT>(T, m, nb, row0, lane, args, xs, cp, rnext, &tmY,
@@ -1359,8 +1384,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     const PairSchedule sched =
         make_pair_schedule((M + 2 * BM - 1) / (2 * BM), (N + BN - 1) / BN, args.pair_plan);
     const int num_items = sched.items;
+    auto item_at = [&](int i, int &m0, int &n0, int &bn) {
+        if (OUT == kOutGated) grouped_item_at(sched, args.gt.group, i, m0, n0, bn);
+        else pair_item_at(sched, i, m0, n0, bn);
+    };
     const int nkb = (K + BK - 1) / BK;
-    const int chunk_kb = exact_pass_kb(args, nkb, warp, lane, S.l1max);
+    const int chunk_kb = OUT == kOutGated ? exact_pass_kb_gated(args, nkb, warp, lane, S.l1max)
+                                          : exact_pass_kb(args, nkb, warp, lane, S.l1max);
     const int nchunks = (nkb + chunk_kb - 1) / chunk_kb;
 
     if (warp == 0) {
@@ -1370,7 +1400,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint32_t phase = 0;
             for (int i = cluster_id; i < num_items; i += num_clusters) {
                 int pm0, n0, bn;
-                pair_item_at(sched, i, pm0, n0, bn);
+                item_at(i, pm0, n0, bn);
                 const int m0 = pm0 + (int)rank * BM;
                 const int nB = n0 + (int)rank * (bn / 2);  // this CTA's rows of B
                 const CUtensorMap *mapB = bn == BN ? &tmB : &tmBq;
@@ -1412,7 +1442,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             int it = 0;
             for (int i = cluster_id; i < num_items; i += num_clusters, ++it) {
                 int pm0, n0, bn;
-                pair_item_at(sched, i, pm0, n0, bn);
+                item_at(i, pm0, n0, bn);
                 const uint32_t idesc = idesc_pair(bn);
                 for (int c = 0; c < nchunks; ++c) {
                     const uint32_t b = nchunks == 1 ? (uint32_t)(it & 1) : 0u;
@@ -1463,7 +1493,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int it = 0;
         for (int i = cluster_id; i < num_items; i += num_clusters, ++it) {
             int pm0, n0, bn;
-            pair_item_at(sched, i, pm0, n0, bn);
+            item_at(i, pm0, n0, bn);
             const int m0 = pm0 + (int)rank * BM;
             const int row0 = m0 + q * 32;
             const int64_t m = (int64_t)row0 + lane;
@@ -1684,6 +1714,12 @@ sq_status launch_pair_mode(const CUtensorMap &ta, const CUtensorMap &tbp, const 
     return launch_pair_kernel<MODE, kOutPlain>(ta, tbp, tbq, ty, args, K, device, st);
 }
 
+// Row blocks of a gated launch that share a pass over the weights: 8 where these take
+// more than half of L2 (129 MB), else all of the weights stay there.  Measured (8192 x
+// 4096 x 12288, 201 MB): 1, 4, 8, 16 row blocks
+// 1279, 1172, 1168, 1168 us.
+int gated_group(int64_t weight_bytes) { return weight_bytes > (64ll << 20) ? 8 : 1; }
+
 // Which kernel runs a launch: CTA pairs for every launch of at least one full
 // 256-row pair tile that is not split over K.
 bool use_pair(int64_t M, const Schedule &sched) {
@@ -1754,6 +1790,7 @@ sq_status launch_gemm_tc(const __nv_bfloat16 *Xop, const float *sx, const int32_
                   (!rq->Yop || aligned16(rq->Yop));
     args.rq_fast = rq && rq->scale >= 0x1p-70f;
     args.gt = gated ? *gated : GatedOut{};
+    if (gated) args.gt.group = gated_group(N * K * 2);
     args.rm_pairs = reinterpret_cast<const float4 *>(rm_pairs);
     args.row_amax = row_amax;
     CUtensorMap ta, tb, tbs, ty;

@@ -32,16 +32,34 @@ __device__ __forceinline__ void turn_pair(float &x, float &y, float c, float s) 
     x = __fsub_rn(__fmul_rn(x0, c), __fmul_rn(y0, s));
     y = __fadd_rn(__fmul_rn(x0, s), __fmul_rn(y0, c));
 }
-// Four codes of a row with this scale, the first in the low byte.  Below 2^-100 the
-// reciprocal may leave fp32's range.
-__device__ __forceinline__ uint32_t codes4(float4 x, float scale, float rscale) {
+// Four codes of a row, the first in the low byte, from the products with the scale's
+// rounded reciprocal, and how far one is from its code at most.  A product p = RN(v RN(1
+// / scale)) is within a relative 3 2^-24 of the quotient, |p| < 127.1, so both round to
+// the same code unless p lies within 2^-14 of a half-integer.  Adding 1.5 2^23 rounds p
+// to a whole number, half to even, whose low byte is the sum's.
+__device__ __forceinline__ uint32_t near_codes(float4 x, float rscale, float &off) {
+    const float magic = 12582912.0f;
+    const unsigned long long r2 = pk(rscale, rscale), up = pk(magic, magic);
+    const unsigned long long down = pk(-magic, -magic), minus = pk(-1.0f, -1.0f);
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const unsigned long long p = mul2(i ? pk(x.z, x.w) : pk(x.x, x.y), r2);
+        const unsigned long long k = add2(p, up);
+        float a, b;
+        upk(fma2(add2(k, down), minus, p), a, b);
+        off = fmaxf(off, fmaxf(fabsf(a), fabsf(b)));
+        upk(k, a, b);
+        w[i] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040);
+    }
+    return __byte_perm(w[0], w[1], 0x5410);
+}
+// The same by divisions.
+__device__ __noinline__ uint32_t exact_codes(float4 x, float scale) {
     const float v[4] = {x.x, x.y, x.z, x.w};
     uint32_t w = 0;
-#pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float c = scale >= 0x1p-100f
-                            ? static_code(v[i], scale, rscale)
-                            : fminf(127.0f, fmaxf(-127.0f, rintf(__fdiv_rn(v[i], scale))));
+        const float c = fminf(127.0f, fmaxf(-127.0f, rintf(__fdiv_rn(v[i], scale))));
         w |= (uint32_t)(__float2int_rn(c) & 0xff) << (8 * i);
     }
     return w;
@@ -49,18 +67,18 @@ __device__ __forceinline__ uint32_t codes4(float4 x, float scale, float rscale) 
 
 // A row of blocks per token.  A unit is 8 elements of a head: for the "half" pairs
 // elements 4u.. and rot/2 + 4u.., otherwise elements 8u...
-__global__ void __launch_bounds__(kAppendThreads) kv_append_i8_kernel(
+__global__ void __launch_bounds__(kAppendThreads, 6) kv_append_i8_kernel(
     const float *QKV, int64_t T, int Hq, int Hkv, int D, const float *__restrict__ rope,
     int64_t rope_positions, int rot, int interleaved, const int *__restrict__ q_start,
     const int *__restrict__ kv_len, int B, const int *__restrict__ block_table,
     int64_t max_pages, int8_t *__restrict__ k_cache, int8_t *__restrict__ v_cache,
-    float *__restrict__ k_scale, float *__restrict__ v_scale, int64_t num_pages, int page_size,
+    float *__restrict__ k_scale, float *__restrict__ v_scale, int64_t num_pages, int page_shift,
     float *Qout, int64_t ldq) {
     pdl_launch_dependents();
     pdl_wait();
     const int heads = Hq + 2 * Hkv;
-    const int upd = D / 8;  // units per head: 8 or 16, so that a head lies in one warp
-    const int units = heads * upd;
+    const int upd_log = D == 128 ? 4 : 3, upd = 1 << upd_log;  // units per head: in one warp
+    const int units = heads << upd_log;
     const int lane = threadIdx.x & 31;
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
         const int b = token_sequence(q_start, B, (int)t, lane);
@@ -68,8 +86,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_i8_kernel(
         const int64_t pos = (int64_t)__ldg(kv_len + b) - __ldg(q_start + b + 1) + t;
         const bool rotated = pos >= 0 && (rot == 0 || pos < rope_positions);
         int64_t page = -1;
-        if (rotated && pos / page_size < max_pages)
-            page = __ldg(block_table + b * max_pages + pos / page_size);
+        if (rotated && pos >> page_shift < max_pages)
+            page = __ldg(block_table + b * max_pages + (pos >> page_shift));
         const bool stored = page >= 0 && page < num_pages;
         const float *src = QKV + t * heads * D;
         // whole warps go round, so that a head's maximum can be shuffled
@@ -77,7 +95,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_i8_kernel(
              u0 += kAppendThreads * gridDim.y) {
             const int u = u0 + lane;
             const bool live = u < units;
-            const int head = live ? u / upd : 0, e = u % upd;
+            const int head = live ? u >> upd_log : 0, e = u & (upd - 1);
             const bool turn = head < Hq + Hkv && e < rot / 8;
             const bool split = turn && !interleaved;
             const int c0 = split ? 4 * e : 8 * e;              // the unit's first four elements
@@ -104,11 +122,17 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_i8_kernel(
                     turn_pair(a.w, d.w, r1.z, r1.w);
                 }
             }
-            float top = max_or_nan(
-                max_or_nan(max_or_nan(fabsf(a.x), fabsf(a.y)), max_or_nan(fabsf(a.z), fabsf(a.w))),
-                max_or_nan(max_or_nan(fabsf(d.x), fabsf(d.y)), max_or_nan(fabsf(d.z), fabsf(d.w))));
-            for (int o = upd / 2; o > 0; o >>= 1)
-                top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+            float top = 0.0f;
+            if (__any_sync(0xffffffffu, head >= Hq)) {
+                top = max_or_nan(max_or_nan(max_or_nan(fabsf(a.x), fabsf(a.y)),
+                                            max_or_nan(fabsf(a.z), fabsf(a.w))),
+                                 max_or_nan(max_or_nan(fabsf(d.x), fabsf(d.y)),
+                                            max_or_nan(fabsf(d.z), fabsf(d.w))));
+                top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                if (D == 128) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            }
             if (!live) continue;
             if (head < Hq) {
                 if (!rotated) a = d = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -118,15 +142,21 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_i8_kernel(
             } else if (stored) {
                 const int hk = head - Hq;
                 const bool key = hk < Hkv;
-                const int64_t row = (page * Hkv + (key ? hk : hk - Hkv)) * page_size +
-                                    pos % page_size;
+                const int64_t row = ((page * Hkv + (key ? hk : hk - Hkv)) << page_shift) +
+                                    (pos & ((1 << page_shift) - 1));
                 float scale = __fdiv_rn(top, 127.0f);
                 if (scale == 0.0f) scale = 1.0f;
                 uint32_t w0 = 0, w1 = 0;
                 if (top <= 3.402823466e38f) {
                     const float rscale = __frcp_rn(scale);
-                    w0 = codes4(a, scale, rscale);
-                    w1 = codes4(d, scale, rscale);
+                    float off = 0.0f;
+                    w0 = near_codes(a, rscale, off);
+                    w1 = near_codes(d, rscale, off);
+                    // (a reciprocal below 2^-100 may leave fp32's range)
+                    if (off > 0.49993896484375f || scale < 0x1p-100f) {  // 0.5 - 2^-14
+                        w0 = exact_codes(a, scale);
+                        w1 = exact_codes(d, scale);
+                    }
                 } else {
                     scale = __int_as_float(0x7fffffff);
                 }
@@ -155,11 +185,12 @@ sq_status launch_kv_append_i8(const float *QKV, int64_t T, int64_t Hq, int64_t H
     const int64_t units = (Hq + 2 * Hkv) * D / 8;
     const int64_t gy = T <= 2 * di.sms ? (units + kAppendThreads - 1) / kAppendThreads : 1;
     const int64_t grid = std::min<int64_t>(T, (int64_t)di.sms * 64);
+    int page_shift = 4;
+    while (1 << page_shift < page_size) ++page_shift;
     return launch_pdl(kv_append_i8_kernel, dim3((unsigned)grid, (unsigned)gy),
                       dim3(kAppendThreads), 0, st, 1, QKV, T, (int)Hq, (int)Hkv, (int)D, rope,
                       rope_positions, (int)rot, interleaved, q_start, kv_len, (int)B, block_table,
-                      max_pages, k_cache, v_cache, k_scale, v_scale, num_pages, (int)page_size, Q,
-                      ldq);
+                      max_pages, k_cache, v_cache, k_scale, v_scale, num_pages, page_shift, Q, ldq);
 }
 
 }  // namespace sq

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     walk.start(a, share);
     int npieces = 0, left = 0, key = 0, held = -1, entry = -1;
     int buf = 0;  // the ring's buffer that is filled next
-    int64_t head_row = 0;  // the piece's head, in cache rows of a page
+    int head_row = 0;  // the piece's head, in cache rows of a page
     int keys = 0;
     unsigned holes = 0;    // bit i: the page of the step in buffer i is missing
     const int *table = nullptr;
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 left = p.ntiles;
                 key = p.key0;
                 keys = p.keys;
-                head_row = (int64_t)p.head << a.page_shift;
+                head_row = p.head << a.page_shift;
                 table = a.block_table + (int64_t)p.seq * a.max_pages;
                 held = -1;
             }
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             const int r0 = lane / kLanes, ch = lane % kLanes;
             const uint32_t dst = ring + buf * C::kStepBytes;
             holes &= ~(3u << 2 * buf);
-            int64_t rows[2];
+            int rows[2];  // (a cache has 2^30 at most)
             bool there[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -130,11 +130,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 there[h] = e >= 0 && e < a.num_pages;
                 holes |= (there[h] ? 0u : 1u) << (2 * buf + h);
                 const int at = h && second != idx ? 0 : in_page + 16 * h;
-                rows[h] = there[h] ? (((int64_t)e * a.Hkv) << a.page_shift) + head_row + at : 0;
+                rows[h] = there[h] ? ((e * a.Hkv) << a.page_shift) + head_row + at : 0;
                 // lane: chunk lane % kLanes of row lane / kLanes of every kStride rows.  (Rows
                 // of no key are masked whatever they hold: codes are finite.)
-                const int8_t *ks = k_cache + rows[h] * D + lane * 16;
-                const int8_t *vs = v_cache + rows[h] * D + lane * 16;
+                const int64_t from = (int64_t)rows[h] * D + lane * 16;
+                const int8_t *ks = k_cache + from, *vs = v_cache + from;
 #pragma unroll
                 for (int j = 0; j < kCopies; ++j) {
                     const uint32_t d = dst + place<D>(16 * h + r0 + j * kStride, ch);
@@ -214,8 +214,25 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             F::fill(x[0], 0, qf[i]);
             F::fill(x[1], 2, qf[i]);
         }
-        // o[i][2 r + q]: row r's element NT (2 t + q) + i
-        float o[NT][2 * R], m[R], l[R];
+        // o[i][r]: row r's elements NT 2 t + i and NT (2 t + 1) + i
+        unsigned long long o[NT][R];
+        float m[R], l[R];
+        // four columns of row r from its element i of group q, and back
+        auto four = [&](int r, int q, int i) {
+            float x[4], y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) upk(o[i + k][r], x[k], y[k]);
+            return q ? make_float4(y[0], y[1], y[2], y[3]) : make_float4(x[0], x[1], x[2], x[3]);
+        };
+        auto set_four = [&](int r, int q, int i, float4 v) {
+            const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float x, y;
+                upk(o[i + k][r], x, y);
+                o[i + k][r] = q ? pk(x, w[k]) : pk(w[k], y);
+            }
+        };
         auto each_column = [&](auto &&f) {  // f(i of four columns, q, their first)
 #pragma unroll
             for (int q = 0; q < 2; ++q)
@@ -223,7 +240,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 for (int i = 0; i < NT; i += 4) f(i, q, NT * (2 * t + q) + i);
         };
 #pragma unroll
-        for (int i = 0; i < NT * 2 * R; ++i) o[i / (2 * R)][i % (2 * R)] = 0.0f;
+        for (int i = 0; i < NT * R; ++i) o[i / R][i % R] = 0;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             m[r] = -INFINITY;
@@ -234,11 +251,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 m[r] = f.x;
                 l[r] = t == 0 ? f.y : 0.0f;  // (the row's four threads' sums are added)
                 each_column([&](int i, int q, int d) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.prefix_o + row * D + d));
-                    o[i][2 * r + q] = v.x;
-                    o[i + 1][2 * r + q] = v.y;
-                    o[i + 2][2 * r + q] = v.z;
-                    o[i + 3][2 * r + q] = v.w;
+                    set_four(r, q, i,
+                             __ldcg(reinterpret_cast<const float4 *>(a.prefix_o + row * D + d)));
                 });
             }
         }
@@ -324,13 +338,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        o[i][2 * r] *= grow[r];
-                        o[i][2 * r + 1] *= grow[r];
-                    }
+                    for (int r = 0; r < R; ++r) o[i][r] = mul2(o[i][r], pk(grow[r], grow[r]));
             }
             uint32_t pf[2][S][4];  // of the step's two blocks of 16 keys
-            float down[R];
+            unsigned long long down2[R];
             {
                 float w[4][R][2];
 #pragma unroll
@@ -350,7 +361,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     // the row's largest weight into [2^14, 2^15)
                     const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100) - 14;
                     const float up = pow2(-e);
-                    down[r] = pow2(e);
+                    down2[r] = pk(pow2(e), pow2(e));
 #pragma unroll
                     for (int i = 0; i < 8; ++i) w[i >> 1][r][i & 1] *= up;
                 }
@@ -395,14 +406,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
                     for (int k = 0; k < S; ++k) mma16816<false>(c, pf[h][k], b0, b1);
                 }
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    if (R == 1) {
-                        o[i][q] = fmaf(c[q] + c[2 + q], down[0], o[i][q]);
-                    } else {
-                        o[i][q] = fmaf(c[q], down[0], o[i][q]);
-                        o[i][2 * R - 2 + q] = fmaf(c[2 + q], down[R - 1], o[i][2 * R - 2 + q]);
-                    }
+                if (R == 1) {
+                    o[i][0] = fma2(add2(pk(c[0], c[1]), pk(c[2], c[3])), down2[0], o[i][0]);
+                } else {
+                    o[i][0] = fma2(pk(c[0], c[1]), down2[0], o[i][0]);
+                    o[i][R - 1] = fma2(pk(c[2], c[3]), down2[R - 1], o[i][R - 1]);
                 }
             }
             __syncwarp();  // the step's buffer is free
@@ -426,8 +434,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 for (int r = 0; r < R; ++r) {
                     each_column([&](int i, int q, int d) {
                         __stcg(reinterpret_cast<float4 *>(a.part_o + (at + 8 * r) * D + d),
-                               make_float4(o[i][2 * r + q], o[i + 1][2 * r + q],
-                                           o[i + 2][2 * r + q], o[i + 3][2 * r + q]));
+                               four(r, q, i));
                     });
                     if (t == 0) __stcg(a.part_ml + at + 8 * r, make_float2(m[r], l[r]));
                 }
@@ -455,7 +462,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     m[r] = -INFINITY;
                     l[r] = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) o[i][2 * r] = o[i][2 * r + 1] = 0.0f;
+                    for (int i = 0; i < NT; ++i) o[i][r] = 0;
 #pragma unroll 2
                     for (int c = 0; c < join.n; ++c) {
                         const int64_t base = part_row(join.first + c * join.step) + 8 * r;
@@ -467,10 +474,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                         each_column([&](int i, int q, int d) {
                             const float4 v =
                                 __ldcg(reinterpret_cast<const float4 *>(a.part_o + base * D + d));
-                            const float u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                o[i + k][2 * r + q] = o[i + k][2 * r + q] * fo + u[k] * fp;
+                            const float4 w = four(r, q, i);
+                            set_four(r, q, i,
+                                     make_float4(w.x * fo + v.x * fp, w.y * fo + v.y * fp,
+                                                 w.z * fo + v.z * fp, w.w * fo + v.w * fp));
                         });
                     }
                 }
@@ -489,9 +496,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             const float f = row_factor(a, row, m[r], l[r], t == 0);
             float *dst = row_target(a) + row * D;
             each_column([&](int i, int q, int d) {
+                const float4 v = four(r, q, i);
                 *reinterpret_cast<float4 *>(dst + d) =
-                    make_float4(o[i][2 * r + q] * f, o[i + 1][2 * r + q] * f,
-                                o[i + 2][2 * r + q] * f, o[i + 3][2 * r + q] * f);
+                    make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
             });
         }
     }

@@ -219,6 +219,25 @@ __host__ __device__ __forceinline__ void pair_item_at(const PairSchedule &sc, in
 }
 
 
+// The same items for operands that do not fit L2 (a gated block's two projections):
+// tiles of `group` row blocks are numbered m-fastest, group after group, so that the
+// weights are read from DRAM once a group and its rows stay in L2 meanwhile.
+__host__ __device__ __forceinline__ void grouped_item_at(const PairSchedule &sc, int group, int i,
+                                                         int &m0, int &n0, int &bn) {
+    int t = i, part = 0;
+    bn = BN;
+    if (i >= sc.full_items) {
+        const int j = i - sc.full_items;
+        t = sc.full_items + j / sc.sub;
+        part = j % sc.sub;
+        bn = BN / sc.sub;
+    }
+    const int per = group * sc.n_tiles, g0 = t / per, r = t - g0 * per;
+    const int rows = sc.m_pairs - g0 * group < group ? sc.m_pairs - g0 * group : group;
+    n0 = r / rows * BN + part * bn;
+    m0 = (g0 * group + r % rows) * 2 * BM;
+}
+
 // Schedule of an M x N x K launch on `sms` SMs, and the grid it runs on.
 inline Schedule plan_launch(int64_t M, int64_t N, int64_t K, int sms, bool split_k, int *grid) {
     const int m_tiles = (int)((M + BM - 1) / BM), n_tiles = (int)((N + BN - 1) / BN);
