@@ -440,9 +440,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t kb = ring + (ks % NS) * C::kSlot;
                 const uint32_t d = tmem + (t_s & 1) * C::kArea + C::kS0;
                 // the smallest part first: what the accumulator truncates is relative
-                // to the sum so far
+                // to the sum so far.  (8 bits: a loop over the parts, here and below, for the
+                // code's length: prompts 606 us, unrolled 629; 16 bits, whose code is
+                // shorter: 537 us instead of 529)
                 const uint32_t qd = desc_low(qbase, 16), kd = desc_low(kb, 16);
-#pragma unroll
+#pragma unroll (CT == kI8 ? 1 : NP)
                 for (int part = NP - 1; part >= 0; --part)
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
@@ -473,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t pa = tmem + (t_pv & 1) * C::kArea;
                 const uint32_t v = ring + (vs % NS) * C::kSlot;
                 const uint32_t vd = desc_low(v, C::kSlab);
-#pragma unroll
+#pragma unroll (CT == kI8 ? 1 : NP)
                 for (int part = NP - 1; part >= 0; --part)
 #pragma unroll
                     for (int i = 0; i < kKT / 16; ++i)
@@ -644,13 +646,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // the end, for those that widen; and every copy lands before the CTA's
                     // shared memory goes away
                     const uint32_t sl = seq % kRawSlots;
-                    if (ok && (seq < kRawSlots ||
-                               warp_wait(&X.raw_empty[sl], (seq / kRawSlots - 1) & 1u, abort,
-                                         a.error))) {
-                        if (lane == 0) {
-                            X.raw_stop[sl] = 1;
-                            bar_arrive(&X.raw_full[sl]);
-                        }
+                    ok = ok && (seq < kRawSlots ||
+                                warp_wait(&X.raw_empty[sl], (seq / kRawSlots - 1) & 1u, abort,
+                                          a.error));
+                    if (ok && lane == 0) {
+                        X.raw_stop[sl] = 1;
+                        bar_arrive(&X.raw_full[sl]);
                     }
                     for (uint32_t d = seq < kRawSlots ? 0 : seq - kRawSlots; d < seq; ++d)
                         if (d + kRawSlots > seq || !ok)
@@ -987,7 +988,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // took 897 us instead of 772.  The logits go back to tensor memory with
                     // their scales applied and masked (702 us): a scale that every lane reads
                     // from shared memory is a cycle of its pipe, which the products and the
-                    // widening want too.  A chunk's weights take its place.
+                    // widening want too.  A chunk's weights take its place.  A wild tile's
+                    // weights have a loop of their own, out of the other's way (688 -> 628 us).
                     const int sc = t % kScaleTiles;
                     if (!warp_wait(&X.scale_full[sc], (t / kScaleTiles) & 1u, abort, a.error)) {
                         ok = false;
@@ -1028,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st_wait();
                     // the row's maximum, with the other half's
                     B.half_max[t & 1][g][r] = mx;
-                    if (wild) {
+                    if (__builtin_expect(wild, 0)) {
                         float top = -INFINITY;
 #pragma unroll 1
                         for (int q = 0; q < 64; q += 16) {
@@ -1055,13 +1057,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     unsigned long long sum2 = 0;
                     // of a wild tile's row: its largest weight is near 2^kBias
                     int shift = 0;
-                    if (wild) {
+                    if (__builtin_expect(wild, 0)) {
                         const float top =
                             fmaxf(X.half_top[t & 1][0][r], X.half_top[t & 1][1][r]);
                         shift = (int)fminf(fmaxf(kBias - ceilf(top - m), -126.0f), 126.0f);
                     }
-#pragma unroll 1
-                    for (int q = 0; q < 64; q += 16) {
+                    // 16 logits to their weights; `to_weights` multiplies the values' scales in
+                    auto weigh = [&](int q, auto to_weights) {
                         uint32_t v[16], parts[2][8];
                         const uint32_t chunk = area + C::kS0 + 64 * g + q;
                         tmem_ld16(chunk, v);
@@ -1075,22 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             x[i + 1] = ex2(x[i + 1]);
                             sum2 = add2(sum2, pk(x[i], x[i + 1]));
                         }
-                        if (wild) {
-                            // (a masked key's scale need not be finite; the shift in two
-                            // steps, none of which leaves fp32's range)
-                            const float s1 = pow2(shift / 2), s2 = pow2(shift - shift / 2);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                x[i] = v[i] == 0xff800000u ? 0.0f : x[i] * s1 * vscale[q + i] * s2;
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; i += 4) {
-                                const float4 vs = *reinterpret_cast<const float4 *>(vscale + q + i);
-                                upk(mul2(pk(x[i], x[i + 1]), pk(vs.x, vs.y)), x[i], x[i + 1]);
-                                upk(mul2(pk(x[i + 2], x[i + 3]), pk(vs.z, vs.w)), x[i + 2],
-                                    x[i + 3]);
-                            }
-                        }
+                        to_weights(q, v, x);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             uint32_t z[2];
@@ -1100,6 +1087,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tmem_st8(chunk, parts[0]);
                         tmem_st8(chunk + 8, parts[1]);
+                    };
+                    if (!__builtin_expect(wild, 0)) {
+#pragma unroll 1
+                        for (int q = 0; q < 64; q += 16)
+                            weigh(q, [&](int q, const uint32_t (&)[16], float (&x)[16]) {
+#pragma unroll
+                                for (int i = 0; i < 16; i += 4) {
+                                    const float4 vs =
+                                        *reinterpret_cast<const float4 *>(vscale + q + i);
+                                    upk(mul2(pk(x[i], x[i + 1]), pk(vs.x, vs.y)), x[i], x[i + 1]);
+                                    upk(mul2(pk(x[i + 2], x[i + 3]), pk(vs.z, vs.w)), x[i + 2],
+                                        x[i + 3]);
+                                }
+                            });
+                    } else {
+                        // (a masked key's scale need not be finite; the shift in two
+                        // steps, none of which leaves fp32's range)
+                        const float s1 = pow2(shift / 2), s2 = pow2(shift - shift / 2);
+#pragma unroll 1
+                        for (int q = 0; q < 64; q += 16)
+                            weigh(q, [&](int q, const uint32_t (&v)[16], float (&x)[16]) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    x[i] =
+                                        v[i] == 0xff800000u ? 0.0f : x[i] * s1 * vscale[q + i] * s2;
+                            });
                     }
                     float sa, sb;
                     upk(sum2, sa, sb);
