@@ -1028,25 +1028,56 @@ __device__ __forceinline__ int exact_pass_kb(const EpiArgs &args, int nkb, int w
 }
 
 // The same for the gated kernels, whose weights have many rows (24,576 norms took 6 us
-// of a decoding step's 45): the other operand's norms alone decide if they can.
+// of a decoding step's 45): the other operand's norms alone decide if they can.  Where
+// both operands have rows beyond the bound, `bad` (of the pair kernel) holds a bit for
+// each block of 256 rows with such a row: a tile is in danger only if its rows and its
+// columns both are.  (Of Gaussian rows of 4096 one in a thousand is beyond the bound;
+// 8192 x 4096 x 12288: 7 and 33 rows, 6 % of the tiles.)
+constexpr int kBadWords = 32;
 __device__ __forceinline__ int exact_pass_kb_gated(const EpiArgs &args, int nkb, int warp,
-                                                   int lane, int32_t (*l1max)[2]) {
+                                                   int lane, int32_t (*l1max)[2],
+                                                   uint32_t (*bad)[kBadWords]) {
     if (warp == 0 || nkb <= KB_PER_CHUNK) return KB_PER_CHUNK;
+    constexpr int kScan = THREADS - 32;
     const int tid = threadIdx.x - 32;
 #pragma unroll 1
     for (int side = 0; side < 2; ++side) {
         const int32_t *l1 = side ? args.w_l1 : args.x_l1;
+        if (bad) {
+            if (tid < kBadWords) bad[side][tid] = l1 ? 0u : ~0u;
+            asm volatile("bar.sync 1, %0;" ::"n"(kScan) : "memory");
+        }
         if (!l1) continue;
         const int rows = side ? args.N : args.M;
         int32_t most = 0;
-        for (int i = tid; i < rows; i += THREADS - 32) most = max(most, __ldg(l1 + i));
+        for (int i0 = tid; i0 < rows; i0 += 4 * kScan) {
+            int32_t v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = i0 + j * kScan < rows ? __ldg(l1 + i0 + j * kScan) : 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                most = max(most, v[j]);
+                const int block = (i0 + j * kScan) >> 8;
+                if (bad && v[j] > kSinglePassL1 && block < 32 * kBadWords)
+                    atomicOr(&bad[side][block >> 5], 1u << (block & 31));
+            }
+        }
         most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 0) l1max[warp - 1][side] = most;
-        asm volatile("bar.sync 1, %0;" ::"n"(THREADS - 32) : "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(kScan) : "memory");
         for (int w = 0; w < 9; ++w) most = max(most, l1max[w][side]);
         if (most <= kSinglePassL1) return nkb;
     }
     return KB_PER_CHUNK;
+}
+// Whether the tile at (m0, n0), multiples of 256 and (a half's) of 128, may hold a sum
+// that leaves fp32's whole numbers.
+__device__ __forceinline__ bool tile_in_danger(const uint32_t (*bad)[kBadWords], int m0, int n0) {
+    auto is_bad = [&](int side, int block) {
+        return block >= 32 * kBadWords || (bad[side][block >> 5] >> (block & 31) & 1u);
+    };
+    return is_bad(0, m0 >> 8) && is_bad(1, n0 >> 8);
 }
 
 template <int MODE, int OUT>
@@ -1096,7 +1127,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     // K per exact fp32 pass: 1024, or all of K when the row L1 norms of either
     // operand bound every partial sum below 2^24.  Decided by warps 1..9 (the
     // MMA issuer and the epilogue); the producer does not need it.
-    const int chunk_kb = OUT == kOutGated ? exact_pass_kb_gated(args, nkb, warp, lane, S.l1max)
+    const int chunk_kb = OUT == kOutGated
+                             ? exact_pass_kb_gated(args, nkb, warp, lane, S.l1max, nullptr)
                                           : exact_pass_kb(args, nkb, warp, lane, S.l1max);
     const int nchunks = (nkb + chunk_kb - 1) / chunk_kb;
 
@@ -1331,6 +1363,7 @@ struct PairSmem {
     uint32_t tmem_base;
     int abort_flag;
     int32_t l1max[9][2];
+    uint32_t bad[2][kBadWords];  // see exact_pass_kb_gated
 };
 static_assert(sizeof(PairSmem) <= BAR_BYTES, "barrier block");
 
@@ -1389,9 +1422,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         else pair_item_at(sched, i, m0, n0, bn);
     };
     const int nkb = (K + BK - 1) / BK;
-    const int chunk_kb = OUT == kOutGated ? exact_pass_kb_gated(args, nkb, warp, lane, S.l1max)
-                                          : exact_pass_kb(args, nkb, warp, lane, S.l1max);
+    const int chunk_kb = OUT == kOutGated
+                             ? exact_pass_kb_gated(args, nkb, warp, lane, S.l1max, S.bad)
+                             : exact_pass_kb(args, nkb, warp, lane, S.l1max);
     const int nchunks = (nkb + chunk_kb - 1) / chunk_kb;
+    // passes of an item: of a gated launch, one wherever its own rows allow it
+    auto passes = [&](int m0, int n0) {
+        return OUT == kOutGated && nchunks > 1 && !tile_in_danger(S.bad, m0, n0) ? 1 : nchunks;
+    };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -1439,20 +1477,31 @@ __global__ void __launch_bounds__(THREADS, 1)
             // ------------------------------------------------ MMA issuer (leader)
             int stage = 0;
             uint32_t phase = 0, tph = 0;
-            int it = 0;
-            for (int i = cluster_id; i < num_items; i += num_clusters, ++it) {
+            uint32_t next = 0;  // the accumulator of the next item of one pass
+            for (int i = cluster_id; i < num_items; i += num_clusters) {
                 int pm0, n0, bn;
                 item_at(i, pm0, n0, bn);
                 const uint32_t idesc = idesc_pair(bn);
-                for (int c = 0; c < nchunks; ++c) {
-                    const uint32_t b = nchunks == 1 ? (uint32_t)(it & 1) : 0u;
+                const int chunks = passes(pm0, n0);
+                const uint32_t b = chunks == 1 ? next : 0u;
+                next = chunks == 1 ? next ^ 1u : 0u;
+                for (int c = 0; c < chunks; ++c) {
                     const uint32_t par = (tph >> b) & 1u;
                     if (!mbar_wait(smem_u32(&S.tempty[b]), par ^ 1, abort_flag)) goto done_m;
                     tph ^= 1u << b;
+                    if (OUT == kOutGated && c == 1) {
+                        // the partial sums stand in the second accumulator, which an item of
+                        // one pass may want next: its use here is counted like any other
+                        // (the item before is done with it, or this one's first chunk would
+                        // not have been taken out)
+                        if (!mbar_wait(smem_u32(&S.tempty[1]), (tph >> 1 & 1u) ^ 1, abort_flag))
+                            goto done_m;
+                        tph ^= 2u;
+                    }
                     tc_fence_after();
                     const uint32_t d = tmem_base + b * BN;
                     const int kb0 = c * chunk_kb;
-                    const int kb1 = min(nkb, kb0 + chunk_kb);
+                    const int kb1 = chunks == 1 ? nkb : min(nkb, kb0 + chunk_kb);
                     for (int kb = kb0; kb < kb1; ++kb) {
                         if (!mbar_wait(smem_u32(&S.full[stage]), phase, abort_flag)) goto done_m;
                         tc_fence_after();
@@ -1490,10 +1539,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t colP = BN;
         const uint32_t tempty_leader0 = map_to_rank(smem_u32(&S.tempty[0]), 0);
         const uint32_t tempty_leader1 = map_to_rank(smem_u32(&S.tempty[1]), 0);
-        int it = 0;
-        for (int i = cluster_id; i < num_items; i += num_clusters, ++it) {
+        uint32_t next = 0;  // as the issuer's
+        for (int i = cluster_id; i < num_items; i += num_clusters) {
             int pm0, n0, bn;
             item_at(i, pm0, n0, bn);
+            const int chunks = passes(pm0, n0);
             const int m0 = pm0 + (int)rank * BM;
             const int row0 = m0 + q * 32;
             const int64_t m = (int64_t)row0 + lane;
@@ -1513,8 +1563,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 prefetch_residual(args, m, nb, nsl);
                 load_residual<OUT != kOutRequant>(rnext, args, m, nb);
             }
-            if (nchunks == 1) {
-                const uint32_t b = (uint32_t)(it & 1);
+            if (chunks == 1) {
+                const uint32_t b = next;
+                next ^= 1u;
                 if (!mbar_wait(smem_u32(&S.tfull[b]), (fph >> b) & 1u, abort_flag)) goto done_e;
                 fph ^= 1u << b;
                 tc_fence_after();
@@ -1530,7 +1581,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // the item's width: the quarter's other warp may still be reading
                 // its partial of the previous item when this one starts the next
                 const uint32_t tP = tmem_base + lane_off + colP + half * COLS_PER_WARP;
-                for (int c = 0; c < nchunks; ++c) {
+                next = 0;
+                for (int c = 0; c < chunks; ++c) {
                     if (!mbar_wait(smem_u32(&S.tfull[0]), fph & 1u, abort_flag)) goto done_e;
                     fph ^= 1u;
                     tc_fence_after();
@@ -1556,6 +1608,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 epilogue_tile<MODE, true, OUT>(tP, m, nb, row0, lane, args, xs, cp, rnext, &tmY,
                                                  stg, nsl);
+                if (OUT == kOutGated) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(tempty_leader1);
+                }
             }
         }
     done_e:

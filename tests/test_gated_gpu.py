@@ -157,6 +157,34 @@ def test_many_tiles(sq):
     c.verify(sq, 2, c.run(sq, 2))
 
 
+@pytest.mark.parametrize("rows,columns", [
+    ([3], [5]), ([0, 257, 1299], [0, 4999]), (range(0, 1300, 256), range(0, 5000, 400)),
+    (range(0, 1300, 512), range(0, 5000, 128)), (range(1300), [17, 2500]), ([], [1, 2]),
+    ([700], []), ([300, 301, 1200], range(5000))])
+def test_sums_beyond_2_to_the_24(sq, rows, columns):
+    """A launch whose tiles are summed in one pass where their rows' norms allow it and
+    in chunks where they do not: codes of 127 against each other leave fp32's whole
+    numbers at K = 2064, so a tile that was summed the wrong way would differ from the
+    launch without norms, whose tiles are all chunks."""
+    M, F, K = 1300, 5000, 2064
+    c = Case(M, F, K, seed=3, bias=(False, True))
+    c.wg, c.wu, c.s = c.wg.clamp(-2 / K ** 0.5, 2 / K ** 0.5), c.wu * 0.1, torch.ones(K)
+    c.wu[:, 0] = 3.0  # (a row's largest: the others' codes stay small)
+    big = 127.0 - (torch.arange(K) % 97 == 0).float()
+    c.x = (c.x * 0.5).round()
+    c.x[list(rows)] = big
+    for w in (c.wg, c.wu):
+        w[list(columns)] = torch.flip(big, (0,)) / 127
+    c.packed(sq)
+    first = c.run(sq, 0)
+    assert torch.equal(c.run(sq, 0, l1=False), first)
+    limit = 132104  # 127 * limit < 2^24
+    assert (c.x.abs().sum(1) > limit).sum() == len(rows)
+    if len(columns):
+        assert int((c.l1 > limit).sum()) == 2 * len(columns)
+    c.verify(sq, 0, first)
+
+
 def test_rows_are_not_written_beyond_the_output(sq):
     c = Case(130, 101, 64, seed=2).packed(sq)
     whole = torch.full((132 * 101,), 5.0, device="cuda")
