@@ -328,7 +328,7 @@ sq_status sq_kv_append_i8(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv, 
  * Everything said there holds, with these differences.  Codes enter the tensor cores as
  * they are (as fp16 numbers, exactly), fp32 queries and the products of probabilities
  * and value scales as two fp16 numbers each, a row's largest scaled near the top of
- * fp16's range: within 2^-22, or 2^-32 of the row's largest (or 2^-130), and so O agrees
+ * fp16's range: within 2^-22, or 2^-30 of the row's largest (or 2^-130), and so O agrees
  * with the exact attention over the rows as sq_paged_attention's does for an fp16 cache,
  * whatever the scales' range within a row's keys is (weights below 2^-100 of the largest
  * may count as 0).  Key scales are 2^96 at most, larger ones may leave the rows that see

@@ -149,7 +149,10 @@ constexpr int kJoin = 6;
 // (300 keys, 1 item), 35, 31, 36 and 42 (1024 keys, 19 items), 71, 57, 58 and 62
 // (30,000 keys, 1 item)
 constexpr int kMinTiles = 4;
-constexpr float kBias = 12.0f;  // log2 of the probabilities' factor
+// log2 of the probabilities' factor.  (8 bits: a row's largest weight, its probability
+// times a value scale in [2^-8, 2), stays below 2^15 and is 2^6 at least, so that what is
+// below fp16's range, 2^-24 in both parts, is 2^-30 of it)
+constexpr float kBias16 = 12.0f, kBiasI8 = 14.0f;
 
 constexpr int kI8 = kCacheI8;
 
@@ -171,6 +174,7 @@ template <int D, int CT>
 struct TilesCfg {
     static constexpr bool BF = CT == SQ_CACHE_BF16;
     static constexpr int kParts = BF ? 3 : 2;
+    static constexpr float kBias = CT == kI8 ? kBiasI8 : kBias16;
     static constexpr int kSlab = kKT * 128;            // 128 rows x 64 elements
     static constexpr int kSlot = kSlab * (D / 64);     // keys or values of a tile
     static constexpr int kSlots = CT == kI8 ? (D == 64 ? 5 : 3) : D == 64 ? 6 : BF ? 3 : 4;
@@ -315,6 +319,17 @@ __device__ __forceinline__ void hide(uint32_t (&v)[N], unsigned seen) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
         if (!(seen >> i & 1)) v[i] = 0xff800000u;
+}
+// split16 for two fp16 numbers, the first by cutting off what it cannot hold: as near
+// (2^-22; the rest has 13 bits), with one conversion less (prompts 595 -> 582 us).
+__device__ __forceinline__ void split_cut(float a, float b, uint32_t (&w)[2]) {
+    const float x = __uint_as_float(__float_as_uint(a) & 0xffffe000u);
+    const float y = __uint_as_float(__float_as_uint(b) & 0xffffe000u);
+    const __half2 high = __floats2half2_rn(x, y);
+    w[0] = *reinterpret_cast<const uint32_t *>(&high);
+    upk(sub2(pk(a, b), pk(x, y)), a, b);
+    const __half2 low = __floats2half2_rn(a, b);
+    w[1] = *reinterpret_cast<const uint32_t *>(&low);
 }
 __device__ __forceinline__ float lg2(float x) {
     float y;
@@ -679,18 +694,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (X.raw_stop[rw]) break;
                 if (d >= NS && !warp_wait(&B.empty[sl], (d / NS - 1) & 1u, abort, a.error)) break;
                 const uint32_t from = from0 + rw * C::kRaw, to = to0 + sl * C::kSlot;
+                // (two rows at a time: four 605 us instead of 597 for prompts, one 614)
 #pragma unroll 1
-                for (int j0 = 0; j0 < kKT / kRowStep; j0 += 4) {
-                    uint32_t w[4 * kHalves][2];
+                for (int j0 = 0; j0 < kKT / kRowStep; j0 += 2) {
+                    uint32_t w[2 * kHalves][2];
 #pragma unroll
-                    for (int j = 0; j < 4 * kHalves; ++j)
+                    for (int j = 0; j < 2 * kHalves; ++j)
                         asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
                                      : "=r"(w[j][0]), "=r"(w[j][1])
                                      : "r"(from + (j0 + j / kHalves) * kRowStep * D +
                                            64 * (j % kHalves ^ h0))
                                      : "memory");
 #pragma unroll
-                    for (int j = 0; j < 4 * kHalves; ++j) {
+                    for (int j = 0; j < 2 * kHalves; ++j) {
                         const uint32_t x = w[j][0] ^ kCodeBias, y = w[j][1] ^ kCodeBias;
                         sts4(to + (j0 + j / kHalves) * kRowStep * 128 +
                                  (j % kHalves ^ h0) * C::kSlab,
@@ -1052,15 +1068,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     mx = fmaxf(mx, B.half_max[t & 1][1 - g][r]);
                     // (see below)
-                    const float m = mx == -INFINITY ? 0.0f : __fmaf_ru(mx, c, -kBias);
+                    const float m = mx == -INFINITY ? 0.0f : __fmaf_ru(mx, c, -C::kBias);
                     const unsigned long long c2 = pk(c, c), m2 = pk(-m, -m);
                     unsigned long long sum2 = 0;
-                    // of a wild tile's row: its largest weight is near 2^kBias
+                    // of a wild tile's row: its largest weight is near the probabilities' factor
                     int shift = 0;
                     if (__builtin_expect(wild, 0)) {
                         const float top =
                             fmaxf(X.half_top[t & 1][0][r], X.half_top[t & 1][1][r]);
-                        shift = (int)fminf(fmaxf(kBias - ceilf(top - m), -126.0f), 126.0f);
+                        shift = (int)fminf(fmaxf(C::kBias - ceilf(top - m), -126.0f), 126.0f);
                     }
                     // 16 logits to their weights; `to_weights` multiplies the values' scales in
                     auto weigh = [&](int q, auto to_weights) {
@@ -1081,7 +1097,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             uint32_t z[2];
-                            split16<false, 2>(x[2 * i], x[2 * i + 1], z);
+                            split_cut(x[2 * i], x[2 * i + 1], z);
                             parts[0][i] = z[0];
                             parts[1][i] = z[1];
                         }
@@ -1163,7 +1179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mx = fmaxf(mx, B.half_max[t & 1][1 - g][r]);
                     // (rounded up: mx c is exact, so the largest exponent is 12 at most, and
                     // at least 0 where 12 is less than the maximum's last place)
-                    const float m = mx == -INFINITY ? 0.0f : __fmaf_ru(mx, c, -kBias);
+                    const float m = mx == -INFINITY ? 0.0f : __fmaf_ru(mx, c, -C::kBias);
                     const unsigned long long c2 = pk(c, c), m2 = pk(-m, -m);
                     unsigned long long sum2 = 0;
                     // per 16 keys 8 columns of each part
