@@ -435,13 +435,14 @@ def _rows_of(t: torch.Tensor, cols: int, name: str, dev, rows: Optional[int] = N
     columns of a wider matrix); returns the row stride."""
     if t.dtype is not torch.float32 or t.device != dev:
         raise ValueError(f"{name} must be {torch.float32} on {dev}, is {t.dtype} on {t.device}")
-    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows):
         raise ValueError(f"{name} must have shape ({'T' if rows is None else rows}, {cols}), "
-                         f"got {tuple(t.shape)}")
+                         f"got {tuple(shape)}")
     apart, step = t.stride()
-    if t.shape[0] <= 1:  # a single row's stride says nothing
+    if shape[0] <= 1:  # a single row's stride says nothing
         apart = cols
-    if (t.numel() and step != 1) or apart < cols:
+    if (step != 1 and t.numel()) or apart < cols:
         raise ValueError(f"{name}'s columns must be contiguous and its rows apart")
     return apart
 
@@ -454,25 +455,37 @@ def _need_paged(k_cache, v_cache, block_table, q_start, kv_len, k_scale, v_scale
         raise ValueError(f"k_cache must be bfloat16, float16 or int8, got {k_cache.dtype}")
     if (k_scale is None) != (ctype != _CACHE_I8) or (v_scale is None) != (ctype != _CACHE_I8):
         raise ValueError("k_scale and v_scale go with an int8 cache, and it with both")
-    if k_cache.dim() != 4:
+    dev, i32, shape, tables = k_cache.device, torch.int32, k_cache.shape, block_table.shape
+    if len(shape) != 4:
         raise ValueError("k_cache must have shape (num_pages, kv_heads, page_size, D)")
     if kv_len.dim() != 1:
         raise ValueError("kv_len must have one dimension")
     B = kv_len.shape[0]
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    if len(tables) != 2 or tables[0] != B:
         raise ValueError(f"block_table must have shape ({B}, max_pages)")
-    _need(k_cache, k_cache.dtype, "k_cache")
-    dev, i32, shape = k_cache.device, torch.int32, k_cache.shape
+    on = k_cache.get_device()
+    if not (on >= 0 and k_cache.is_contiguous() and v_cache.dtype is k_cache.dtype
+            and v_cache.get_device() == on and v_cache.shape == shape and v_cache.is_contiguous()
+            and block_table.dtype is i32 and block_table.get_device() == on
+            and block_table.is_contiguous() and q_start.dtype is i32
+            and q_start.get_device() == on and q_start.shape == (B + 1,)
+            and q_start.is_contiguous() and kv_len.dtype is i32 and kv_len.get_device() == on
+            and kv_len.is_contiguous()):  # (in one line of a good call: as _arg has it)
+        _need(k_cache, k_cache.dtype, "k_cache")
+        for t, dtype, name, want in ((v_cache, k_cache.dtype, "v_cache", shape),
+                                     (block_table, i32, "block_table", tables),
+                                     (q_start, i32, "q_start", (B + 1,)),
+                                     (kv_len, i32, "kv_len", (B,))):
+            _arg(t, dtype, name, want, dev)
     pages, Hkv, page_size, D = shape
-    width = block_table.shape[1]
     scales = ()
     if k_scale is not None:
-        scales = tuple(_arg(t, torch.float32, n, shape[:3], dev)
-                       for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")))
-    return (ctype, pages, Hkv, page_size, D, B, width), scales, (
-        k_cache.data_ptr(), _arg(v_cache, k_cache.dtype, "v_cache", shape, dev),
-        _arg(block_table, i32, "block_table", (B, width), dev),
-        _arg(q_start, i32, "q_start", (B + 1,), dev), _arg(kv_len, i32, "kv_len", (B,), dev))
+        f32, rows = torch.float32, (pages, Hkv, page_size)
+        scales = (_arg(k_scale, f32, "k_scale", rows, dev),
+                  _arg(v_scale, f32, "v_scale", rows, dev))
+    return (ctype, pages, Hkv, page_size, D, B, tables[1]), scales, (
+        k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), q_start.data_ptr(),
+        kv_len.data_ptr())
 
 
 def kv_append(QKV: torch.Tensor, Hq: int, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -498,10 +511,11 @@ def kv_append(QKV: torch.Tensor, Hq: int, k_cache: torch.Tensor, v_cache: torch.
     rot = positions = 0
     rope_at = None
     if rope is not None:
-        if rope.dim() != 3 or rope.shape[2] != 2:
+        angles = rope.shape
+        if len(angles) != 3 or angles[2] != 2:
             raise ValueError("rope must have shape (positions, n, 2)")
-        rope_at = _arg(rope, f32, "rope", rope.shape, dev)
-        positions, rot = rope.shape[0], 2 * rope.shape[1]
+        rope_at = _arg(rope, f32, "rope", angles, dev)
+        positions, rot = angles[0], 2 * angles[1]
     with _on(QKV, stream) as st:
         if q_out is None:
             q_out = torch.zeros(T, Hq * D, dtype=f32, device=dev)
@@ -544,9 +558,10 @@ def paged_attention(Q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     (ctype, pages, Hkv, page_size, D, B, width), scales, (k, v, table, starts, lens) = _need_paged(
         k_cache, v_cache, block_table, q_start, kv_len, k_scale, v_scale)
     dev = k_cache.device
-    if Q.dim() != 2 or Q.shape[1] % D != 0 or Q.shape[1] == 0:
-        raise ValueError(f"Q must have shape (T, heads * {D}), got {tuple(Q.shape)}")
-    T, Hq = Q.shape[0], Q.shape[1] // D
+    rows = Q.shape
+    if len(rows) != 2 or rows[1] % D != 0 or rows[1] == 0:
+        raise ValueError(f"Q must have shape (T, heads * {D}), got {tuple(rows)}")
+    T, Hq = rows[0], rows[1] // D
     ldq = _rows_of(Q, Hq * D, "Q", dev)
     pages_at = None
     if prefix_pages is not None:
