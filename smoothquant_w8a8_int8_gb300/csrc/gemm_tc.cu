@@ -1129,7 +1129,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // MMA issuer and the epilogue); the producer does not need it.
     const int chunk_kb = OUT == kOutGated
                              ? exact_pass_kb_gated(args, nkb, warp, lane, S.l1max, nullptr)
-                                          : exact_pass_kb(args, nkb, warp, lane, S.l1max);
+                             : exact_pass_kb(args, nkb, warp, lane, S.l1max);
     const int nchunks = (nkb + chunk_kb - 1) / chunk_kb;
 
     if (warp == 0) {
@@ -1146,7 +1146,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int kb = t.kb0; kb < t.kb1; ++kb) {
                     if (!mbar_wait(smem_u32(&S.empty[stage]), phase ^ 1, abort_flag)) goto done_p;
                     const uint32_t full = smem_u32(&S.full[stage]);
-                    mbar_expect_tx(full, A_BYTES + t.bn * BK * 2);
+                    const int a_rows = OUT == kOutGated ? args.gt.a_rows : BM;
+                    mbar_expect_tx(full, (a_rows + t.bn) * BK * 2);
                     const uint32_t sa = ring + stage * STAGE_BYTES;
                     tma_load_2d(sa, &tmA, full, kb * BK, t.m0);
                     tma_load_2d(sa + A_BYTES, slice ? &tmBs : &tmB, full, kb * BK, t.n0);
@@ -1771,11 +1772,14 @@ sq_status launch_pair_mode(const CUtensorMap &ta, const CUtensorMap &tbp, const 
     return launch_pair_kernel<MODE, kOutPlain>(ta, tbp, tbq, ty, args, K, device, st);
 }
 
-// Row blocks of a gated launch that share a pass over the weights: 8 where these take
-// more than half of L2 (129 MB), else all of the weights stay there.  Measured (8192 x
-// 4096 x 12288, 201 MB): 1, 4, 8, 16 row blocks
-// 1279, 1172, 1168, 1168 us.
-int gated_group(int64_t weight_bytes) { return weight_bytes > (64ll << 20) ? 8 : 1; }
+// Row blocks of a gated launch that share a pass over the weights: where these take more
+// than half of L2 (129 MB), as many as hold 32 MB of activations; else the weights stay
+// there.  Measured (8192 x 4096 x 12288, 201 MB of weights): 1, 4, 8, 16 row blocks 1097,
+// 993, 940, 925 us.
+int gated_group(int64_t weight_bytes, int64_t K) {
+    if (weight_bytes <= (64ll << 20)) return 1;
+    return (int)std::max<int64_t>(1, (32ll << 20) / (2 * BM * 2 * K));
+}
 
 // Which kernel runs a launch: CTA pairs for every launch of at least one full
 // 256-row pair tile that is not split over K.
@@ -1847,11 +1851,16 @@ sq_status launch_gemm_tc(const __nv_bfloat16 *Xop, const float *sx, const int32_
                   (!rq->Yop || aligned16(rq->Yop));
     args.rq_fast = rq && rq->scale >= 0x1p-70f;
     args.gt = gated ? *gated : GatedOut{};
-    if (gated) args.gt.group = gated_group(N * K * 2);
+    // A gated launch of a few rows copies those alone: the rest of a stage's 128 rows is
+    // whatever it was, and so are the sums of rows that Y has not.  (1 x 4096 x 12288: 39.5
+    // us, with boxes of 128 rows 60; 16 and more rows take the same either way.)
+    const int a_rows = gated && M < BM ? (int)M : BM;
+    args.gt.group = gated ? gated_group(N * K * 2, K) : 1;
+    args.gt.a_rows = a_rows;
     args.rm_pairs = reinterpret_cast<const float4 *>(rm_pairs);
     args.row_amax = row_amax;
     CUtensorMap ta, tb, tbs, ty;
-    if ((rc = make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Xop, M, K, BM, BK)) != SQ_OK)
+    if ((rc = make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Xop, M, K, a_rows, BK)) != SQ_OK)
         return rc;
     if ((rc = make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Wop, N, K, BN, BK)) != SQ_OK)
         return rc;

@@ -114,7 +114,7 @@ def test_packing_rows_of_zeros(sq):
 
 SHAPES = [(1, 1, 16), (1, 96, 64), (2, 33, 1040), (16, 1000, 512), (127, 31, 80), (128, 32, 2080),
           (129, 257, 48), (255, 130, 4112), (256, 128, 64), (257, 515, 1040), (300, 64, 2080),
-          (700, 1028, 144), (1030, 40, 32)]
+          (700, 1028, 144), (1030, 40, 32), (7, 300, 2080), (15, 64, 144), (65, 96, 64)]
 
 
 @pytest.mark.parametrize("act", [0, 1, 2])
@@ -136,7 +136,7 @@ def test_range(sq, size, act):
 
 
 @pytest.mark.parametrize("M,F,K", [(1, 64, 2048), (16, 500, 4096), (128, 1000, 2560),
-                                   (130, 33, 8192), (300, 128, 3584)])
+                                   (130, 33, 8192), (300, 128, 3584), (1, 4000, 4096)])
 def test_split_k_is_the_same_bits(sq, M, F, K):
     c = Case(M, F, K, seed=K).packed(sq)
     nbytes = sq.gated_workspace_bytes(M, F, K)
