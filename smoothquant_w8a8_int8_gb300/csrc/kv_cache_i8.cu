@@ -12,6 +12,8 @@
 // Memory-bound like the append to a 16-bit cache: every projected element is read once
 // and written once.  A head's row lies in D / 8 neighbouring threads' registers, its
 // maximum is theirs by shuffles.
+// Measured: 7976 tokens of 32 + 2 x 8 heads of 128 55 us, 348 MB at 94 % of the measured
+// copy rate (codes by division in every place 73 us); 64 tokens 3.3 us, latency.
 #include "kv_tokens.cuh"
 
 #include <algorithm>

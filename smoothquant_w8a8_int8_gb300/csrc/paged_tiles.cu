@@ -42,9 +42,14 @@
 //   warps 8-11       the output: sum over the tiles, partial results, rows;
 //   warps 12-15      copies: keys and values with cp.async into a ring of
 //                    128-row slots in the operands' layout (128-byte swizzle;
-//                    rows of no key are zeros);
+//                    rows of no key are zeros); 8 bits: codes into such slots;
 //   warp 16          tensor memory, and lane 0 issues the products;
-//   warp 17          walks the CTA's share and hands its pieces to the others.
+//   warp 17          walks the CTA's share and hands its pieces to the others;
+//   warps 18, 19     8 bits: codes of a tile by bulk copies, the scales.
+// 8 bits (two parts, as fp16): the key scales stand at the logits, the value scales at the
+// probabilities.  Bound by the softmax warps, 85 % busy, for long items: the prompts above
+// 584 us (2.4 us a tile, tensor pipe 43 %), the drafts 99 us; twice as many softmax warps
+// took as long, and every longer code lost (see the loops).
 // Tensor memory, 512 columns: two areas of 64 columns per part for S and then P,
 // and two areas (bf16: one) of 128 for P V.
 // Every wait is bounded (4 s); on expiry the CTA records an error for
