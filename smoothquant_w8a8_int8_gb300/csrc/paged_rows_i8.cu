@@ -20,8 +20,8 @@
 //
 // Bound: memory and instruction issue together.  64 single tokens of 32 / 8 heads of 128,
 // contexts to 8192: 103 us, 5.2 TB/s (79 % of the measured copy rate) at 46 % of the issue
-// slots; steps of 16 keys 124 us, scales as fp32 products of their own 106.  4 tokens of 64
-// sequences of 4000 keys (16 rows): 167 us, the widening and twice the products.
+// slots; steps of 16 keys 124 us, sums one by one instead of in pairs 106.  4 tokens of 64
+// sequences of 4000 keys (16 rows): 167 us (200), the widening and twice the products.
 //
 // Precision: codes are exact in fp16; fp32 queries and weights p v_scale are sums of two
 // fp16 numbers, each row scaled by a power of two so that its largest is within

@@ -157,16 +157,17 @@ def test_many_tiles(sq):
     c.verify(sq, 2, c.run(sq, 2))
 
 
+@pytest.mark.parametrize("K", [1104, 2064])
 @pytest.mark.parametrize("rows,columns", [
     ([3], [5]), ([0, 257, 1299], [0, 4999]), (range(0, 1300, 256), range(0, 5000, 400)),
     (range(0, 1300, 512), range(0, 5000, 128)), (range(1300), [17, 2500]), ([], [1, 2]),
     ([700], []), ([300, 301, 1200], range(5000))])
-def test_sums_beyond_2_to_the_24(sq, rows, columns):
+def test_sums_beyond_2_to_the_24(sq, rows, columns, K):
     """A launch whose tiles are summed in one pass where their rows' norms allow it and
     in chunks where they do not: codes of 127 against each other leave fp32's whole
-    numbers at K = 2064, so a tile that was summed the wrong way would differ from the
+    numbers at K = 1104, so a tile that was summed the wrong way would differ from the
     launch without norms, whose tiles are all chunks."""
-    M, F, K = 1300, 5000, 2064
+    M, F = 1300, 5000
     c = Case(M, F, K, seed=3, bias=(False, True))
     c.wg, c.wu, c.s = c.wg.clamp(-2 / K ** 0.5, 2 / K ** 0.5), c.wu * 0.1, torch.ones(K)
     c.wu[:, 0] = 3.0  # (a row's largest: the others' codes stay small)
