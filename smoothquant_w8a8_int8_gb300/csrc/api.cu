@@ -623,7 +623,7 @@ sq_status sq_gated_workspace_bytes(int64_t M, int64_t F, int64_t K, size_t *byte
     if (M < 0 || F < 0 || K <= 0) return SQ_ERR_INVALID_ARG;
     if (F > kMaxGated || K > kMaxK) return SQ_ERR_UNSUPPORTED;
     if (M == 0 || F == 0) return SQ_OK;
-    return gemm_tc_workspace_bytes(M, gated_rows(F), K, bytes);
+    return gemm_tc_workspace_bytes(M, gated_rows(F), K, bytes, true);
 }
 
 sq_status sq_linear_i8_gated(const void *Xop, const float *x_scale, const int32_t *x_row_l1,
@@ -643,7 +643,7 @@ sq_status sq_linear_i8_gated(const void *Xop, const float *x_scale, const int32_
         return SQ_ERR_ALIGNMENT;
     if ((rc = require_sm103()) != SQ_OK) return rc;
     constexpr float kLog2e = 1.4426950408889634f;
-    GatedOut g = {bias_gate, bias_up, (int)F, act, 1, 0, -kLog2e, 0.0f};
+    GatedOut g = {bias_gate, bias_up, (int)F, act, 1, 0, 0, -kLog2e, 0.0f};
     if (act == SQ_GATE_GELU_TANH) {
         const double two_root = 1.5957691216057308;  // 2 sqrt(2 / pi)
         g.c1 = (float)(-two_root * 1.4426950408889634);

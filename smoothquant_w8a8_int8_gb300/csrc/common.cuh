@@ -191,7 +191,9 @@ sq_status launch_gemm_tc(const __nv_bfloat16 *Xop, const float *sx, const int32_
                          const float *rm_pairs = nullptr, float *row_amax = nullptr,
                          const GatedOut *gated = nullptr);
 // Bytes of the split-K workspace of an M x N x K launch on the current device (0: none used).
-sq_status gemm_tc_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes);
+// gated: of a gated block's linear (N: the packed operand's rows).
+sq_status gemm_tc_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes,
+                                  bool gated = false);
 // Read and clear the device error words of the tcgen05 GEMM and of the
 // activation quantiser (synchronous).
 sq_status gemm_tc_take_error(cudaStream_t st);

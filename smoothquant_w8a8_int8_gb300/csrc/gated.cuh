@@ -21,6 +21,7 @@ struct GatedOut {
     int F;
     int act;       // sq_gate
     int group;     // row blocks that share a pass over the weights (grouped_item_at)
+    int tile_n;    // columns of a whole tile (plan_gated)
     int a_rows;    // rows of a copy of the activations (gemm_tc_kernel)
     float c1, c3;  // the logistic function's argument, times -log2 e (see sigmoid_gate2)
 };

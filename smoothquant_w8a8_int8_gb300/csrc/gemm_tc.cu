@@ -1134,6 +1134,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                              ? exact_pass_kb_gated(args, nkb, warp, lane, S.l1max, nullptr)
                              : exact_pass_kb(args, nkb, warp, lane, S.l1max);
     const int nchunks = (nkb + chunk_kb - 1) / chunk_kb;
+    const int tile_n = OUT == kOutGated ? args.gt.tile_n : BN;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -1144,7 +1145,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             Cursor cu;
             cursor_init(sched, cu, blockIdx.x);
             Work t;
-            while (next_work(sched, cu, t, gridDim.x)) {
+            while (next_work(sched, cu, t, gridDim.x, tile_n)) {
                 const bool slice = t.bn < BN;
                 for (int kb = t.kb0; kb < t.kb1; ++kb) {
                     if (!mbar_wait(smem_u32(&S.empty[stage]), phase ^ 1, abort_flag)) goto done_p;
@@ -1176,7 +1177,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             Cursor cu;
             cursor_init(sched, cu, blockIdx.x);
             Work t;
-            for (int it = 0; next_work(sched, cu, t, gridDim.x); ++it) {
+            for (int it = 0; next_work(sched, cu, t, gridDim.x, tile_n); ++it) {
                 const uint32_t idesc = idesc_for(t.bn);
                 // exact fp32 passes: the unit's K blocks cut at multiples of chunk_kb
                 for (int c = t.kb0 / chunk_kb; c * chunk_kb < t.kb1; ++c) {
@@ -1229,7 +1230,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         Cursor cu;
         cursor_init(sched, cu, blockIdx.x);
         Work t;
-        for (int it = 0; next_work(sched, cu, t, gridDim.x); ++it) {
+        for (int it = 0; next_work(sched, cu, t, gridDim.x, tile_n); ++it) {
             const int row0 = t.m0 + q * 32;
             const int64_t m = (int64_t)row0 + lane;
             const int nb = t.n0 + half * COLS_PER_WARP;
@@ -1798,15 +1799,16 @@ static bool shape_ok(int64_t M, int64_t N, int64_t K) {
     return ((M + BM - 1) / BM) * ((N + BN - 1) / BN) <= 0x7fffffff;
 }
 
-sq_status gemm_tc_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes) {
+sq_status gemm_tc_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes, bool gated) {
     *bytes = 0;
     if (M == 0 || N == 0) return SQ_OK;
     if (!shape_ok(M, N, K)) return SQ_ERR_UNSUPPORTED;
     DeviceInfo di;
     sq_status rc = device_info(&di);
     if (rc != SQ_OK) return rc;
-    int grid;
-    *bytes = (size_t)sk_workspace_bytes(plan_launch(M, N, K, di.sms, true, &grid));
+    int grid, tile_n;
+    *bytes = (size_t)sk_workspace_bytes(gated ? plan_gated(M, N, K, di.sms, true, &grid, &tile_n)
+                                              : plan_launch(M, N, K, di.sms, true, &grid));
     return SQ_OK;
 }
 
@@ -1868,7 +1870,10 @@ sq_status launch_gemm_tc(const __nv_bfloat16 *Xop, const float *sx, const int32_
     if ((rc = make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Wop, N, K, BN, BK)) != SQ_OK)
         return rc;
     int grid;
-    const Schedule sched = plan_launch(M, N, K, di.sms, workspace != nullptr, &grid);
+    const bool split = workspace != nullptr;
+    const Schedule sched = gated
+                               ? plan_gated(M, N, K, di.sms, split, &grid, &args.gt.tile_n)
+                               : plan_launch(M, N, K, di.sms, split, &grid);
     args.sched = sched;
     args.ws_cnt = nullptr;
     args.ws_slots = nullptr;
@@ -1880,10 +1885,11 @@ sq_status launch_gemm_tc(const __nv_bfloat16 *Xop, const float *sx, const int32_
                                                  sk_counter_bytes(sched));
     }
     // B box of the column slices of the last wave's tiles (see make_schedule)
+    // or of a gated launch's narrower tiles
+    const int sub_n = gated && args.gt.tile_n < BN ? args.gt.tile_n : BN / sched.sub;
     tbs = tb;
-    if (sched.sub > 1 &&
-        (rc = make_map(&tbs, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Wop, N, K, BN / sched.sub, BK)) !=
-            SQ_OK)
+    if (sub_n < BN && (rc = make_map(&tbs, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Wop, N, K, sub_n,
+                                     BK)) != SQ_OK)
         return rc;
     ty = ta;  // unused placeholder unless Y is stored through TMA
     if (args.tma_io && !rq) {

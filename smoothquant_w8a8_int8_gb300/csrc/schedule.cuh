@@ -112,9 +112,10 @@ __host__ __device__ __forceinline__ void cursor_init(const Schedule &sc, Cursor 
     }
 }
 
-// The next unit of a CTA of a `grid`-CTA launch (in a kernel: gridDim.x).
+// The next unit of a CTA of a `grid`-CTA launch (in a kernel: gridDim.x).  tile_n: a whole
+// tile's columns (plan_gated; other than BN only where there is nothing else).
 __host__ __device__ __forceinline__ bool next_work(const Schedule &sc, Cursor &cu, Work &w,
-                                                   int grid) {
+                                                   int grid, int tile_n = BN) {
     if (cu.i < sc.items) {
         const int i = cu.i;
         cu.i += grid;
@@ -123,8 +124,8 @@ __host__ __device__ __forceinline__ bool next_work(const Schedule &sc, Cursor &c
         w.skt = -1;
         if (i < sc.full_items) {
             w.m0 = (i % sc.m_tiles) * BM;
-            w.n0 = (i / sc.m_tiles) * BN;
-            w.bn = BN;
+            w.n0 = (i / sc.m_tiles) * tile_n;
+            w.bn = tile_n;
         } else {
             const int j = i - sc.full_items;
             const int t = sc.full_items + j / sc.sub;
@@ -252,6 +253,34 @@ inline Schedule plan_launch(int64_t M, int64_t N, int64_t K, int sms, bool split
     }
     *grid = tiles < sms ? tiles : sms;
     return make_schedule(m_tiles, n_tiles, nkb, *grid, false);
+}
+
+// The same for a gated block's linear of few rows, which waits for the weights: more SMs
+// fetch them faster, so tiles become as narrow as gives each SM one still (128 or 192
+// columns), and K is split only where that leaves an SM less to fetch, by more than what
+// the joins cost (in columns x K blocks; 430 take a microsecond).  Measured (16 rows, K x F;
+// narrow tiles and split, us): 2048 x 6400 17.1 and 25.0, 4096 x 8192 30.6 and 35.7, 4096 x
+// 3200 25.8 and 26.1, 4096 x 1600 24.9 and 22.9, 12288 x 4864 81 and 54; unsplit with 256
+// columns and with narrower tiles: 1600 x 6000 16.0 and 14.4, 4096 x 12288 39.7 and 39.0.
+constexpr int kJoinCost = 4096;
+inline Schedule plan_gated(int64_t M, int64_t N, int64_t K, int sms, bool split_k, int *grid,
+                           int *tile_n) {
+    Schedule sc = plan_launch(M, N, K, sms, split_k, grid);
+    *tile_n = BN;
+    if (M >= 2 * BM) return sc;
+    for (int bn : {128, 192}) {
+        const int64_t tiles = sc.m_tiles * ((N + bn - 1) / bn);
+        if (tiles > sms) continue;
+        if (sc.sk_tiles > 0) {
+            if (sc.nkb * BN / (sc.sk_ctas / sc.sk_tiles) + kJoinCost < sc.nkb * bn) break;
+            sc = plan_launch(M, N, K, sms, false, grid);
+        }
+        *tile_n = bn;
+        *grid = sc.full_items = sc.items = sc.dp_tiles = (int)tiles;
+        sc.sub = 1;
+        break;
+    }
+    return sc;
 }
 
 }  // namespace sched

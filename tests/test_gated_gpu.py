@@ -114,7 +114,8 @@ def test_packing_rows_of_zeros(sq):
 
 SHAPES = [(1, 1, 16), (1, 96, 64), (2, 33, 1040), (16, 1000, 512), (127, 31, 80), (128, 32, 2080),
           (129, 257, 48), (255, 130, 4112), (256, 128, 64), (257, 515, 1040), (300, 64, 2080),
-          (700, 1028, 144), (1030, 40, 32), (7, 300, 2080), (15, 64, 144), (65, 96, 64)]
+          (700, 1028, 144), (1030, 40, 32), (7, 300, 2080), (15, 64, 144), (65, 96, 64),
+          (20, 12288, 80), (130, 6000, 1056), (3, 14500, 1200)]
 
 
 @pytest.mark.parametrize("act", [0, 1, 2])
@@ -135,8 +136,8 @@ def test_range(sq, size, act):
     c.verify(sq, act, c.run(sq, act))
 
 
-@pytest.mark.parametrize("M,F,K", [(1, 64, 2048), (16, 500, 4096), (128, 1000, 2560),
-                                   (130, 33, 8192), (300, 128, 3584), (1, 4000, 4096)])
+@pytest.mark.parametrize("M,F,K", [(1, 64, 8192), (16, 500, 12288), (128, 1000, 8208),
+                                   (130, 33, 8192), (300, 128, 3584), (1, 4000, 12304)])
 def test_split_k_is_the_same_bits(sq, M, F, K):
     c = Case(M, F, K, seed=K).packed(sq)
     nbytes = sq.gated_workspace_bytes(M, F, K)
@@ -207,10 +208,10 @@ def test_empty(sq):
 
 
 def test_streams_and_graph(sq):
-    cs = [Case(16, 600, 4096, seed=i).packed(sq) for i in range(2)]
+    cs = [Case(16, 600, 12288, seed=i).packed(sq) for i in range(2)]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in cs]
-    ws = [sq.empty_workspace(sq.gated_workspace_bytes(16, 600, 4096)) for _ in cs]
+    ws = [sq.empty_workspace(sq.gated_workspace_bytes(16, 600, 12288)) for _ in cs]
     torch.cuda.synchronize()
     got = []
     for _ in range(5):
@@ -229,6 +230,6 @@ def test_streams_and_graph(sq):
         out.zero_()
         g.replay()
         torch.cuda.synchronize()
-        d = Case(16, 600, 4096, seed=0, bias=(False, False))
+        d = Case(16, 600, 12288, seed=0, bias=(False, False))
         d.sx, d.w, d.sw = c.sx * size, c.w, c.sw
         d.verify(sq, 0, out)
