@@ -663,28 +663,32 @@ def linear_i8_gated(Xop: torch.Tensor, x_scale: torch.Tensor, Wop: torch.Tensor,
     product in one GEMM: act(gate) * up, fp32 [M, F].  Wop and w_scale come from
     pack_gated_weight; workspace: empty_workspace(gated_workspace_bytes(M, F, K)), None
     for no split over K (the same bits either way)."""
-    _need(Xop, torch.bfloat16, "Xop")
-    if Xop.dim() != 2:
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    dev, shape = Xop.device, Xop.shape
+    if Xop.dtype is not bf16 or not Xop.is_cuda or not Xop.is_contiguous():
+        _need(Xop, bf16, "Xop")
+    if len(shape) != 2:
         raise ValueError("Xop must have shape (M, K)")
-    M, K = Xop.shape
-    rows = gated_rows(F)
-    dev, f32, i32 = Xop.device, torch.float32, torch.int32
-
-    def at(t, dtype, name, shape):
-        return None if t is None else _arg(t, dtype, name, shape, dev)
-
+    M, K = shape
+    rows = 64 * ((F + 31) // 32) if 0 <= F <= 1 << 24 else 0  # as gated_rows
     with _on(Xop, stream) as st:
         if out is None:
             out = torch.empty(M, F, dtype=f32, device=dev)
+            y = out.data_ptr()
+        else:
+            y = _arg(out, f32, "out", (M, F), dev)
+        ws, ws_bytes = None, 0
+        if workspace is not None:
+            ws = _arg(workspace, torch.uint8, "workspace", workspace.shape, dev)
+            ws_bytes = workspace.numel()
         _check((_lib or load()).sq_linear_i8_gated(
             Xop.data_ptr(), _arg(x_scale, f32, "x_scale", (M,), dev),
-            at(x_l1, i32, "x_l1", (M,)), _arg(Wop, torch.bfloat16, "Wop", (rows, K), dev),
-            _arg(w_scale, f32, "w_scale", (rows,), dev), at(w_l1, i32, "w_l1", (rows,)),
-            at(bias_gate, f32, "bias_gate", (F,)), at(bias_up, f32, "bias_up", (F,)), M, F, K,
-            int(act), _arg(out, f32, "out", (M, F), dev),
-            None if workspace is None else _arg(workspace, torch.uint8, "workspace",
-                                                workspace.shape, dev),
-            0 if workspace is None else workspace.numel(), st), "sq_linear_i8_gated")
+            None if x_l1 is None else _arg(x_l1, i32, "x_l1", (M,), dev),
+            _arg(Wop, bf16, "Wop", (rows, K), dev), _arg(w_scale, f32, "w_scale", (rows,), dev),
+            None if w_l1 is None else _arg(w_l1, i32, "w_l1", (rows,), dev),
+            None if bias_gate is None else _arg(bias_gate, f32, "bias_gate", (F,), dev),
+            None if bias_up is None else _arg(bias_up, f32, "bias_up", (F,), dev), M, F, K,
+            int(act), y, ws, ws_bytes, st), "sq_linear_i8_gated")
     return out
 
 

@@ -56,12 +56,16 @@ class Case:
                                                         self.s.cuda(), want_l1=True)
         return self
 
-    def run(self, sq, act, l1=True, **kw):
-        b = [None if t is None else t.cuda() for t in self.bias]
-        x_l1 = self.x.abs().sum(1).int().cuda() if l1 else None
-        return sq.linear_i8_gated(self.x.bfloat16().cuda(), self.sx.cuda(), self.w, self.sw,
-                                  self.F, act, b[0], b[1], x_l1=x_l1,
-                                  w_l1=self.l1 if l1 else None, **kw)
+    def inputs(self):
+        return [self.x.bfloat16().cuda(), self.sx.cuda(), self.x.abs().sum(1).int().cuda(),
+                *(None if t is None else t.cuda() for t in self.bias)]
+
+    def run(self, sq, act, l1=True, inputs=None, **kw):
+        """inputs: kept by the caller where the call is on another stream, which may still
+        read them when this returns."""
+        x, sx, x_l1, gate, up = inputs or self.inputs()
+        return sq.linear_i8_gated(x, sx, self.w, self.sw, self.F, act, gate, up,
+                                  x_l1=x_l1 if l1 else None, w_l1=self.l1 if l1 else None, **kw)
 
     def exact(self, act):
         """(Y, bound) from the packed operand as it is on the GPU."""
@@ -212,10 +216,12 @@ def test_streams_and_graph(sq):
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in cs]
     ws = [sq.empty_workspace(sq.gated_workspace_bytes(16, 600, 12288)) for _ in cs]
+    kept = [c.inputs() for c in cs]
     torch.cuda.synchronize()
     got = []
     for _ in range(5):
-        got = [c.run(sq, 0, workspace=w, stream=st) for c, w, st in zip(cs, ws, streams)]
+        got = [c.run(sq, 0, inputs=x, workspace=w, stream=st)
+               for c, x, w, st in zip(cs, kept, ws, streams)]
     torch.cuda.synchronize()
     for c, y in zip(cs, got):
         c.verify(sq, 0, y)
