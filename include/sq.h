@@ -328,13 +328,16 @@ sq_status sq_kv_append_i8(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv, 
  * Everything said there holds, with these differences.  Codes enter the tensor cores as
  * they are (as fp16 numbers, exactly), fp32 queries and the products of probabilities
  * and value scales as two fp16 numbers each, a row's largest scaled near the top of
- * fp16's range: within 2^-22, or 2^-30 of the row's largest (or 2^-130), and so O agrees
- * with the exact attention over the rows as sq_paged_attention's does for an fp16 cache,
- * whatever the scales' range within a row's keys is (weights below 2^-100 of the largest
- * may count as 0).  Key scales are 2^96 at most, larger ones may leave the rows that see
- * them not finite.  Keys and values that a row does not see do not reach it, whatever their
- * codes and scales are; a key or value row that it sees whose scale is not finite leaves
- * the whole row not finite (a key's infinite scale may count as no weight).
+ * fp16's range: queries within 2^-22, or 2^-30 of the row's largest (or 2^-130); the
+ * products within 2^-22, or 2^-30 of the largest scale of its sequence's value rows that
+ * are not all zeros (or 2^-130).  So O agrees with the exact attention over the rows as
+ * sq_paged_attention's does for an fp16 cache, whatever the scales' range within a row's
+ * keys is (weights below 2^-100 of the largest may count as 0); a row of zeros adds
+ * nothing, and its scale takes nothing from the others, unless it is not finite.  Key
+ * scales are 2^96 at most, larger ones may leave the rows that see them not finite.  Keys
+ * and values that a row does not see do not reach it, whatever their codes and scales
+ * are; a key or value row that it sees whose scale is not finite leaves the whole row not
+ * finite (a key's infinite scale may count as no weight).
  * workspace: as for sq_paged_attention, of sq_paged_attention_workspace_bytes. */
 sq_status sq_paged_attention_i8(const float *Q, int64_t ldq, int64_t T, int64_t Hq, int64_t Hkv,
                                 int64_t D, const int8_t *k_cache, const int8_t *v_cache,

@@ -19,15 +19,15 @@
 // 1024 + code + 128, from which 1152 is taken away, two codes at a time.
 //
 // Bound: memory and instruction issue together.  64 single tokens of 32 / 8 heads of 128,
-// contexts to 8192: 103 us, 5.2 TB/s (79 % of the measured copy rate) at 46 % of the issue
+// contexts to 8192: 104 us, 5.2 TB/s (78 % of the measured copy rate) at 46 % of the issue
 // slots; steps of 16 keys 124 us, sums one by one instead of in pairs 106.  4 tokens of 64
-// sequences of 4000 keys (16 rows): 167 us (200), the widening and twice the products.
+// sequences of 4000 keys (16 rows): 176 us (200), the widening and twice the products.
 //
 // Precision: codes are exact in fp16; fp32 queries and weights p v_scale are sums of two
 // fp16 numbers, each row scaled by a power of two so that its largest is within
 // [2^7, 2^15) (queries) and [2^14, 2^15) (a step's weights), and what is 2^-37 of the
-// row's largest weight still counts.  Logits are multiplied by a power of two as in
-// paged_rows.cu.
+// row's largest weight still counts (see drop_zero_rows).  Logits are multiplied by a power
+// of two as in paged_rows.cu.
 #include "paged_rows.cuh"
 
 #include <algorithm>
@@ -61,6 +61,36 @@ __device__ __forceinline__ int place(int r, int ch) {
     return line * 128 + ((((r & 1) << 2 | ch) ^ ((line & 3) << 1)) << 4);
 }
 
+__device__ __forceinline__ float lds_f1(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+// A value row of zeros adds nothing whatever its scale is (the append stores 1), but its
+// weight could be the largest of a step, next to which the others' lose their parts.  So
+// rows with scales above `known` are looked at: the scale of one of zeros becomes 0 (unless
+// it is not finite: its products are NaN), and 2^8 times the largest of the others that
+// are `seen` is known from then on.  Lane l: key l of the step.
+template <int D>
+__device__ __noinline__ float drop_zero_rows(uint32_t values, uint32_t scales, bool seen,
+                                             float known) {
+    static_assert(kKT == 32, "a key per lane");
+    const int lane = threadIdx.x & 31;
+    const float x = fabsf(lds_f1(scales + 4 * lane));
+    const bool look = x > known && x < INFINITY;
+    bool zeros = look;
+#pragma unroll 1
+    for (int ch = 0; ch < D / 16 && __any_sync(0xffffffffu, zeros); ++ch) {
+        uint32_t w[4];
+        lds4(w, values + place<D>(lane, ch));
+        zeros = zeros && (w[0] | w[1] | w[2] | w[3]) == 0;
+    }
+    if (zeros)
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(scales + 4 * lane), "f"(0.0f) : "memory");
+    __syncwarp();
+    const float y = look && !zeros && seen ? 0x1p8f * x : 0.0f;
+    return fmaxf(known, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(y))));
+}
 __device__ __forceinline__ float2 lds_f2(uint32_t addr) {
     float2 v;
     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
@@ -262,11 +292,22 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             }
         }
         int key0 = p.key0;
+        float known = 0.0f;  // see drop_zero_rows
         for (int it = 0; it < p.ntiles; ++it, key0 += kKT) {
             asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
             __syncwarp();
             const uint32_t ks = ring + cur * C::kStepBytes;
             const uint32_t vs = ks + C::kCodes, sc = ks + 2 * C::kCodes;
+            // (us with it here, behind the mask, and without: decode above 104, 104 and 103,
+            // heads of 64 132, 129 and 126, 16 rows 176, 179 and 167)
+            auto check_scales = [&]() {
+                if (__any_sync(0xffffffffu, fabsf(lds_f1(sc + (kKT + lane) * 4)) > known)) {
+                    const KeyRange kr = key_range(a, key0, p.keys);
+                    const int k = kr.key + lane;
+                    known = drop_zero_rows<D>(vs, sc + kKT * 4, kr.lo <= k && k < kr.hi, known);
+                }
+            };
+            if (R > 1) check_scales();
             // logits of the rows x 32 keys
             float s[4][4];
 #pragma unroll
@@ -292,9 +333,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
                 const float2 k2 = lds_f2(sc + (8 * h + 2 * t) * 4);
-                const float2 v2 = lds_f2(sc + (kKT + 8 * h + 2 * t) * 4);
-                vf[2 * h] = v2.x;
-                vf[2 * h + 1] = v2.y;
                 if (R == 1) {
                     x[0][2 * h] = (s[h][0] + s[h][2]) * k2.x;
                     x[0][2 * h + 1] = (s[h][1] + s[h][3]) * k2.y;
@@ -322,6 +360,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                         if ((missing >> (i >> 2) & 1) || k >= (r ? hi1 : kr.hi) || k < kr.lo)
                             x[r][i] = -INFINITY;
                     }
+            }
+            if (R == 1) check_scales();
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const float2 v2 = lds_f2(sc + (kKT + 8 * h + 2 * t) * 4);
+                vf[2 * h] = v2.x;
+                vf[2 * h + 1] = v2.y;
             }
             float grow[R];
             bool any = false;

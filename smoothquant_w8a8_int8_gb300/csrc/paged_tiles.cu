@@ -356,6 +356,26 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
 __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+// Four value rows of an int8 cache, at `row`, and their scales: 0 in the place of the finite
+// one of a row that is nothing but zeros.
+template <int D>
+__device__ __forceinline__ void drop_zero_rows(const int8_t *row, float *(&scale)[4]) {
+    bool zeros[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) zeros[i] = *scale[i] != 0.0f && fabsf(*scale[i]) < INFINITY;
+#pragma unroll 1
+    for (int ch = 0; ch < D / 16 && (zeros[0] || zeros[1] || zeros[2] || zeros[3]); ++ch) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!zeros[i]) continue;
+            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(row + i * D) + ch);
+            zeros[i] = (w.x | w.y | w.z | w.w) == 0;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (zeros[i]) *scale[i] = 0.0f;
+}
 template <int D, int CT>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tiles_kernel(const __grid_constant__ PagedArgs a,
@@ -617,19 +637,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 vs = __ldg(reinterpret_cast<const float4 *>(a.v_scale + from));
                             }
                             float *vv[4] = {&vs.x, &vs.y, &vs.z, &vs.w};
-                            unsigned top = 0, low = 0;
+                            unsigned top, low;
+                            auto far_apart = [&]() {
+                                top = low = 0;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
+                                for (int i = 0; i < 4; ++i) {
+                                    // zeros say nothing; one that is not finite is further from
+                                    // the others than any
+                                    const unsigned x = __float_as_uint(*vv[i]) >> 23 & 255u;
+                                    top = max(top, x == 255u ? 0u : x);
+                                    low = max(low, *vv[i] == 0.0f ? 0u : x == 255u ? 511u : 255u - x);
+                                }
+                                top = __reduce_max_sync(0xffffffffu, top);
+                                low = __reduce_max_sync(0xffffffffu, low);
+                                return (int)top - (255 - (int)low) > 8;
+                            };
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
                                 if (k0 + i < r.lo || k0 + i >= r.hi) *vv[i] = 0.f;
-                                // zeros say nothing; one that is not finite is further from the
-                                // others than any
-                                const unsigned x = __float_as_uint(*vv[i]) >> 23 & 255u;
-                                top = max(top, x == 255u ? 0u : x);
-                                low = max(low, *vv[i] == 0.0f ? 0u : x == 255u ? 511u : 255u - x);
+                            bool wild = far_apart();
+                            if (wild) {
+                                // A row of zeros adds nothing whatever its scale is (one that is
+                                // not finite stays: the product with it is NaN), and the others'
+                                // weights are not to be held next to its.  (Among scales that are
+                                // near each other it costs them 2^8 at most, 2^-31 of a scale.)
+                                drop_zero_rows<D>(v_cache + from * D, vv);
+                                wild = far_apart();
                             }
-                            top = __reduce_max_sync(0xffffffffu, top);
-                            low = __reduce_max_sync(0xffffffffu, low);
-                            const bool wild = (int)top - (255 - (int)low) > 8;
                             const int exp = wild ? 0 : min(max((int)top - 127, -126), 126);
                             const float f = pow2(-exp);
                             if (tile >= kScaleTiles &&
