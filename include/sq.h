@@ -334,10 +334,11 @@ sq_status sq_kv_append_i8(const float *QKV, int64_t T, int64_t Hq, int64_t Hkv, 
  * sq_paged_attention's does for an fp16 cache, whatever the scales' range within a row's
  * keys is (weights below 2^-100 of the largest may count as 0); a row of zeros adds
  * nothing, and its scale takes nothing from the others, unless it is not finite.  Key
- * scales are 2^96 at most, larger ones may leave the rows that see them not finite.  Keys
- * and values that a row does not see do not reach it, whatever their codes and scales
- * are; a key or value row that it sees whose scale is not finite leaves the whole row not
- * finite (a key's infinite scale may count as no weight).
+ * scales are 2^96 at most, larger ones may leave the rows that see them not finite; so may
+ * value rows whose magnitudes, times their weights next to the largest, do not add up
+ * within fp32's range.  Keys and values that a row does not see do not reach it, whatever
+ * their codes and scales are; a key or value row that it sees whose scale is not finite
+ * leaves the whole row not finite (a key's infinite scale may count as no weight).
  * workspace: as for sq_paged_attention, of sq_paged_attention_workspace_bytes. */
 sq_status sq_paged_attention_i8(const float *Q, int64_t ldq, int64_t T, int64_t Hq, int64_t Hkv,
                                 int64_t D, const int8_t *k_cache, const int8_t *v_cache,

@@ -154,10 +154,12 @@ constexpr int kJoin = 6;
 // (300 keys, 1 item), 35, 31, 36 and 42 (1024 keys, 19 items), 71, 57, 58 and 62
 // (30,000 keys, 1 item)
 constexpr int kMinTiles = 4;
-// log2 of the probabilities' factor.  (8 bits: a row's largest weight, its probability
+constexpr float kBias = 12.0f;  // log2 of the probabilities' factor, 16 bits
+// 8 bits: log2 of the value scales' factor.  (A row's largest weight, a probability of 1
 // times a value scale in [2^-8, 2), stays below 2^15 and is 2^6 at least, so that what is
-// below fp16's range, 2^-24 in both parts, is 2^-30 of it)
-constexpr float kBias16 = 12.0f, kBiasI8 = 14.0f;
+// below fp16's range, 2^-24 in both parts, is 2^-30 of it.  A factor of the
+// probabilities would stay in the sums, and O leave fp32's range 2^14 earlier.)
+constexpr int kTopI8 = 14;
 
 constexpr int kI8 = kCacheI8;
 
@@ -166,7 +168,7 @@ constexpr int kI8 = kCacheI8;
 struct TileCodes {
     alignas(16) float k[kScaleTiles][kKT];  // (read 16 bytes at a time)
     alignas(16) float v[kScaleTiles][kKT];  // divided by 2^exp
-    int exp[kScaleTiles];        // the largest value scale's exponent (wild: 0)
+    int exp[kScaleTiles];        // the largest value scale's exponent less kTopI8 (wild: 0)
     int wild[kScaleTiles];       // the smallest is under 2^-8 of it, or one is not finite
     uint64_t scale_full[kScaleTiles], scale_empty[kScaleTiles];
     uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
@@ -179,7 +181,6 @@ template <int D, int CT>
 struct TilesCfg {
     static constexpr bool BF = CT == SQ_CACHE_BF16;
     static constexpr int kParts = BF ? 3 : 2;
-    static constexpr float kBias = CT == kI8 ? kBiasI8 : kBias16;
     static constexpr int kSlab = kKT * 128;            // 128 rows x 64 elements
     static constexpr int kSlot = kSlab * (D / 64);     // keys or values of a tile
     static constexpr int kSlots = CT == kI8 ? (D == 64 ? 5 : 3) : D == 64 ? 6 : BF ? 3 : 4;
@@ -664,7 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 drop_zero_rows<D>(v_cache + from * D, vv);
                                 wild = far_apart();
                             }
-                            const int exp = wild ? 0 : min(max((int)top - 127, -126), 126);
+                            // (2^-exp and, for the output, 2^exp are normal numbers)
+                            const int exp = wild ? 0 : min(max((int)top - 127 - kTopI8, -126), 126);
                             const float f = pow2(-exp);
                             if (tile >= kScaleTiles &&
                                 !warp_wait(&X.scale_empty[at], (tile / kScaleTiles - 1) & 1u, abort,
@@ -1106,16 +1108,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     mx = fmaxf(mx, B.half_max[t & 1][1 - g][r]);
-                    // (see below)
-                    const float m = mx == -INFINITY ? 0.0f : __fmaf_ru(mx, c, -C::kBias);
+                    // (exact: the largest probability is 1)
+                    const float m = mx == -INFINITY ? 0.0f : mx * c;
                     const unsigned long long c2 = pk(c, c), m2 = pk(-m, -m);
                     unsigned long long sum2 = 0;
-                    // of a wild tile's row: its largest weight is near the probabilities' factor
+                    // of a wild tile's row: its largest weight is near the value scales' factor
                     int shift = 0;
                     if (__builtin_expect(wild, 0)) {
                         const float top =
                             fmaxf(X.half_top[t & 1][0][r], X.half_top[t & 1][1][r]);
-                        shift = (int)fminf(fmaxf(C::kBias - ceilf(top - m), -126.0f), 126.0f);
+                        shift = (int)fminf(fmaxf(kTopI8 - ceilf(top - m), -126.0f), 126.0f);
                     }
                     // 16 logits to their weights; `to_weights` multiplies the values' scales in
                     auto weigh = [&](int q, auto to_weights) {
@@ -1218,7 +1220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mx = fmaxf(mx, B.half_max[t & 1][1 - g][r]);
                     // (rounded up: mx c is exact, so the largest exponent is 12 at most, and
                     // at least 0 where 12 is less than the maximum's last place)
-                    const float m = mx == -INFINITY ? 0.0f : __fmaf_ru(mx, c, -C::kBias);
+                    const float m = mx == -INFINITY ? 0.0f : __fmaf_ru(mx, c, -kBias);
                     const unsigned long long c2 = pk(c, c), m2 = pk(-m, -m);
                     unsigned long long sum2 = 0;
                     // per 16 keys 8 columns of each part

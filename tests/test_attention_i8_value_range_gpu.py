@@ -1,5 +1,6 @@
 """sq_paged_attention_i8 where value rows hold nothing but zeros, as the append stores
-them: codes of 0 with scale 1, however small the other rows' scales are."""
+them: codes of 0 with scale 1, however small the other rows' scales are; and values near
+the ends of fp32's range."""
 import pytest
 import torch
 
@@ -134,3 +135,25 @@ def test_rows_of_zeros_whose_scale_is_not_finite(sq, q, kv, places, D, value):  
         e, r = t.row(b, p)
         t.v[e, :, r] = 0
     poisoned(sq, t, places, "vs", value)
+
+
+@pytest.mark.parametrize("q", [FEW, MANY, [300, 7]])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("size", [2.0 ** 80, 2.0 ** 100, 2.0 ** 115, 2.0 ** -100])
+def test_large_and_small_value_scales(sq, size, D, q):  # noqa: F811
+    """Values whose sum over a row's keys is still an fp32 number: 333 of them, each below
+    2^3 `size`; and values so small that what a weight may lose, 2^-130, counts."""
+    t = BatchI8(q, [300, 333], 8, 2, D, 32, seed=21)
+    t.vs = t.vs * size
+    verify_rows(sq, t, slack=127 * 333 * 2.0 ** -130 if size < 1 else 0.0)
+
+
+@pytest.mark.parametrize("q", [FEW, MANY])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("far", [2.0 ** 110, 2.0 ** 60])
+def test_one_large_value_row_at_full_weight(sq, far, D, q):  # noqa: F811
+    """One key's values far above the others', its weight as theirs."""
+    t = BatchI8(q, [140, 333], 8, 2, D, 16, seed=7)
+    e, r = t.row(1, 200)
+    t.vs[e, :, r] = far
+    verify_rows(sq, t)
