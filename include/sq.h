@@ -393,7 +393,8 @@ int64_t sq_gated_rows(int64_t F);
 /* Packs the two weights (offline), row by row as sq_pack_weight: W_gate and W_up
  * fp32 [F][K], s fp32 [K] their common input's smoothing factor.  R =
  * sq_gated_rows(F): Wop GEMM operand of sq_operand_bytes(R, K) bytes, w_scale fp32
- * [R] (4-byte aligned), w_row_l1 int32 [R] (nullable).  F <= 2^24. */
+ * [R] (4-byte aligned), w_row_l1 int32 [R] (nullable; a norm of 2^31 and more is 2^31 -
+ * 1).  F <= 2^24. */
 sq_status sq_pack_gated_weight(const float *W_gate, const float *W_up, const float *s, int64_t F,
                                int64_t K, float *w_scale, void *Wop, int32_t *w_row_l1,
                                void *stream);

@@ -17,7 +17,7 @@ __global__ void __launch_bounds__(kThreads) pack_gated_kernel(
     int64_t F, int64_t K, float *__restrict__ w_scale, __nv_bfloat16 *__restrict__ Wop,
     int32_t *__restrict__ l1) {
     __shared__ float warp_max[kThreads / 32];
-    __shared__ int warp_l1[kThreads / 32];
+    __shared__ long long warp_l1[kThreads / 32];
     pdl_launch_dependents();
     pdl_wait();
     const int64_t p = blockIdx.x;
@@ -43,15 +43,17 @@ __global__ void __launch_bounds__(kThreads) pack_gated_kernel(
         Wop[p * K + j] = __float2bfloat16_rn(c);
         sum += abs(__float2int_rn(c));
     }
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) warp_l1[warp] = sum;
+    // (a thread's part fits 32 bits, K being 2^30 at most; a row's norm may not)
+    long long norm = sum;
+    for (int o = 16; o > 0; o >>= 1) norm += __shfl_xor_sync(0xffffffffu, norm, o);
+    if (lane == 0) warp_l1[warp] = norm;
     __syncthreads();
     if (threadIdx.x == 0) {
         w_scale[p] = scale;
         if (l1) {
-            sum = 0;
-            for (int i = 0; i < kThreads / 32; ++i) sum += warp_l1[i];
-            l1[p] = sum;
+            norm = 0;
+            for (int i = 0; i < kThreads / 32; ++i) norm += warp_l1[i];
+            l1[p] = norm > 0x7fffffffLL ? 0x7fffffff : (int32_t)norm;
         }
     }
 }
