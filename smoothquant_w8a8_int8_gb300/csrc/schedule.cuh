@@ -257,12 +257,21 @@ inline Schedule plan_launch(int64_t M, int64_t N, int64_t K, int sms, bool split
 
 // The same for a gated block's linear of few rows, which waits for the weights: more SMs
 // fetch them faster, so tiles become as narrow as gives each SM one still (128 or 192
-// columns), and K is split only where that leaves an SM less to fetch, by more than what
-// the joins cost (in columns x K blocks; 430 take a microsecond).  Measured (16 rows, K x F;
-// narrow tiles and split, us): 2048 x 6400 17.1 and 25.0, 4096 x 8192 30.6 and 35.7, 4096 x
-// 3200 25.8 and 26.1, 4096 x 1600 24.9 and 22.9, 12288 x 4864 81 and 54; unsplit with 256
-// columns and with narrower tiles: 1600 x 6000 16.0 and 14.4, 4096 x 12288 39.7 and 39.0.
-constexpr int kJoinCost = 4096;
+// columns), or K is split where that takes less time.  What counts is a CTA's K blocks,
+// which take about as long with 128 columns as with 256 and with 1 row as with 128, and the
+// join of P pieces, as long as 36 + 0.12 P of them.  (Fitted to 165 sizes with row norms,
+// on which the other way is 5 % faster at most, and 22 without, 16 %: their blocks take
+// longer, which the sizes do not tell.)
+// Measured (us, K x F; narrow tiles and split): 16 rows, 4096 x 800 25.0 and 22.3, x 1600
+// 24.9 and 23.1, x 2400 25.4 and 24.9, x 3200 25.7 and 26.0 (without norms 29.7 and 26.6),
+// x 4800 26.9 and 29.2, x 8192 30.5 and 35.7, 2048 x 6400 17.0 and 24.6, 8192 x 4096 55.3
+// and 39.7, x 8192 61.2 and 56.5, 12288 x 4864 80.9 and 54.2; 128 rows, 4096 x 1600 25.6
+// and 24.7, x 8192 31.6 and 38.6, 8192 x 8192 62.8 and 60.1; 224 rows, 8192 x 4096 56.5 and
+// 48.8, 12288 x 4864 82.3 and 66.8.  Unsplit with 256 columns and narrower, 16 rows: 1600
+// x 6000 16.0 and 14.3, 4096 x 12288 39.5 and 38.5.
+inline bool split_gated(const Schedule &sc) {  // (in hundredths of a block)
+    return 100 * sc.nkb * (int64_t)sc.sk_tiles / sc.sk_ctas + 3600 + 12 * sc.sk_ctas < 100 * sc.nkb;
+}
 inline Schedule plan_gated(int64_t M, int64_t N, int64_t K, int sms, bool split_k, int *grid,
                            int *tile_n) {
     Schedule sc = plan_launch(M, N, K, sms, split_k, grid);
@@ -272,7 +281,7 @@ inline Schedule plan_gated(int64_t M, int64_t N, int64_t K, int sms, bool split_
         const int64_t tiles = sc.m_tiles * ((N + bn - 1) / bn);
         if (tiles > sms) continue;
         if (sc.sk_tiles > 0) {
-            if (sc.nkb * BN / (sc.sk_ctas / sc.sk_tiles) + kJoinCost < sc.nkb * bn) break;
+            if (split_gated(sc)) break;
             sc = plan_launch(M, N, K, sms, false, grid);
         }
         *tile_n = bn;
