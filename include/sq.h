@@ -405,7 +405,11 @@ sq_status sq_pack_gated_weight(const float *W_gate, const float *W_up, const flo
  * multiple of 4 take bulk stores.  workspace (nullable): splits K over several SMs
  * for small launches, on the rules of sq_linear_i8_ws, sized by
  * sq_gated_workspace_bytes (0: not split); Y is the same bits with and without
- * it.  K <= 133144, F <= 2^24 (SQ_ERR_UNSUPPORTED beyond). */
+ * it.  K <= 133144, F <= 2^24 (SQ_ERR_UNSUPPORTED beyond).
+ * g and u are acc, its product with both scales and the bias' sum, each rounded to
+ * fp32; act(g) is within 2^-24 (5 |z| + 9) of itself for SiLU (z = g) and GELU's tanh
+ * form (z = 2 sqrt(2 / pi) (g + 0.044715 g^3)) or 2^-125 |g|, and within 6.2e-7 |g| for
+ * GELU. */
 sq_status sq_gated_workspace_bytes(int64_t M, int64_t F, int64_t K, size_t *bytes);
 sq_status sq_linear_i8_gated(const void *Xop, const float *x_scale, const int32_t *x_row_l1,
                              const void *Wop, const float *w_scale, const int32_t *w_row_l1,

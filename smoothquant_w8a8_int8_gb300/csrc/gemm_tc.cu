@@ -1035,7 +1035,9 @@ __device__ __forceinline__ int exact_pass_kb(const EpiArgs &args, int nkb, int w
 // both operands have rows beyond the bound, `bad` (of the pair kernel) holds a bit for
 // each block of 256 rows with such a row: a tile is in danger only if its rows and its
 // columns both are.  (Of Gaussian rows of 4096 one in a thousand is beyond the bound;
-// 8192 x 4096 x 12288: 7 and 33 rows, 6 % of the tiles.)
+// 8192 x 4096 x 12288: 7 and 33 rows, 6 % of the tiles.  Of 4352 one in 35 is, so that
+// every block has one and all tiles take chunks from there on: 8192 rows x 12288, 1.86
+// PFLOP/s at 4096, 1.33 at 4352, 1.43 at 8192.)
 constexpr int kBadWords = 32;
 __device__ __forceinline__ int exact_pass_kb_gated(const EpiArgs &args, int nkb, int warp,
                                                    int lane, int32_t (*l1max)[2],

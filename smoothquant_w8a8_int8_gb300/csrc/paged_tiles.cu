@@ -48,8 +48,9 @@
 //   warps 18, 19     8 bits: codes of a tile by bulk copies, the scales.
 // 8 bits (two parts, as fp16): the key scales stand at the logits, the value scales at the
 // probabilities.  Bound by the softmax warps, 85 % busy, for long items: the prompts above
-// 584 us (2.4 us a tile, tensor pipe 43 %), the drafts 99 us; twice as many softmax warps
-// took as long, and every longer code lost (see the loops).
+// 585 us (2.4 us a tile, tensor pipe 43 %), the drafts 99 us; twice as many softmax warps
+// took as long, and every longer code lost (see the loops).  Tiles whose value scales lie
+// far apart (`wild`) take 1.5 times as long: all of the prompts' 892 us, the drafts' 144.
 // Tensor memory, 512 columns: two areas of 64 columns per part for S and then P,
 // and two areas (bf16: one) of 128 for P V.
 // Every wait is bounded (4 s); on expiry the CTA records an error for
@@ -1046,7 +1047,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // their scales applied and masked (702 us): a scale that every lane reads
                     // from shared memory is a cycle of its pipe, which the products and the
                     // widening want too.  A chunk's weights take its place.  A wild tile's
-                    // weights have a loop of their own, out of the other's way (688 -> 628 us).
+                    // weights have a loop of their own, out of the other's way (688 -> 628 us;
+                    // 892 us where every tile takes it).
                     const int sc = t % kScaleTiles;
                     if (!warp_wait(&X.scale_full[sc], (t / kScaleTiles) & 1u, abort, a.error)) {
                         ok = false;
